@@ -385,6 +385,139 @@ mx_status mx_grouped_gemm_q(const uint8_t* a_codes, int64_t a_ld, const uint8_t*
                             void* c, uint8_t* c_codes, int64_t c_codes_ld, uint8_t* c_scales,
                             mx_stream stream);
 
+/* Routing of tokens to experts.  The path above takes the routing as given
+ * (group_offsets, row_index); these entry points make it from the router's
+ * logits, give the router its gradient, and sum the experts' rows back into
+ * tokens.
+ *
+ * mx_route: for each of `tokens` rows of logits l [tokens x experts] (fp32 or
+ * bf16, rows logits_ld elements apart, 0 = experts) the top_k experts and
+ * their weights.
+ *   - Scores: s = softmax(l) over the row (MX_SOFTMAX) or s_e =
+ *     1 / (1 + exp(-l_e)) (MX_SIGMOID), in fp32.
+ *   - Availability: a logit of -inf (a masked expert, a padding token) or a
+ *     bias of -inf makes an expert unavailable.  The type's lowest finite
+ *     value does not: such an expert is chosen after all others.
+ *   - Keys order the choice: s_e + bias_e with a bias (fp32 [experts], or
+ *     NULL; it only steers the choice, not the weights), s_e without.  Where
+ *     neither a bias nor a sum of scores is involved the logits themselves
+ *     are compared, which is the same order without any rounding.  A NaN key
+ *     ranks behind every other available one.
+ *   - Groups: the experts form `groups` groups of experts / groups
+ *     consecutive ones.  A group's score is its best key (group_best = 1) or
+ *     the sum of its two best (2; of one, if only one is available), rounded
+ *     to fp32.  Experts outside the top_groups best groups are not chosen.
+ *     groups = 1: no such limit.
+ *   - ids [tokens x top_k] int32: the chosen experts, best first; of equal
+ *     keys (and equal groups) the lower index wins.  Where fewer than top_k
+ *     are available the rest are -1, with weight 0.
+ *   - weights [tokens x top_k] fp32: scale * s_e, or with renorm != 0
+ *     scale * s_e / (sum of the chosen s).  Scores that underflow keep their
+ *     proportions when renormalised.  A NaN or +inf logit makes a row's
+ *     softmax NaN (renormalised: if it is among the chosen), as the formula
+ *     says; ids stay valid and distinct.
+ * 1 <= experts <= 1024, 1 <= top_k <= 32 and at most the experts of
+ * top_groups groups, groups <= 64 dividing experts, tokens <= 2^24 and
+ * tokens * top_k < 2^31.  Device pointers owned by the caller, aligned to
+ * their elements.
+ * Errors: MX_ERR_DTYPE, MX_ERR_UNSUPPORTED (score), MX_ERR_SHAPE (sizes,
+ * logits_ld, group_best not 1 or 2, a scale that is not finite), MX_ERR_NULL,
+ * MX_ERR_ALIGN, MX_ERR_LAUNCH.  tokens == 0 launches nothing. */
+typedef enum { MX_SOFTMAX = 0, MX_SIGMOID = 1 } mx_score;
+
+mx_status mx_route(const void* logits, mx_dtype lt, int64_t tokens, int32_t experts, int64_t logits_ld,
+                   const float* bias, mx_score score, int32_t groups, int32_t top_groups, int32_t group_best,
+                   int32_t top_k, int renorm, float scale, int32_t* ids, float* weights, mx_stream stream);
+
+/* Gradient of mx_route's weights: dlogits [tokens x experts] (type lt, rows
+ * dlogits_ld apart, 0 = experts; every element is written) from dweights
+ * [tokens x top_k] fp32, for the ids that mx_route chose (distinct in a row;
+ * -1 or any other id out of range carries no gradient).  logits, score,
+ * renorm and scale as in mx_route; the choice itself, and so the bias and the
+ * groups, has no gradient.  Errors as mx_route. */
+mx_status mx_route_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t experts, int64_t logits_ld,
+                       mx_score score, int32_t top_k, int renorm, float scale, const int32_t* ids,
+                       const float* dweights, void* dlogits, int64_t dlogits_ld, mx_stream stream);
+
+/* The dispatch plan of ids [tokens x top_k]: assignment i = t * top_k + j
+ * sends token t to expert ids[i].  The assignments are sorted by expert,
+ * those of one expert in their own order (a stable sort); an id out of
+ * [0, experts) means no expert and sorts behind the last group.
+ *   offsets [experts + 1]: group starts, [0] = 0, [experts] = the number of
+ *     assignments that have an expert: the group_offsets of
+ *     mx_quantize_1d and mx_grouped_gemm.
+ *   row_index [tokens * top_k]: the token of each grouped position: their
+ *     row_index.  Positions past offsets[experts] hold the tokens of the
+ *     assignments without an expert, so every entry is a valid row.
+ *   slot [tokens x top_k]: the grouped position of each assignment, -1
+ *     without an expert: what mx_combine reads.
+ * workspace: mx_route_plan_workspace(tokens, top_k, experts) bytes, 4-byte
+ * aligned, its contents irrelevant before and after (0 bytes: NULL).
+ * experts <= 1024, tokens * top_k < 2^31.  Errors: MX_ERR_SHAPE, MX_ERR_NULL,
+ * MX_ERR_ALIGN, MX_ERR_LAUNCH.  tokens == 0 writes the offsets, all 0. */
+int64_t mx_route_plan_workspace(int64_t tokens, int32_t top_k, int32_t experts);
+mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t* offsets,
+                        int32_t* row_index, int32_t* slot, void* workspace, mx_stream stream);
+
+/* The weighted sum of the experts' rows: out[t] = residual[t] +
+ * sum_j weights[t][j] * y[slot[t][j]], summed in fp32 in the order of j and
+ * rounded once.
+ * y [rows x cols] (fp32 or bf16, rows y_ld elements apart, 0 = cols): the
+ * experts' outputs in grouped order.  slot [tokens x top_k] int32; a slot
+ * outside [0, rows) adds nothing.  weights [tokens x top_k] fp32, or NULL for
+ * 1 (the gradient of the gather of tokens into grouped order).  residual
+ * [tokens x cols] of out's type, or NULL; it may be out itself.  out
+ * [tokens x cols], ot fp32 or bf16 whatever y's type.
+ * Any cols >= 1 and any pitch; rows that start at 16-byte boundaries and hold
+ * whole 16-byte pieces are read fastest.  rows <= 2^31 - 1, tokens * top_k <
+ * 2^31.  Device pointers owned by the caller, aligned to their elements.
+ * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
+ * MX_ERR_LAUNCH.  tokens == 0 launches nothing. */
+mx_status mx_combine(const void* y, mx_dtype yt, int64_t rows, int64_t cols, int64_t y_ld, const int32_t* slot,
+                     const float* weights, int64_t tokens, int32_t top_k, const void* residual, int64_t residual_ld,
+                     void* out, mx_dtype ot, int64_t out_ld, mx_stream stream);
+
+/* Gradient of mx_combine (the residual's is dout itself): for every
+ * assignment with a slot s, dy[s] = weights[t][j] * dout[t], rounded once to
+ * y's type: the experts' output gradient in grouped order, which
+ * mx_quantize_1d and mx_quantize_1d_dual read; and dweights[t][j] =
+ * <dout[t], y[s]> summed in fp32 in a fixed order (0 without a slot).
+ * dout [tokens x cols] (dt), y and dy [rows x cols] (yt), pitches in
+ * elements, 0 = cols.  dweights may be NULL (y is then not read and may be
+ * NULL); weights may be NULL for 1.  Slots of different assignments are
+ * different, as mx_route_plan makes them.
+ * used_rows (DEVICE int32[1], or NULL): rows of dy from *used_rows on are set
+ * to 0, and a slot that names one of them counts as none (pass the plan's
+ * offsets + experts); with NULL rows that no slot names are not written.
+ * Errors as mx_combine. */
+mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const void* y, mx_dtype yt, int64_t rows,
+                         int64_t cols, int64_t y_ld, const int32_t* slot, const float* weights, int64_t tokens,
+                         int32_t top_k, const int32_t* used_rows, void* dy, int64_t dy_ld, float* dweights,
+                         mx_stream stream);
+
+/* The L2 norm over all elements of `count` gradient tensors, and clipping by
+ * it.  grads, types, numels (and outs) are HOST arrays of `count` entries:
+ * device pointers, element types (fp32 and bf16 may be mixed) and element
+ * counts (0 is allowed; its pointer is not looked at).  They are read during
+ * the call only.  Squares are summed in fp64 in a fixed order, so no square
+ * over- or underflows and equal inputs give equal bits.
+ * mx_grad_norm: *norm (DEVICE fp32) = sqrt(sum g^2); no tensors: 0.
+ * mx_grad_clip: also multiplies by c = min(1, max_norm / (norm + 1e-6))
+ * (rounded to fp32; each product rounded once to the tensor's type) into
+ * outs[i], of the same type and count; outs NULL, or outs[i] == grads[i]:
+ * in place.  A norm that is NaN or infinite leaves the values as they are
+ * (outs gets copies): the caller sees it in *norm and drops the step.
+ * max_norm >= 0.  workspace: mx_grad_workspace(count) bytes, 8-byte aligned,
+ * contents irrelevant before and after.  Outputs may not overlap other
+ * tensors.  At most 2^40 elements in all.
+ * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
+ * MX_ERR_LAUNCH. */
+int64_t mx_grad_workspace(int32_t count);
+mx_status mx_grad_norm(const void* const* grads, const mx_dtype* types, const int64_t* numels, int32_t count,
+                       double* workspace, float* norm, mx_stream stream);
+mx_status mx_grad_clip(const void* const* grads, const mx_dtype* types, const int64_t* numels, int32_t count,
+                       void* const* outs, float max_norm, double* workspace, float* norm, mx_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,598 @@
+// mx_route.hip -- routing tokens to experts: scores, selection, weights, their
+// gradient, and the dispatch plan the grouped kernels read (gfx950).
+#include <hip/hip_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/mx.h"
+#include "mx_device.h"
+#include "mx_host.h"
+
+namespace {
+
+using namespace mx;
+
+constexpr int MAX_EXPERTS = 1024;
+constexpr int MAX_TOP_K = 32;
+constexpr int MAX_GROUPS = 64;
+
+struct RouteArgs {
+    const void* logits;
+    int64_t tokens, ld;       // row pitch in elements
+    int experts;
+    const float* bias;        // or null
+    int score;                // MX_SOFTMAX, MX_SIGMOID
+    int groups, top_groups, group_best;
+    int top_k, renorm;
+    float scale;
+    int vec;                  // rows can be read four experts at a time
+    int32_t* ids;
+    float* weights;
+};
+
+// ---------------------------------------------------------------------------
+// Reductions over the L lanes (8, 16, 32 or 64) that share a row.  Within 16
+// lanes a rotation by a DPP row costs one move; between the 16-lane rows of a
+// wave a shuffle.  Every lane gets the result, in a fixed order.
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+
+struct MaxF { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+struct AddF { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
+// Keys are never NaN, so the plain instruction does; fmax() would first quiet
+// its operands, two instructions more.
+struct MaxD {
+    __device__ __forceinline__ double operator()(double a, double b) const {
+        double r;
+        asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+        return r;
+    }
+};
+
+constexpr int DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_HALF_MIRROR = 0x141, DPP_MIRROR = 0x140;
+
+template <int L, class T, class Op>
+__device__ __forceinline__ T row_reduce(T v, Op op) {
+    v = op(v, dpp<DPP_XOR1>(v));
+    v = op(v, dpp<DPP_XOR2>(v));
+    v = op(v, dpp<DPP_HALF_MIRROR>(v));       // the other quad of 8 lanes
+    if constexpr (L >= 16) v = op(v, dpp<DPP_MIRROR>(v));   // the other half of 16
+    if constexpr (L >= 32) v = op(v, __shfl_xor(v, 16));
+    if constexpr (L >= 64) v = op(v, __shfl_xor(v, 32));
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// Keys.  A selection key is an fp32 number; widened to fp64 it leaves 29 low
+// mantissa bits free, and the expert's index goes into the lowest 10 so that
+// the larger double is the larger key, or for equal keys the lower index.  All
+// keys of a row are then distinct and a maximum is one v_max_f64.
+// +inf becomes 2^128 and NaN -2^129, both outside fp32's range, so the index
+// fits in them too; an expert that cannot be chosen is NOT_THERE.
+// ---------------------------------------------------------------------------
+constexpr double NOT_THERE = -0x1p130;
+
+__device__ __forceinline__ double pack_key(float key, int e) {
+    double d = (double)(key + 0.0f);                       // -0 counts as 0
+    d = key == __builtin_inff() ? 0x1p128 : d;
+    d = key != key ? -0x1p129 : d;
+    uint64_t b = (uint64_t)__double_as_longlong(d);
+    b |= (b >> 63) ? (uint64_t)e : (uint64_t)(MAX_EXPERTS - 1 - e);
+    d = __longlong_as_double((long long)b);
+    return key == -__builtin_inff() ? NOT_THERE : d;
+}
+__device__ __forceinline__ bool key_there(double d) { return d > -0x1.8p129; }
+__device__ __forceinline__ int key_index(double d) {
+    const uint64_t b = (uint64_t)__double_as_longlong(d);
+    const int low = (int)(b & (MAX_EXPERTS - 1));
+    return (b >> 63) ? low : MAX_EXPERTS - 1 - low;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+    if constexpr (BF16) return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
+    else return ((const float*)p)[i];
+}
+
+// A lane's experts of a row: C chunks of four, chunk c at 4 (lane + L c).
+// Beyond the row's end: -inf.
+template <bool BF16, int L, int C>
+__device__ __forceinline__ void load_row(const void* logits, int64_t base, int experts, int vec, int lane, float* v) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = 4 * (lane + L * c);
+        if (vec && e < experts) {              // whole chunks only: experts % 4 == 0
+            if constexpr (BF16) {
+                const uint2 w = *(const uint2*)((const uint16_t*)logits + base + e);
+                v[4 * c + 0] = bf16lo(w.x);
+                v[4 * c + 1] = bf16hi(w.x);
+                v[4 * c + 2] = bf16lo(w.y);
+                v[4 * c + 3] = bf16hi(w.y);
+            } else {
+                const float4 w = *(const float4*)((const float*)logits + base + e);
+                v[4 * c + 0] = w.x;
+                v[4 * c + 1] = w.y;
+                v[4 * c + 2] = w.z;
+                v[4 * c + 3] = w.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[4 * c + i] = e + i < experts ? load_logit<BF16>(logits, base + e + i) : -__builtin_inff();
+        }
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// Row maximum and sum of exp(l - max) of a softmax; a row of -inf alone gives
+// (0, 0), and its scores are 0.
+template <int L, int N>
+__device__ __forceinline__ void softmax_stats(const float* v, float& top, float& sum) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+    m = row_reduce<L>(m, MaxF());
+    top = m == -__builtin_inff() ? 0.0f : m;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += expf(v[i] - top);
+    sum = row_reduce<L>(s, AddF());
+}
+
+// The chosen experts' part in their sum, renormalised: lane j holds chosen
+// expert j (there = it exists).  Softmax: p is the softmax over the chosen
+// logits.  Sigmoid: p = s / sum s; below -40 the scores are e^l to 24 bits, so
+// when the largest chosen logit is that low they are all scaled by its
+// e^-l, and scores that would underflow keep their proportions.
+// Every lane of the row calls it.
+template <int L>
+__device__ __forceinline__ float renormalised(float l, bool there, bool softmax, float& s) {
+    const float ninf = -__builtin_inff();
+    float top = row_reduce<L>(there ? l : ninf, MaxF());
+    top = top == ninf ? 0.0f : top;
+    s = softmax ? 0.0f : sigmoid(l);
+    const float part = !there ? 0.0f : softmax || top < -40.0f ? expf(l - top) : s;
+    const float sum = row_reduce<L>(part, AddF());
+    return there ? part / sum : 0.0f;
+}
+
+template <bool BF16, int L, int C>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+    constexpr int N = 4 * C, ROWS = 256 / L;
+    extern __shared__ float smem[];           // groups: keys, then the groups' scores and flags
+    const int lane = threadIdx.x & (L - 1), r = threadIdx.x / L;
+    const int64_t row0 = (int64_t)blockIdx.x * ROWS + r;
+    const bool live = row0 < a.tokens;
+    const int64_t row = live ? row0 : a.tokens - 1;
+    const int64_t base = row * a.ld;
+    const bool softmax = a.score == MX_SOFTMAX;
+    float v[N];
+    load_row<BF16, L, C>(a.logits, base, a.experts, a.vec, lane, v);
+
+    const bool by_score = a.bias || (a.groups > 1 && a.group_best > 1);
+    float top = 0.0f, sum = 1.0f;
+    if (softmax && (by_score || !a.renorm)) softmax_stats<L, N>(v, top, sum);
+    if (by_score) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = 4 * (lane + L * (i >> 2)) + (i & 3);
+            const float s = softmax ? expf(v[i] - top) / sum : sigmoid(v[i]);
+            const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+            v[i] = v[i] == -__builtin_inff() ? v[i] : s + b;
+        }
+    }
+    if (a.groups > 1) {
+        const int size = a.experts / a.groups;
+        // one spare word a group keeps the lanes that scan neighbouring groups on different banks
+        float* keys = smem + r * (a.experts + 3 * a.groups);
+        float* score = keys + a.experts + a.groups;
+        float* kept = score + a.groups;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = 4 * (lane + L * (i >> 2)) + (i & 3);
+            if (e < a.experts) keys[e + e / size] = v[i];
+        }
+        __syncthreads();
+        for (int g = lane; g < a.groups; g += L) {
+            double b1 = NOT_THERE, b2 = NOT_THERE;
+            for (int i = 0; i < size; ++i) {
+                const double d = pack_key(keys[g * (size + 1) + i], 0);
+                b2 = MaxD()(b2, fmin(b1, d));
+                b1 = MaxD()(b1, d);
+            }
+            const float none = -__builtin_inff();
+            // the packed index is below fp32's last place, so the keys come back whole
+            const float k1 = b1 == -0x1p129 ? __builtin_nanf("") : (float)b1;
+            const float k2 = b2 == -0x1p129 ? __builtin_nanf("") : (float)b2;
+            const float two = a.group_best > 1 && key_there(b2) ? k1 + k2 : k1;
+            // a sum of two lowest values stays above the score of an empty group
+            score[g] = !key_there(b1) ? none : two < -FLT_MAX ? -FLT_MAX : two;
+        }
+        __syncthreads();
+        for (int g = lane; g < a.groups; g += L) {
+            const double mine = pack_key(score[g], g);
+            int before = 0;
+            for (int h = 0; h < a.groups; ++h) before += pack_key(score[h], h) > mine;
+            kept[g] = before < a.top_groups ? 1.0f : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = 4 * (lane + L * (i >> 2)) + (i & 3);
+            if (e < a.experts && kept[e / size] == 0.0f) v[i] = -__builtin_inff();
+        }
+    }
+
+    double key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = pack_key(v[i], 4 * (lane + L * (i >> 2)) + (i & 3));
+    double mine = NOT_THERE;
+    for (int j = 0; j < a.top_k; ++j) {
+        double m = key[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) m = MaxD()(m, key[i]);
+        m = row_reduce<L>(m, MaxD());
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = key[i] == m ? NOT_THERE : key[i];
+        mine = lane == j ? m : mine;
+    }
+
+    const bool there = key_there(mine);
+    const int id = there ? key_index(mine) : -1;
+    const float l = there ? load_logit<BF16>(a.logits, base + id) : 0.0f;
+    float w;
+    if (a.renorm) {
+        float s;
+        w = renormalised<L>(l, there, softmax, s);
+    } else {
+        w = !there ? 0.0f : softmax ? expf(l - top) / sum : sigmoid(l);
+    }
+    if (live && lane < a.top_k) {
+        a.ids[row * a.top_k + lane] = id;
+        a.weights[row * a.top_k + lane] = a.scale * w;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the weights with respect to the logits (the choice is held
+// fixed).  With ds_j = scale dw_j at the chosen experts:
+//   softmax          dl_e = s_e (ds_e - sum_j ds_j s_j)        (every expert)
+//   softmax, renorm  dl_j = p_j (ds_j - sum_m ds_m p_m)
+//   sigmoid          dl_j = ds_j s_j (1 - s_j)
+//   sigmoid, renorm  dl_j = p_j (1 - s_j)(ds_j - sum_m ds_m p_m)
+// Only the first reads a whole row of logits.  The dense row is put together
+// in LDS and written once.
+// ---------------------------------------------------------------------------
+struct RouteBwdArgs {
+    const void* logits;
+    int64_t tokens, ld;
+    int experts, score, top_k, renorm;
+    float scale;
+    int vec, vec_out;
+    const int32_t* ids;
+    const float* dweights;
+    void* dlogits;
+    int64_t dld;
+};
+
+template <bool BF16, int L, int C>
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
+    constexpr int N = 4 * C, ROWS = 256 / L;
+    __shared__ float4 rows_of[ROWS][L * C];
+    const int lane = threadIdx.x & (L - 1), r = threadIdx.x / L;
+    const int64_t row0 = (int64_t)blockIdx.x * ROWS + r;
+    const bool live = row0 < a.tokens;
+    const int64_t row = live ? row0 : a.tokens - 1;
+    const int64_t base = row * a.ld;
+    const bool softmax = a.score == MX_SOFTMAX, dense = softmax && !a.renorm;
+    float v[N];
+    float top = 0.0f, sum = 1.0f;
+    if (dense) {
+        load_row<BF16, L, C>(a.logits, base, a.experts, a.vec, lane, v);
+        softmax_stats<L, N>(v, top, sum);
+    }
+    const int id = lane < a.top_k ? a.ids[row * a.top_k + lane] : -1;
+    const bool there = id >= 0 && id < a.experts;
+    const float ds = there ? a.scale * a.dweights[row * a.top_k + lane] : 0.0f;
+    const float l = there ? load_logit<BF16>(a.logits, base + id) : 0.0f;
+    float put = ds, dot = 0.0f;
+    if (a.renorm) {
+        float s;
+        const float p = renormalised<L>(l, there, softmax, s);
+        dot = row_reduce<L>(there ? ds * p : 0.0f, AddF());
+        put = p * (ds - dot) * (softmax ? 1.0f : sigmoid(-l));
+    } else if (softmax) {
+        dot = row_reduce<L>(there ? ds * (expf(l - top) / sum) : 0.0f, AddF());
+    } else {
+        put = ds * sigmoid(l) * sigmoid(-l);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) rows_of[r][lane + L * c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    __syncthreads();
+    if (there) ((float*)rows_of[r])[id] = put;
+    __syncthreads();
+    if (!live) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const float4 q = rows_of[r][lane + L * c];
+        float o[4] = {q.x, q.y, q.z, q.w};
+        const int e = 4 * (lane + L * c);
+        if (dense) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float s = v[4 * c + i] == -__builtin_inff() ? 0.0f : expf(v[4 * c + i] - top) / sum;
+                o[i] = s * (o[i] - dot);
+            }
+        }
+        if (a.vec_out && e < a.experts) {
+            if constexpr (BF16) {
+                uint2 w;
+                w.x = f32_to_bf16_rne(o[0]) | f32_to_bf16_rne(o[1]) << 16;
+                w.y = f32_to_bf16_rne(o[2]) | f32_to_bf16_rne(o[3]) << 16;
+                *(uint2*)((uint16_t*)a.dlogits + row * a.dld + e) = w;
+            } else {
+                *(float4*)((float*)a.dlogits + row * a.dld + e) = make_float4(o[0], o[1], o[2], o[3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (e + i >= a.experts) continue;
+                if constexpr (BF16) ((uint16_t*)a.dlogits)[row * a.dld + e + i] = (uint16_t)f32_to_bf16_rne(o[i]);
+                else ((float*)a.dlogits)[row * a.dld + e + i] = o[i];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch plan: a stable counting sort of the assignments i = t * top_k + j
+// by expert.  Assignments without an expert sort into one more bin behind the
+// last group.
+//
+// Within a wave the lanes with the same expert find each other by comparing
+// the bits of the expert's number (one ballot a bit); an assignment's place is
+// its group's start, plus its expert's count in the workgroups, waves and
+// lanes before it.  All counts are integers: the result is the same every run.
+// ---------------------------------------------------------------------------
+constexpr int PLAN_THREADS = 1024, PLAN_WAVES = PLAN_THREADS / 64;
+constexpr int PLAN_BINS = MAX_EXPERTS + 1;
+
+struct PlanArgs {
+    const int32_t* ids;
+    int64_t assignments;
+    int top_k, experts;
+    int64_t chunk;            // assignments of a workgroup, a multiple of PLAN_THREADS
+    int blocks;               // workgroups with assignments
+    int32_t* counts;          // [workgroups][experts + 1]
+    int32_t *offsets, *row_index, *slot;
+};
+
+__device__ __forceinline__ int plan_bin(const PlanArgs& a, int64_t i) {
+    const int id = a.ids[i];
+    return id >= 0 && id < a.experts ? id : a.experts;
+}
+
+__global__ __launch_bounds__(PLAN_THREADS) void plan_count_kernel(PlanArgs a) {
+    __shared__ int hist[PLAN_BINS];
+    for (int e = threadIdx.x; e <= a.experts; e += PLAN_THREADS) hist[e] = 0;
+    __syncthreads();
+    const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(begin + a.chunk, a.assignments);
+    for (int64_t i = begin + threadIdx.x; i < end; i += PLAN_THREADS) atomicAdd(&hist[plan_bin(a, i)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.experts; e += PLAN_THREADS)
+        a.counts[(int64_t)blockIdx.x * (a.experts + 1) + e] = hist[e];
+}
+
+// Exclusive prefix sums of n counts in LDS, by one wave.
+__device__ __forceinline__ void wave_scan(const int* in, int* out, int n) {
+    int run = 0;
+    for (int at = 0; at < n; at += 64) {
+        const int i = at + (int)threadIdx.x;
+        const int own = i < n ? in[i] : 0;
+        int x = own;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(x, d);
+            if ((int)threadIdx.x >= d) x += y;
+        }
+        if (i < n) out[i] = run + x - own;
+        run += __shfl(x, 63);
+    }
+}
+
+__global__ __launch_bounds__(PLAN_THREADS) void plan_scatter_kernel(PlanArgs a) {
+    __shared__ int total[PLAN_BINS], before[PLAN_BINS], base[PLAN_BINS];
+    __shared__ uint16_t wave_count[PLAN_WAVES][PLAN_BINS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int bins = a.experts + 1;
+    for (int e = tid; e < bins; e += PLAN_THREADS) total[e] = before[e] = 0;
+    __syncthreads();
+    // the counts of all workgroups, and of those before this one: several
+    // threads share a bin when there are fewer bins than threads
+    const int share = max(1, PLAN_THREADS / bins);
+    for (int at = tid; at < bins * share; at += PLAN_THREADS) {
+        const int e = at % bins;
+        int all = 0, mine = 0;
+        for (int b = at / bins; b < a.blocks; b += share) {
+            const int n = a.counts[(int64_t)b * bins + e];
+            all += n;
+            if (b < (int)blockIdx.x) mine += n;
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&before[e], mine);
+    }
+    __syncthreads();
+    if (wave == 0) wave_scan(total, base, bins);
+    __syncthreads();
+    for (int e = tid; e < bins; e += PLAN_THREADS) {
+        if (blockIdx.x == 0) a.offsets[e] = base[e];
+        base[e] += before[e];
+    }
+    const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(begin + a.chunk, a.assignments);
+    for (int64_t at = begin; at < end; at += PLAN_THREADS) {
+        for (int e = lane; e < bins; e += 64) wave_count[wave][e] = 0;
+        __syncthreads();
+        const int64_t i = at + tid;
+        const bool live = i < end;
+        const int e = live ? plan_bin(a, i) : 0;
+        uint64_t same = __ballot(live);
+        for (int bit = 1; bit <= a.experts; bit <<= 1) {
+            const uint64_t set = __ballot((e & bit) != 0);
+            same &= (e & bit) ? set : ~set;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        if (live && rank == 0) wave_count[wave][e] = (uint16_t)__popcll(same);
+        __syncthreads();
+        for (int b = tid; b < bins; b += PLAN_THREADS) {
+            int run = 0;
+#pragma unroll
+            for (int w = 0; w < PLAN_WAVES; ++w) {
+                const int n = wave_count[w][b];
+                wave_count[w][b] = (uint16_t)run;
+                run += n;
+            }
+            before[b] = run;                  // this tile's count
+        }
+        __syncthreads();
+        if (live) {
+            const int pos = base[e] + wave_count[wave][e] + rank;
+            a.row_index[pos] = (int)(i / a.top_k);
+            a.slot[i] = e < a.experts ? pos : -1;
+        }
+        __syncthreads();
+        for (int b = tid; b < bins; b += PLAN_THREADS) base[b] += before[b];
+    }
+}
+
+int64_t plan_chunk(int64_t assignments) {
+    // at most 256 workgroups, each a whole number of tiles
+    const int64_t tiles = ceil_div(assignments, PLAN_THREADS);
+    return PLAN_THREADS * (tiles <= 0 ? 1 : ceil_div(tiles, 256));
+}
+
+template <bool B, int L, int C>
+void launch_route(const RouteArgs& a, hipStream_t s) {
+    constexpr int ROWS = 256 / L;
+    const size_t lds = a.groups > 1 ? sizeof(float) * ROWS * (size_t)(a.experts + 3 * a.groups) : 0;
+    hipLaunchKernelGGL((route_kernel<B, L, C>), dim3((uint32_t)ceil_div(a.tokens, ROWS)), dim3(256), lds, s, a);
+}
+template <bool B, int L, int C>
+void launch_route(const RouteBwdArgs& a, hipStream_t s) {
+    constexpr int ROWS = 256 / L;
+    hipLaunchKernelGGL((route_bwd_kernel<B, L, C>), dim3((uint32_t)ceil_div(a.tokens, ROWS)), dim3(256), 0, s, a);
+}
+
+// The lanes that share a row and the chunks of four experts each holds: enough
+// for the experts, and a lane for each chosen one.
+template <bool B, class A>
+void dispatch_route(const A& a, hipStream_t s) {
+    const int e = a.experts, k = a.top_k;
+    if (e <= 32 && k <= 8) launch_route<B, 8, 1>(a, s);
+    else if (e <= 64 && k <= 16) launch_route<B, 16, 1>(a, s);
+    else if (e <= 128 && k <= 16) launch_route<B, 16, 2>(a, s);
+    else if (e <= 256 && k <= 16) launch_route<B, 16, 4>(a, s);
+    else if (e <= 512) launch_route<B, 32, 4>(a, s);
+    else launch_route<B, 64, 4>(a, s);
+}
+
+mx_status check_route(mx_dtype lt, int64_t tokens, int32_t experts, int64_t ld, mx_score score, int32_t top_k,
+                      float scale) {
+    if (lt != MX_F32 && lt != MX_BF16) return MX_ERR_DTYPE;
+    if (score != MX_SOFTMAX && score != MX_SIGMOID) return MX_ERR_UNSUPPORTED;
+    if (tokens < 0 || experts < 1 || experts > MAX_EXPERTS) return MX_ERR_SHAPE;
+    if (top_k < 1 || top_k > experts || top_k > MAX_TOP_K) return MX_ERR_SHAPE;
+    if (ld && ld < experts) return MX_ERR_SHAPE;
+    if (!(scale - scale == 0.0f)) return MX_ERR_SHAPE;
+    if (tokens > (int64_t)INT32_MAX / top_k) return MX_ERR_SHAPE;
+    if (tokens > ((int64_t)1 << 24)) return MX_ERR_SHAPE;   // 64 lanes a token at most, fewer than 2^32 threads
+    return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_route(const void* logits, mx_dtype lt, int64_t tokens, int32_t experts, int64_t logits_ld,
+                   const float* bias, mx_score score, int32_t groups, int32_t top_groups, int32_t group_best,
+                   int32_t top_k, int renorm, float scale, int32_t* ids, float* weights, mx_stream stream) {
+    const mx_status bad = check_route(lt, tokens, experts, logits_ld, score, top_k, scale);
+    if (bad != MX_OK) return bad;
+    if (groups < 1 || groups > MAX_GROUPS || experts % groups || top_groups < 1 || top_groups > groups)
+        return MX_ERR_SHAPE;
+    if (group_best != 1 && group_best != 2) return MX_ERR_SHAPE;
+    if (top_k > top_groups * (experts / groups)) return MX_ERR_SHAPE;
+    if (tokens == 0) return MX_OK;
+    if (!logits || !ids || !weights) return MX_ERR_NULL;
+    if (!aligned_to(logits, type_bytes(lt)) || !aligned_to(bias, 4) || !aligned_to(ids, 4) || !aligned_to(weights, 4))
+        return MX_ERR_ALIGN;
+    RouteArgs a{logits, tokens, logits_ld ? logits_ld : experts, experts, bias, score, groups, top_groups, group_best,
+                top_k, renorm != 0, scale, 0, ids, weights};
+    if (groups == top_groups) a.groups = 1;   // every group stays
+    a.vec = experts % 4 == 0 && a.ld % 4 == 0 && aligned_to(logits, 4 * type_bytes(lt));
+    (void)hipGetLastError();
+    if (lt == MX_BF16) dispatch_route<true>(a, (hipStream_t)stream);
+    else dispatch_route<false>(a, (hipStream_t)stream);
+    return launch_status();
+}
+
+mx_status mx_route_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t experts, int64_t logits_ld,
+                       mx_score score, int32_t top_k, int renorm, float scale, const int32_t* ids,
+                       const float* dweights, void* dlogits, int64_t dlogits_ld, mx_stream stream) {
+    const mx_status bad = check_route(lt, tokens, experts, logits_ld, score, top_k, scale);
+    if (bad != MX_OK) return bad;
+    if (dlogits_ld && dlogits_ld < experts) return MX_ERR_SHAPE;
+    if (tokens == 0) return MX_OK;
+    if (!logits || !ids || !dweights || !dlogits) return MX_ERR_NULL;
+    if (!aligned_to(logits, type_bytes(lt)) || !aligned_to(ids, 4) || !aligned_to(dweights, 4) ||
+        !aligned_to(dlogits, type_bytes(lt)))
+        return MX_ERR_ALIGN;
+    RouteBwdArgs a{logits, tokens, logits_ld ? logits_ld : experts, experts, score, top_k, renorm != 0, scale, 0, 0,
+                   ids, dweights, dlogits, dlogits_ld ? dlogits_ld : experts};
+    a.vec = experts % 4 == 0 && a.ld % 4 == 0 && aligned_to(logits, 4 * type_bytes(lt));
+    a.vec_out = experts % 4 == 0 && a.dld % 4 == 0 && aligned_to(dlogits, 4 * type_bytes(lt));
+    (void)hipGetLastError();
+    if (lt == MX_BF16) dispatch_route<true>(a, (hipStream_t)stream);
+    else dispatch_route<false>(a, (hipStream_t)stream);
+    return launch_status();
+}
+
+int64_t mx_route_plan_workspace(int64_t tokens, int32_t top_k, int32_t experts) {
+    if (tokens < 0 || top_k < 1 || experts < 1 || experts > MAX_EXPERTS || tokens > (int64_t)INT32_MAX / top_k)
+        return 0;
+    const int64_t n = tokens * top_k;
+    return 4 * ceil_div(n, plan_chunk(n)) * (experts + 1);
+}
+
+mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t* offsets,
+                        int32_t* row_index, int32_t* slot, void* workspace, mx_stream stream) {
+    if (tokens < 0 || experts < 1 || experts > MAX_EXPERTS || top_k < 1) return MX_ERR_SHAPE;
+    if (tokens > (int64_t)INT32_MAX / top_k) return MX_ERR_SHAPE;
+    if (!offsets) return MX_ERR_NULL;
+    const int64_t n = tokens * top_k;
+    if (n > 0 && (!ids || !row_index || !slot || !workspace)) return MX_ERR_NULL;
+    if (!aligned_to(ids, 4) || !aligned_to(offsets, 4) || !aligned_to(row_index, 4) || !aligned_to(slot, 4) ||
+        !aligned_to(workspace, 4))
+        return MX_ERR_ALIGN;
+    const int64_t chunk = plan_chunk(n);
+    PlanArgs a{ids, n, top_k, experts, chunk, (int)ceil_div(n, chunk), (int32_t*)workspace, offsets, row_index, slot};
+    hipStream_t s = (hipStream_t)stream;
+    (void)hipGetLastError();
+    if (n > 0) hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(PLAN_THREADS), 0, s, a);
+    // with nothing to sort one workgroup writes the offsets, all 0
+    hipLaunchKernelGGL(plan_scatter_kernel, dim3(max(a.blocks, 1)), dim3(PLAN_THREADS), 0, s, a);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -20,6 +20,8 @@ RNE, SR = 0, 1
 # scale storage orders (include/mx.h): 2D B scales; staged ([stage][row][8 bytes]);
 # column-wise groups padded to 256 tokens
 SCALES_B_2D, SCALES_STAGED, GROUPS_PAD256 = 1, 2, 4
+# the router's scores (include/mx.h, mx_score)
+SOFTMAX, SIGMOID = 0, 1
 STATUS = {0: "MX_OK", 1: "MX_ERR_NULL", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGN",
           4: "MX_ERR_DTYPE", 5: "MX_ERR_UNSUPPORTED", 6: "MX_ERR_LAUNCH"}
 
@@ -64,9 +66,22 @@ def lib():
                                       ctypes.c_float, P, c_int, P]
         L.mx_grouped_gemm_q.argtypes = [P, i64, P, P, P, i64, P, c_int, P, i32, i64, i64, i64,
                                         ctypes.c_float, P, P, i64, P, P]
+        f32 = ctypes.c_float
+        L.mx_route.argtypes = [P, c_int, i64, i32, i64, P, c_int, i32, i32, i32, i32, c_int, f32, P, P, P]
+        L.mx_route_bwd.argtypes = [P, c_int, i64, i32, i64, c_int, i32, c_int, f32, P, P, P, i64, P]
+        L.mx_route_plan_workspace.argtypes = [i64, i32, i32]
+        L.mx_route_plan_workspace.restype = i64
+        L.mx_route_plan.argtypes = [P, i64, i32, i32, P, P, P, P, P]
+        L.mx_combine.argtypes = [P, c_int, i64, i64, i64, P, P, i64, i32, P, i64, P, c_int, i64, P]
+        L.mx_combine_bwd.argtypes = [P, c_int, i64, P, c_int, i64, i64, i64, P, P, i64, i32, P, P, i64, P, P]
+        L.mx_grad_workspace.argtypes = [i32]
+        L.mx_grad_workspace.restype = i64
+        L.mx_grad_norm.argtypes = [P, P, P, i32, P, P, P]
+        L.mx_grad_clip.argtypes = [P, P, P, i32, P, f32, P, P, P]
         for name in ("mx_rht", "mx_quantize_1d", "mx_quantize_2d", "mx_quantize_2d_deosc", "mx_dequantize",
                      "mx_quantize_1d_ex", "mx_dequantize_1d_ex", "mx_quantize_1d_dual",
-                     "mx_grouped_gemm", "mx_grouped_gemm_q"):
+                     "mx_grouped_gemm", "mx_grouped_gemm_q", "mx_route", "mx_route_bwd", "mx_route_plan",
+                     "mx_combine", "mx_combine_bwd", "mx_grad_norm", "mx_grad_clip"):
             getattr(L, name).restype = c_int
         _lib = L
     return _lib
@@ -498,3 +513,217 @@ def grouped_gemm_q(a_codes, a_scales, b_codes, b_scales, group_offsets, M, N, K,
         _scale_flags(b_scale_2d, staged), _ptr(group_offsets), G, M, N, K, float(alpha),
         _ptr(c), _ptr(codes), c_ld, _ptr(scales), _stream()))
     return c, codes, scales
+
+
+# ---------------------------------------------------------------------------
+# Routing, the experts' rows back into tokens, gradient clipping
+# ---------------------------------------------------------------------------
+def _rows(t, name, shape=None, dtype=None):
+    """A device matrix with contiguous rows any pitch apart; returns the pitch
+    in elements (0 when the rows are contiguous)."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s: expected shape %s, got %s" % (name, shape or "[rows, cols]", tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    rows, cols = t.shape
+    if rows == 0:
+        return 0
+    ld = t.stride(0)
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and ld < cols):
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    return ld if rows > 1 and ld != cols else 0
+
+
+def route(logits, top_k: int, score: int = SOFTMAX, bias=None, groups: int = 1, top_groups: int = 1,
+          group_best: int = 1, renorm: bool = True, scale: float = 1.0, ids=None, weights=None):
+    """The top_k experts of each token and their weights from the router's
+    logits [tokens, experts] (fp32 or bf16; rows may be padded): ids int32
+    and weights fp32 [tokens, top_k].  See mx_route for scores, bias, groups
+    and what happens to masked experts."""
+    torch = _torch()
+    ld = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    if bias is not None:
+        _shaped(bias, (experts,), torch.float32, "bias")
+    if ids is None:
+        ids = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
+    else:
+        _shaped(ids, (tokens, top_k), torch.int32, "ids")
+    if weights is None:
+        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        _shaped(weights, (tokens, top_k), torch.float32, "weights")
+    _check("mx_route", lib().mx_route(
+        _ptr(logits), _dtype_code(logits), tokens, experts, ld, _ptr(bias), score, groups, top_groups, group_best,
+        top_k, int(bool(renorm)), scale, _ptr(ids), _ptr(weights), _stream()))
+    return ids, weights
+
+
+def route_bwd(logits, ids, dweights, score: int = SOFTMAX, renorm: bool = True, scale: float = 1.0, dlogits=None):
+    """The gradient of route's weights with respect to the logits, for the ids
+    it chose: dlogits [tokens, experts] of the logits' type (see
+    mx_route_bwd)."""
+    torch = _torch()
+    ld = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    top_k = ids.shape[1]
+    _shaped(ids, (tokens, top_k), torch.int32, "ids")
+    _shaped(dweights, (tokens, top_k), torch.float32, "dweights")
+    if dlogits is None:
+        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    dld = _rows(dlogits, "dlogits", (tokens, experts), logits.dtype)
+    _check("mx_route_bwd", lib().mx_route_bwd(
+        _ptr(logits), _dtype_code(logits), tokens, experts, ld, score, top_k, int(bool(renorm)), scale, _ptr(ids),
+        _ptr(dweights), _ptr(dlogits), dld, _stream()))
+    return dlogits
+
+
+def route_plan(ids, num_experts: int, offsets=None, row_index=None, slot=None, workspace=None):
+    """The dispatch plan of ids [tokens, top_k] (-1: no expert): offsets
+    [num_experts + 1] (the group_offsets of the quantizers and the grouped
+    GEMM), row_index [tokens * top_k] (their row gather) and slot [tokens,
+    top_k] (where combine finds each assignment's row, -1: nowhere), all
+    int32; see mx_route_plan.  workspace: uint8, at least
+    mx_route_plan_workspace bytes, or None to allocate it."""
+    torch = _torch()
+    if ids.dim() != 2 or ids.dtype != torch.int32:
+        raise ValueError("ids must be int32 [tokens, top_k]")
+    _dev(ids, "ids")
+    tokens, top_k = ids.shape
+    dev, i32 = ids.device, torch.int32
+    if offsets is None:
+        offsets = torch.empty(num_experts + 1, dtype=i32, device=dev)
+    else:
+        _shaped(offsets, (num_experts + 1,), i32, "offsets")
+    if row_index is None:
+        row_index = torch.empty(tokens * top_k, dtype=i32, device=dev)
+    else:
+        _shaped(row_index, (tokens * top_k,), i32, "row_index")
+    if slot is None:
+        slot = torch.empty((tokens, top_k), dtype=i32, device=dev)
+    else:
+        _shaped(slot, (tokens, top_k), i32, "slot")
+    need = lib().mx_route_plan_workspace(tokens, top_k, num_experts)
+    workspace = _workspace(workspace, need, dev)
+    _check("mx_route_plan", lib().mx_route_plan(
+        _ptr(ids), tokens, top_k, num_experts, _ptr(offsets), _ptr(row_index), _ptr(slot), _ptr(workspace),
+        _stream()))
+    return offsets, row_index, slot
+
+
+def _workspace(t, need, device):
+    """A uint8 device buffer of at least `need` bytes."""
+    torch = _torch()
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if t.dtype != torch.uint8 or t.numel() < need:
+        raise ValueError("workspace must be uint8 of at least %d bytes" % need)
+    return _dev(t, "workspace")
+
+
+def _slots(slot, weights):
+    torch = _torch()
+    if slot.dim() != 2:
+        raise ValueError("slot must be [tokens, top_k]")
+    tokens, top_k = slot.shape
+    _shaped(slot, (tokens, top_k), torch.int32, "slot")
+    if weights is not None:
+        _shaped(weights, (tokens, top_k), torch.float32, "weights")
+    return tokens, top_k
+
+
+def combine(y, slot, weights=None, residual=None, out_dtype=None, out=None):
+    """out[t] = residual[t] + sum_j weights[t, j] * y[slot[t, j]]: the experts'
+    rows y [rows, cols] back into tokens (see mx_combine).  weights None: 1.
+    out is of y's type unless out_dtype or out says otherwise; residual has
+    out's type.  Rows may be padded."""
+    torch = _torch()
+    tokens, top_k = _slots(slot, weights)
+    y_ld = _rows(y, "y")
+    rows, cols = y.shape
+    if out is None:
+        out = torch.empty((tokens, cols), dtype=out_dtype or y.dtype, device=y.device)
+    out_ld = _rows(out, "out", (tokens, cols), out_dtype)
+    res_ld = _rows(residual, "residual", (tokens, cols), out.dtype) if residual is not None else 0
+    _check("mx_combine", lib().mx_combine(
+        _ptr(y), _dtype_code(y), rows, cols, y_ld, _ptr(slot), _ptr(weights), tokens, top_k, _ptr(residual), res_ld,
+        _ptr(out), _dtype_code(out), out_ld, _stream()))
+    return out
+
+
+def combine_bwd(dout, y, slot, weights=None, used_rows=None, dy=None, dweights=None, need_dweights: bool = True):
+    """Gradient of combine: (dy [rows, cols] of y's type, dweights fp32
+    [tokens, top_k]) from dout [tokens, cols] (see mx_combine_bwd).
+    used_rows: an int32 device tensor of one element, the number of rows that
+    slots name (the plan's offsets[-1:]); the rows of dy after it become 0.
+    Without it rows that no slot names are left unwritten.
+    need_dweights=False: dweights is None and y is not read."""
+    torch = _torch()
+    tokens, top_k = _slots(slot, weights)
+    y_ld = _rows(y, "y")
+    rows, cols = y.shape
+    dout_ld = _rows(dout, "dout", (tokens, cols))
+    if used_rows is not None:
+        _index_vector(used_rows, "used_rows", min_numel=1)
+    if dy is None:
+        dy = torch.empty((rows, cols), dtype=y.dtype, device=y.device)
+    dy_ld = _rows(dy, "dy", (rows, cols), y.dtype)
+    if dweights is not None:
+        _shaped(dweights, (tokens, top_k), torch.float32, "dweights")
+    elif need_dweights:
+        dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=y.device)
+    _check("mx_combine_bwd", lib().mx_combine_bwd(
+        _ptr(dout), _dtype_code(dout), dout_ld, _ptr(y), _dtype_code(y), rows, cols, y_ld, _ptr(slot),
+        _ptr(weights), tokens, top_k, _ptr(used_rows), _ptr(dy), dy_ld, _ptr(dweights), _stream()))
+    return dy, dweights
+
+
+def _grad_list(grads, name):
+    """The host arrays of a gradient list (any shapes, contiguous, fp32 and
+    bf16 mixed)."""
+    grads = list(grads)
+    n = len(grads)
+    types = (ctypes.c_int * n)(*[_dtype_code(g) for g in grads])
+    numels = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    ptrs = (ctypes.c_void_p * n)(*[_dev(g, name).data_ptr() for g in grads])
+    return grads, n, types, numels, ptrs
+
+
+def grad_norm(grads, norm=None, workspace=None):
+    """The L2 norm over all elements of the tensors in grads: a 0-dim fp32
+    device tensor (see mx_grad_norm).  workspace: uint8, at least
+    mx_grad_workspace bytes, or None to allocate it."""
+    return _grad_call("mx_grad_norm", grads, None, None, norm, workspace)
+
+
+def grad_clip(grads, max_norm: float, outs=None, norm=None, workspace=None):
+    """Scales the tensors in grads by min(1, max_norm / (norm + 1e-6)), in
+    place or into the tensors of outs (same types and shapes), and returns
+    their norm before that as a 0-dim fp32 device tensor.  A norm that is not
+    finite leaves the values as they are (see mx_grad_clip)."""
+    return _grad_call("mx_grad_clip", grads, outs, float(max_norm), norm, workspace)
+
+
+def _grad_call(fn, grads, outs, max_norm, norm, workspace):
+    torch = _torch()
+    grads, n, types, numels, ptrs = _grad_list(grads, "grads")
+    if outs is not None:
+        outs, m, out_types, out_numels, out_ptrs = _grad_list(outs, "outs")
+        if m != n or out_types[:] != types[:] or any(g.shape != o.shape for g, o in zip(grads, outs)):
+            raise ValueError("outs must match grads in number, types and shapes")
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
+    else:
+        _shaped(norm, (), torch.float32, "norm")
+    workspace = _workspace(workspace, lib().mx_grad_workspace(n), norm.device)
+    if fn == "mx_grad_norm":
+        code = lib().mx_grad_norm(ptrs, types, numels, n, _ptr(workspace), _ptr(norm), _stream())
+    else:
+        code = lib().mx_grad_clip(ptrs, types, numels, n, out_ptrs if outs is not None else None, max_norm,
+                                  _ptr(workspace), _ptr(norm), _stream())
+    _check(fn, code)
+    return norm
