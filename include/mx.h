@@ -406,7 +406,8 @@ mx_status mx_grouped_gemm_q(const uint8_t* a_codes, int64_t a_ld, const uint8_t*
  *   - Groups: the experts form `groups` groups of experts / groups
  *     consecutive ones.  A group's score is its best key (group_best = 1) or
  *     the sum of its two best (2; of one, if only one is available), rounded
- *     to fp32.  Experts outside the top_groups best groups are not chosen.
+ *     to fp32 and no lower than its lowest value, which NaN counts as.
+ *     Experts outside the top_groups best groups are not chosen.
  *     groups = 1: no such limit.
  *   - ids [tokens x top_k] int32: the chosen experts, best first; of equal
  *     keys (and equal groups) the lower index wins.  Where fewer than top_k
@@ -452,7 +453,8 @@ mx_status mx_route_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t 
  *   slot [tokens x top_k]: the grouped position of each assignment, -1
  *     without an expert: what mx_combine reads.
  * workspace: mx_route_plan_workspace(tokens, top_k, experts) bytes, 4-byte
- * aligned, its contents irrelevant before and after (0 bytes: NULL).
+ * aligned, its contents irrelevant before and after; where that is 0, NULL
+ * will do.
  * experts <= 1024, tokens * top_k < 2^31.  Errors: MX_ERR_SHAPE, MX_ERR_NULL,
  * MX_ERR_ALIGN, MX_ERR_LAUNCH.  tokens == 0 writes the offsets, all 0. */
 int64_t mx_route_plan_workspace(int64_t tokens, int32_t top_k, int32_t experts);

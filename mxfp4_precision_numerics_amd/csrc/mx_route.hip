@@ -26,7 +26,7 @@ struct RouteArgs {
     int groups, top_groups, group_best;
     int top_k, renorm;
     float scale;
-    int vec;                  // rows can be read four experts at a time
+    int vec, vec_bias;        // rows, the bias can be read four experts at a time
     int32_t* ids;
     float* weights;
 };
@@ -50,15 +50,6 @@ __device__ __forceinline__ double dpp(double v) {
 
 struct MaxF { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 struct AddF { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
-// Keys are never NaN, so the plain instruction does; fmax() would first quiet
-// its operands, two instructions more.
-struct MaxD {
-    __device__ __forceinline__ double operator()(double a, double b) const {
-        double r;
-        asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-        return r;
-    }
-};
 
 constexpr int DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_HALF_MIRROR = 0x141, DPP_MIRROR = 0x140;
 
@@ -74,29 +65,49 @@ __device__ __forceinline__ T row_reduce(T v, Op op) {
 }
 
 // ---------------------------------------------------------------------------
-// Keys.  A selection key is an fp32 number; widened to fp64 it leaves 29 low
-// mantissa bits free, and the expert's index goes into the lowest 10 so that
-// the larger double is the larger key, or for equal keys the lower index.  All
-// keys of a row are then distinct and a maximum is one v_max_f64.
-// +inf becomes 2^128 and NaN -2^129, both outside fp32's range, so the index
-// fits in them too; an expert that cannot be chosen is NOT_THERE.
+// Keys.  The bits of an fp32 key, flipped so that they grow with it as an
+// unsigned number, are the leading mantissa and exponent bits of a double
+// whose exponent's top bits are fixed (a positive normal number whatever the
+// key), and 1023 - e, e the expert's index, its lowest ten bits.  So a larger
+// double is a larger key, or of equal keys the lower index; all keys of a row
+// are distinct, and keeping the larger or the smaller of two, index and all,
+// is one v_max_f64 or v_min_f64, which this GPU issues as fast as the fp32
+// ones.  A pair of an fp32 key and an index would take a comparison and two
+// selects for each.
+// Unsigned key 0 is an expert that cannot be chosen; NaN takes the place of
+// -inf, behind every number.
 // ---------------------------------------------------------------------------
-constexpr double NOT_THERE = -0x1p130;
+struct MaxD {
+    // (fmax() would quiet its operands first; these are never NaN)
+    __device__ __forceinline__ double operator()(double a, double b) const {
+        double r;
+        asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+        return r;
+    }
+};
+struct MinD {
+    __device__ __forceinline__ double operator()(double a, double b) const {
+        double r;
+        asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+        return r;
+    }
+};
 
-__device__ __forceinline__ double pack_key(float key, int e) {
-    double d = (double)(key + 0.0f);                       // -0 counts as 0
-    d = key == __builtin_inff() ? 0x1p128 : d;
-    d = key != key ? -0x1p129 : d;
-    uint64_t b = (uint64_t)__double_as_longlong(d);
-    b |= (b >> 63) ? (uint64_t)e : (uint64_t)(MAX_EXPERTS - 1 - e);
-    d = __longlong_as_double((long long)b);
-    return key == -__builtin_inff() ? NOT_THERE : d;
+__device__ __forceinline__ double make_key(uint32_t u, int e) {
+    const uint32_t hi = __builtin_amdgcn_alignbit(1u, u, 3);       // 001 and the upper 29 bits
+    const uint32_t lo = (u << 29) | (uint32_t)(MAX_EXPERTS - 1 - e);
+    return __hiloint2double((int)hi, (int)lo);
 }
-__device__ __forceinline__ bool key_there(double d) { return d > -0x1.8p129; }
+__device__ __forceinline__ double pack_key(float key, int e) {
+    const uint32_t b = __float_as_uint(fmaxf(key, -__builtin_inff()) + 0.0f);    // NaN: -inf; -0: 0
+    const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    return make_key(key == -__builtin_inff() ? 0u : u, e);
+}
+__device__ __forceinline__ bool key_there(double d) {
+    return __builtin_amdgcn_alignbit((uint32_t)__double2hiint(d), (uint32_t)__double2loint(d), 29) != 0;
+}
 __device__ __forceinline__ int key_index(double d) {
-    const uint64_t b = (uint64_t)__double_as_longlong(d);
-    const int low = (int)(b & (MAX_EXPERTS - 1));
-    return (b >> 63) ? low : MAX_EXPERTS - 1 - low;
+    return MAX_EXPERTS - 1 - (__double2loint(d) & (MAX_EXPERTS - 1));
 }
 
 template <bool BF16>
@@ -136,6 +147,15 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t base, int e
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
+// e^x and 1 / (1 + e^-x) by the exponential and reciprocal instructions, for
+// every expert of a row: e^x is off by |x| 2^-23 relative, which the sums and
+// keys it goes into hold at a share of e^x itself; as keys the scores are good
+// to 2e-7 absolute.  The weights of the chosen few use expf and a division.
+__device__ __forceinline__ float quick_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float quick_sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + quick_exp(-x));
+}
+
 // Row maximum and sum of exp(l - max) of a softmax; a row of -inf alone gives
 // (0, 0), and its scores are 0.
 template <int L, int N>
@@ -147,7 +167,7 @@ __device__ __forceinline__ void softmax_stats(const float* v, float& top, float&
     top = m == -__builtin_inff() ? 0.0f : m;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) s += expf(v[i] - top);
+    for (int i = 0; i < N; ++i) s += quick_exp(v[i] - top);
     sum = row_reduce<L>(s, AddF());
 }
 
@@ -168,10 +188,145 @@ __device__ __forceinline__ float renormalised(float l, bool there, bool softmax,
     return there ? part / sum : 0.0f;
 }
 
-template <bool BF16, int L, int C>
+// ---------------------------------------------------------------------------
+// Group scores and the mask of the groups that stay (bit g).  The lanes of a
+// row put their keys into LDS, each group behind four spare words so that
+// lanes scanning neighbouring groups meet different banks; 2^n lanes share the
+// scan of a group, as many as there are.  A group's place is the number of
+// groups before it.  Rows lie within a wave, so its own order is enough.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int L, int C>
+__device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, float* keys, int lane, const float* v) {
+    const int size = a.experts / a.groups;
+    const float inv = 1.0f / (float)size;
+    float* score = keys + a.experts + 4 * a.groups;
+    if (size % 4 == 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = 4 * (lane + L * c), g = (int)(((float)e + 0.5f) * inv);
+            if (e < a.experts) *(float4*)(keys + e + 4 * g) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * C; ++i) {
+            const int e = 4 * (lane + L * (i >> 2)) + (i & 3), g = (int)(((float)e + 0.5f) * inv);
+            if (e < a.experts) keys[e + 4 * g] = v[i];
+        }
+    }
+    wave_fence();
+    int share = 1;
+    while (2 * share * a.groups <= L) share *= 2;
+    for (int at = lane; at < a.groups * share; at += L) {
+        const int g = at / share, part = at & (share - 1);
+        const float none = -__builtin_inff();
+        float b1 = none, b2 = none;
+        for (int i = part; i < size; i += share) {
+            const float x = keys[g * (size + 4) + i];
+            const float k = x != x ? -FLT_MAX : x;         // NaN counts as the lowest value
+            b2 = fmaxf(b2, fminf(b1, k));
+            b1 = fmaxf(b1, k);
+        }
+        // (a group's lanes run the loop over `at` together)
+        for (int o = 1; o < share; o *= 2) {
+            const float p1 = __shfl_xor(b1, o), p2 = __shfl_xor(b2, o);
+            b2 = fmaxf(fminf(b1, p1), fmaxf(b2, p2));
+            b1 = fmaxf(b1, p1);
+        }
+        // a sum of two lowest values stays above the score of an empty group
+        if (part == 0) score[g] = a.group_best > 1 && b2 != none ? fmaxf(b1 + b2, -FLT_MAX) : b1;
+    }
+    wave_fence();
+    uint64_t kept = 0;
+    const int shift = (threadIdx.x & 63) & ~(L - 1);
+    for (int g0 = 0; g0 < a.groups; g0 += L) {
+        const int g = g0 + lane;
+        const float mine = score[min(g, a.groups - 1)];
+        int before = 0;
+        for (int h = 0; h < a.groups; ++h) {
+            const float s = score[h];
+            before += s > mine || (s == mine && h < g);
+        }
+        uint64_t m = __ballot(g < a.groups && before < a.top_groups) >> shift;
+        if constexpr (L < 64) m &= (1ull << L) - 1;
+        kept |= m << g0;
+    }
+    return kept;
+}
+
+// ---------------------------------------------------------------------------
+// The K largest keys of a row in order, K a power of two: every lane sorts its
+// own, then log2(L) times a lane and its partner keep the larger half of both
+// lists.  Of two descending lists a and b the K largest are max(a_i, b_K-1-i),
+// a bitonic list, which log2(K) rounds of exchanges put in order.  There are
+// no branches and no serial chain of K row maxima.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void exchange(double& a, double& b) {
+    const double x = MaxD()(a, b);
+    b = MinD()(a, b);
+    a = x;
+}
+template <int K>
+__device__ __forceinline__ void bitonic_merge(double* v) {
+#pragma unroll
+    for (int h = K / 2; h; h /= 2)
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (!(i & h)) exchange(v[i], v[i + h]);
+}
+// Descending order of K values by odd-even merges.
+template <int K>
+__device__ __forceinline__ void sort_down(double* v) {
+#pragma unroll
+    for (int p = 1; p < K; p *= 2)
+#pragma unroll
+        for (int q = p; q; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < K; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < K && (i + j) / (2 * p) == (i + j + q) / (2 * p)) exchange(v[i + j], v[i + j + q]);
+}
+template <int K, class From>
+__device__ __forceinline__ void keep_larger(double* v, From from) {
+    double o[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) o[i] = from(v[K - 1 - i]);
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = MaxD()(v[i], o[i]);
+    bitonic_merge<K>(v);
+}
+template <int K, int L, int N>
+__device__ __forceinline__ void row_largest(double* key, double* list) {
+    const double none = make_key(0u, MAX_EXPERTS - 1);     // below every key there is
+#pragma unroll
+    for (int i = 0; i < K; ++i) list[i] = i < N ? key[i] : none;
+    sort_down<(N < K ? N : K)>(list);
+#pragma unroll
+    for (int at = K; at < N; at += K) {
+        sort_down<K>(key + at);
+#pragma unroll
+        for (int i = 0; i < K; ++i) list[i] = MaxD()(list[i], key[at + K - 1 - i]);
+        bitonic_merge<K>(list);
+    }
+    keep_larger<K>(list, [](double d) { return dpp<DPP_XOR1>(d); });
+    keep_larger<K>(list, [](double d) { return dpp<DPP_XOR2>(d); });
+    keep_larger<K>(list, [](double d) { return dpp<DPP_HALF_MIRROR>(d); });
+    if constexpr (L >= 16) keep_larger<K>(list, [](double d) { return dpp<DPP_MIRROR>(d); });
+    if constexpr (L >= 32) keep_larger<K>(list, [](double d) { return __shfl_xor(d, 16); });
+    if constexpr (L >= 64) keep_larger<K>(list, [](double d) { return __shfl_xor(d, 32); });
+}
+
+// K = 8: five to eight experts by the merged lists; K = 0: any number, one row
+// maximum after the other.
+template <bool BF16, int L, int C, int K>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     constexpr int N = 4 * C, ROWS = 256 / L;
-    extern __shared__ float smem[];           // groups: keys, then the groups' scores and flags
+    extern __shared__ float4 smem[];
     const int lane = threadIdx.x & (L - 1), r = threadIdx.x / L;
     const int64_t row0 = (int64_t)blockIdx.x * ROWS + r;
     const bool live = row0 < a.tokens;
@@ -185,71 +340,52 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     float top = 0.0f, sum = 1.0f;
     if (softmax && (by_score || !a.renorm)) softmax_stats<L, N>(v, top, sum);
     if (by_score) {
+        const float inv = 1.0f / sum;
+        float b[N];
+        if (a.bias) {
+            load_row<false, L, C>(a.bias, 0, a.experts, a.vec_bias, lane, b);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) b[i] = 0.0f;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = 4 * (lane + L * (i >> 2)) + (i & 3);
-            const float s = softmax ? expf(v[i] - top) / sum : sigmoid(v[i]);
-            const float b = a.bias && e < a.experts ? a.bias[e] : 0.0f;
-            v[i] = v[i] == -__builtin_inff() ? v[i] : s + b;
+            const float s = softmax ? quick_exp(v[i] - top) * inv : quick_sigmoid(v[i]);
+            v[i] = v[i] == -__builtin_inff() ? v[i] : s + b[i];
         }
     }
     if (a.groups > 1) {
-        const int size = a.experts / a.groups;
-        // one spare word a group keeps the lanes that scan neighbouring groups on different banks
-        float* keys = smem + r * (a.experts + 3 * a.groups);
-        float* score = keys + a.experts + a.groups;
-        float* kept = score + a.groups;
+        const uint64_t kept = groups_kept<L, C>(a, (float*)smem + r * (a.experts + 5 * a.groups + 3 & ~3), lane, v);
+        const float inv = (float)a.groups / (float)a.experts;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int e = 4 * (lane + L * (i >> 2)) + (i & 3);
-            if (e < a.experts) keys[e + e / size] = v[i];
-        }
-        __syncthreads();
-        for (int g = lane; g < a.groups; g += L) {
-            double b1 = NOT_THERE, b2 = NOT_THERE;
-            for (int i = 0; i < size; ++i) {
-                const double d = pack_key(keys[g * (size + 1) + i], 0);
-                b2 = MaxD()(b2, fmin(b1, d));
-                b1 = MaxD()(b1, d);
-            }
-            const float none = -__builtin_inff();
-            // the packed index is below fp32's last place, so the keys come back whole
-            const float k1 = b1 == -0x1p129 ? __builtin_nanf("") : (float)b1;
-            const float k2 = b2 == -0x1p129 ? __builtin_nanf("") : (float)b2;
-            const float two = a.group_best > 1 && key_there(b2) ? k1 + k2 : k1;
-            // a sum of two lowest values stays above the score of an empty group
-            score[g] = !key_there(b1) ? none : two < -FLT_MAX ? -FLT_MAX : two;
-        }
-        __syncthreads();
-        for (int g = lane; g < a.groups; g += L) {
-            const double mine = pack_key(score[g], g);
-            int before = 0;
-            for (int h = 0; h < a.groups; ++h) before += pack_key(score[h], h) > mine;
-            kept[g] = before < a.top_groups ? 1.0f : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = 4 * (lane + L * (i >> 2)) + (i & 3);
-            if (e < a.experts && kept[e / size] == 0.0f) v[i] = -__builtin_inff();
+            const int e = 4 * (lane + L * (i >> 2)) + (i & 3), g = (int)(((float)e + 0.5f) * inv);
+            if (!(kept >> (g & 63) & 1)) v[i] = -__builtin_inff();
         }
     }
 
-    double key[N];
+    double key[N], mine = make_key(0u, 0);
 #pragma unroll
     for (int i = 0; i < N; ++i) key[i] = pack_key(v[i], 4 * (lane + L * (i >> 2)) + (i & 3));
-    double mine = NOT_THERE;
-    for (int j = 0; j < a.top_k; ++j) {
-        double m = key[0];
+    if constexpr (K > 0) {
+        double list[K];
+        row_largest<K, L, N>(key, list);
 #pragma unroll
-        for (int i = 1; i < N; ++i) m = MaxD()(m, key[i]);
-        m = row_reduce<L>(m, MaxD());
+        for (int j = 0; j < K; ++j) mine = lane == j ? list[j] : mine;
+    } else {
+        const double none = mine;
+        for (int j = 0; j < a.top_k; ++j) {
+            double m = key[0];
 #pragma unroll
-        for (int i = 0; i < N; ++i) key[i] = key[i] == m ? NOT_THERE : key[i];
-        mine = lane == j ? m : mine;
+            for (int i = 1; i < N; ++i) m = MaxD()(m, key[i]);
+            m = row_reduce<L>(m, MaxD());
+#pragma unroll
+            for (int i = 0; i < N; ++i) key[i] = key[i] == m ? none : key[i];
+            mine = lane == j ? m : mine;
+        }
     }
 
-    const bool there = key_there(mine);
+    const bool there = lane < a.top_k && key_there(mine);
     const int id = there ? key_index(mine) : -1;
     const float l = there ? load_logit<BF16>(a.logits, base + id) : 0.0f;
     float w;
@@ -307,6 +443,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
     const bool there = id >= 0 && id < a.experts;
     const float ds = there ? a.scale * a.dweights[row * a.top_k + lane] : 0.0f;
     const float l = there ? load_logit<BF16>(a.logits, base + id) : 0.0f;
+    const float inv = 1.0f / sum;
     float put = ds, dot = 0.0f;
     if (a.renorm) {
         float s;
@@ -331,10 +468,8 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
         const int e = 4 * (lane + L * c);
         if (dense) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float s = v[4 * c + i] == -__builtin_inff() ? 0.0f : expf(v[4 * c + i] - top) / sum;
-                o[i] = s * (o[i] - dot);
-            }
+            for (int i = 0; i < 4; ++i)
+                o[i] = v[4 * c + i] == -__builtin_inff() ? 0.0f : quick_exp(v[4 * c + i] - top) * inv * (o[i] - dot);
         }
         if (a.vec_out && e < a.experts) {
             if constexpr (BF16) {
@@ -368,6 +503,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024, PLAN_WAVES = PLAN_THREADS / 64;
 constexpr int PLAN_BINS = MAX_EXPERTS + 1;
+constexpr int PLAN_ALONE = 4;               // tiles that one workgroup sorts by itself
 
 struct PlanArgs {
     const int32_t* ids;
@@ -422,13 +558,24 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_scatter_kernel(PlanArgs a) 
     // the counts of all workgroups, and of those before this one: several
     // threads share a bin when there are fewer bins than threads
     const int share = max(1, PLAN_THREADS / bins);
-    for (int at = tid; at < bins * share; at += PLAN_THREADS) {
+    if (a.blocks <= 1)                        // one workgroup counts for itself
+        for (int64_t i = tid; i < a.assignments; i += PLAN_THREADS) atomicAdd(&total[plan_bin(a, i)], 1);
+    else for (int at = tid; at < bins * share; at += PLAN_THREADS) {
         const int e = at % bins;
         int all = 0, mine = 0;
-        for (int b = at / bins; b < a.blocks; b += share) {
-            const int n = a.counts[(int64_t)b * bins + e];
-            all += n;
-            if (b < (int)blockIdx.x) mine += n;
+        constexpr int AHEAD = 16;             // loads in flight: each takes an L2 round trip
+        for (int b0 = at / bins; b0 < a.blocks; b0 += AHEAD * share) {
+            int n[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int b = b0 + i * share;
+                n[i] = b < a.blocks ? a.counts[(int64_t)b * bins + e] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                all += n[i];
+                mine += b0 + i * share < (int)blockIdx.x ? n[i] : 0;
+            }
         }
         atomicAdd(&total[e], all);
         atomicAdd(&before[e], mine);
@@ -476,17 +623,21 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_scatter_kernel(PlanArgs a) 
     }
 }
 
+// Assignments of a workgroup: all, while one workgroup is done with them
+// before two launches would be; otherwise a tile, or as many as keep the
+// workgroups at 256.
 int64_t plan_chunk(int64_t assignments) {
-    // at most 256 workgroups, each a whole number of tiles
-    const int64_t tiles = ceil_div(assignments, PLAN_THREADS);
-    return PLAN_THREADS * (tiles <= 0 ? 1 : ceil_div(tiles, 256));
+    const int64_t tiles = max((int64_t)1, ceil_div(assignments, PLAN_THREADS));
+    return PLAN_THREADS * (tiles <= PLAN_ALONE ? tiles : ceil_div(tiles, 256));
 }
 
 template <bool B, int L, int C>
 void launch_route(const RouteArgs& a, hipStream_t s) {
     constexpr int ROWS = 256 / L;
-    const size_t lds = a.groups > 1 ? sizeof(float) * ROWS * (size_t)(a.experts + 3 * a.groups) : 0;
-    hipLaunchKernelGGL((route_kernel<B, L, C>), dim3((uint32_t)ceil_div(a.tokens, ROWS)), dim3(256), lds, s, a);
+    const size_t lds = a.groups > 1 ? sizeof(float) * ROWS * (size_t)((a.experts + 5 * a.groups + 3) & ~3) : 0;
+    const dim3 grid((uint32_t)ceil_div(a.tokens, ROWS));
+    if (a.top_k >= 5 && a.top_k <= 8) hipLaunchKernelGGL((route_kernel<B, L, C, 8>), grid, dim3(256), lds, s, a);
+    else hipLaunchKernelGGL((route_kernel<B, L, C, 0>), grid, dim3(256), lds, s, a);
 }
 template <bool B, int L, int C>
 void launch_route(const RouteBwdArgs& a, hipStream_t s) {
@@ -538,9 +689,10 @@ mx_status mx_route(const void* logits, mx_dtype lt, int64_t tokens, int32_t expe
     if (!aligned_to(logits, type_bytes(lt)) || !aligned_to(bias, 4) || !aligned_to(ids, 4) || !aligned_to(weights, 4))
         return MX_ERR_ALIGN;
     RouteArgs a{logits, tokens, logits_ld ? logits_ld : experts, experts, bias, score, groups, top_groups, group_best,
-                top_k, renorm != 0, scale, 0, ids, weights};
+                top_k, renorm != 0, scale, 0, 0, ids, weights};
     if (groups == top_groups) a.groups = 1;   // every group stays
     a.vec = experts % 4 == 0 && a.ld % 4 == 0 && aligned_to(logits, 4 * type_bytes(lt));
+    a.vec_bias = experts % 4 == 0 && aligned_to(bias, 16);
     (void)hipGetLastError();
     if (lt == MX_BF16) dispatch_route<true>(a, (hipStream_t)stream);
     else dispatch_route<false>(a, (hipStream_t)stream);
@@ -571,8 +723,8 @@ mx_status mx_route_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t 
 int64_t mx_route_plan_workspace(int64_t tokens, int32_t top_k, int32_t experts) {
     if (tokens < 0 || top_k < 1 || experts < 1 || experts > MAX_EXPERTS || tokens > (int64_t)INT32_MAX / top_k)
         return 0;
-    const int64_t n = tokens * top_k;
-    return 4 * ceil_div(n, plan_chunk(n)) * (experts + 1);
+    const int64_t n = tokens * top_k, blocks = ceil_div(n, plan_chunk(n));
+    return blocks <= 1 ? 0 : 4 * blocks * (experts + 1);
 }
 
 mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t* offsets,
@@ -581,15 +733,15 @@ mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32
     if (tokens > (int64_t)INT32_MAX / top_k) return MX_ERR_SHAPE;
     if (!offsets) return MX_ERR_NULL;
     const int64_t n = tokens * top_k;
-    if (n > 0 && (!ids || !row_index || !slot || !workspace)) return MX_ERR_NULL;
+    const int64_t chunk = plan_chunk(n), blocks = ceil_div(n, chunk);
+    if (n > 0 && (!ids || !row_index || !slot || (blocks > 1 && !workspace))) return MX_ERR_NULL;
     if (!aligned_to(ids, 4) || !aligned_to(offsets, 4) || !aligned_to(row_index, 4) || !aligned_to(slot, 4) ||
         !aligned_to(workspace, 4))
         return MX_ERR_ALIGN;
-    const int64_t chunk = plan_chunk(n);
-    PlanArgs a{ids, n, top_k, experts, chunk, (int)ceil_div(n, chunk), (int32_t*)workspace, offsets, row_index, slot};
+    PlanArgs a{ids, n, top_k, experts, chunk, (int)blocks, (int32_t*)workspace, offsets, row_index, slot};
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (n > 0) hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(PLAN_THREADS), 0, s, a);
+    if (blocks > 1) hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(PLAN_THREADS), 0, s, a);
     // with nothing to sort one workgroup writes the offsets, all 0
     hipLaunchKernelGGL(plan_scatter_kernel, dim3(max(a.blocks, 1)), dim3(PLAN_THREADS), 0, s, a);
     return launch_status();

@@ -7,6 +7,7 @@ or a GPU is missing, calls raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -111,7 +112,10 @@ def _ptr(t):
 
 
 def _stream():
-    return _torch().cuda.current_stream().cuda_stream
+    # the current device's current stream as a handle; building a
+    # torch.cuda.Stream for it would take ten times as long
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype_code(t):
@@ -619,7 +623,7 @@ def _workspace(t, need, device):
     """A uint8 device buffer of at least `need` bytes."""
     torch = _torch()
     if t is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return None if need == 0 else torch.empty(need, dtype=torch.uint8, device=device)
     if t.dtype != torch.uint8 or t.numel() < need:
         raise ValueError("workspace must be uint8 of at least %d bytes" % need)
     return _dev(t, "workspace")
@@ -685,12 +689,17 @@ def combine_bwd(dout, y, slot, weights=None, used_rows=None, dy=None, dweights=N
 def _grad_list(grads, name):
     """The host arrays of a gradient list (any shapes, contiguous, fp32 and
     bf16 mixed)."""
+    torch = _torch()
+    codes = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}
     grads = list(grads)
-    n = len(grads)
-    types = (ctypes.c_int * n)(*[_dtype_code(g) for g in grads])
-    numels = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    ptrs = (ctypes.c_void_p * n)(*[_dev(g, name).data_ptr() for g in grads])
-    return grads, n, types, numels, ptrs
+    if not all([g.is_cuda and g.is_contiguous() for g in grads]):
+        raise ValueError("%s must be contiguous device tensors" % name)
+    try:
+        types = array.array("i", [codes[g.dtype] for g in grads])
+    except KeyError as e:
+        raise TypeError("%s: expected float32 or bfloat16, got %s" % (name, e.args[0])) from None
+    return (grads, types, array.array("q", [g.numel() for g in grads]),
+            array.array("Q", [g.data_ptr() for g in grads]))
 
 
 def grad_norm(grads, norm=None, workspace=None):
@@ -710,20 +719,22 @@ def grad_clip(grads, max_norm: float, outs=None, norm=None, workspace=None):
 
 def _grad_call(fn, grads, outs, max_norm, norm, workspace):
     torch = _torch()
-    grads, n, types, numels, ptrs = _grad_list(grads, "grads")
+    grads, types, numels, ptrs = _grad_list(grads, "grads")
+    n, outs_at = len(grads), None
     if outs is not None:
-        outs, m, out_types, out_numels, out_ptrs = _grad_list(outs, "outs")
-        if m != n or out_types[:] != types[:] or any(g.shape != o.shape for g, o in zip(grads, outs)):
+        outs, out_types, _, out_ptrs = _grad_list(outs, "outs")
+        if out_types != types or [g.shape for g in grads] != [o.shape for o in outs]:
             raise ValueError("outs must match grads in number, types and shapes")
+        outs_at = out_ptrs.buffer_info()[0]
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
     else:
         _shaped(norm, (), torch.float32, "norm")
     workspace = _workspace(workspace, lib().mx_grad_workspace(n), norm.device)
+    head = (ptrs.buffer_info()[0], types.buffer_info()[0], numels.buffer_info()[0], n)
     if fn == "mx_grad_norm":
-        code = lib().mx_grad_norm(ptrs, types, numels, n, _ptr(workspace), _ptr(norm), _stream())
+        code = lib().mx_grad_norm(*head, _ptr(workspace), _ptr(norm), _stream())
     else:
-        code = lib().mx_grad_clip(ptrs, types, numels, n, out_ptrs if outs is not None else None, max_norm,
-                                  _ptr(workspace), _ptr(norm), _stream())
+        code = lib().mx_grad_clip(*head, outs_at, max_norm, _ptr(workspace), _ptr(norm), _stream())
     _check(fn, code)
     return norm

@@ -44,10 +44,10 @@ def group_scores(key, groups, group_best):
     out = np.full(groups, -np.inf)
     size = len(key) // groups
     for g in range(groups):
-        k = key[g * size:(g + 1) * size]
-        best = [k[i] for i in _order(k) if not np.isneginf(k[i])][:group_best]
-        if best:
-            out[g] = max(sum(best), -float(np.finfo(np.float32).max)) if not np.isnan(sum(best)) else np.nan
+        low = -float(np.finfo(np.float32).max)             # NaN counts as the lowest value
+        k = [low if np.isnan(x) else x for x in key[g * size:(g + 1) * size] if not np.isneginf(x)]
+        if k:
+            out[g] = max(sum(sorted(k)[-group_best:]), low)
     return out
 
 

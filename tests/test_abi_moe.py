@@ -62,14 +62,14 @@ def test_route_bwd_validation(L):
 
 
 def test_route_plan_validation(L):
-    call = caller(L.mx_route_plan, ids=FAKE, t=4, k=4, e=32, off=FAKE, row=FAKE, slot=FAKE, ws=FAKE, s=None)
+    call = caller(L.mx_route_plan, ids=FAKE, t=65536, k=4, e=32, off=FAKE, row=FAKE, slot=FAKE, ws=FAKE, s=None)
     for bad in (dict(t=-1), dict(k=0), dict(e=0), dict(e=1025), dict(t=2 ** 30, k=2)):
         assert call(**bad) == SHAPE, bad
     for name in ("ids", "off", "row", "slot", "ws"):
         assert call(**{name: None}) == NULL and call(**{name: FAKE + 2}) == ALIGN
     assert call(t=0, off=None) == NULL
     ws = L.mx_route_plan_workspace
-    assert ws(0, 4, 32) == 0 and ws(4, 4, 32) >= 0 and ws(65536, 8, 256) >= 0
+    assert ws(0, 4, 32) == 0 and ws(4, 4, 32) >= 0 and ws(65536, 4, 32) > 0 and ws(65536, 8, 256) > 0
     for bad in ((-1, 4, 32), (4, 0, 32), (4, 4, 0), (4, 4, 1025), (2 ** 30, 2, 32)):
         assert ws(*bad) == 0
 

@@ -320,4 +320,5 @@ def test_refusals():
     with pytest.raises(mx.MXError):
         mx.route_plan(ids, 1025)
     with pytest.raises(ValueError):
-        mx.route_plan(ids, 32, workspace=tt.zeros(8, dtype=tt.uint8, device="cuda"))
+        mx.route_plan(tt.zeros((65536, 2), dtype=tt.int32, device="cuda"), 32,
+                      workspace=tt.zeros(8, dtype=tt.uint8, device="cuda"))
