@@ -406,7 +406,7 @@ mx_status mx_grouped_gemm_q(const uint8_t* a_codes, int64_t a_ld, const uint8_t*
  *   - Groups: the experts form `groups` groups of experts / groups
  *     consecutive ones.  A group's score is its best key (group_best = 1) or
  *     the sum of its two best (2; of one, if only one is available), rounded
- *     to fp32 and no lower than its lowest value, which NaN counts as.
+ *     to fp32 and no lower than its lowest value; a NaN key adds nothing.
  *     Experts outside the top_groups best groups are not chosen.
  *     groups = 1: no such limit.
  *   - ids [tokens x top_k] int32: the chosen experts, best first; of equal
@@ -470,8 +470,7 @@ mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32
  * 1 (the gradient of the gather of tokens into grouped order).  residual
  * [tokens x cols] of out's type, or NULL; it may be out itself.  out
  * [tokens x cols], ot fp32 or bf16 whatever y's type.
- * Any cols >= 1 and any pitch; rows that start at 16-byte boundaries and hold
- * whole 16-byte pieces are read fastest.  rows <= 2^31 - 1, tokens * top_k <
+ * Any cols >= 1 and any pitch; rows <= 2^31 - 1, tokens * top_k <
  * 2^31.  Device pointers owned by the caller, aligned to their elements.
  * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
  * MX_ERR_LAUNCH.  tokens == 0 launches nothing. */

@@ -22,93 +22,160 @@ struct CombineArgs {
     int64_t res_ld;
     void* out;
     int64_t out_ld;
-    int chunks;               // waves that share a row
+    int64_t chunks;           // waves that share a row
 };
 
-// V consecutive elements of a row as fp32.  VEC: one aligned load (16 bytes
-// at the most); otherwise element by element, those past the end 0.
-template <bool BF16, int V, bool VEC>
-__device__ __forceinline__ void load_v(const void* p, int64_t at, int64_t left, float* f) {
-    if constexpr (VEC) {
-        if constexpr (BF16 && V == 8) {
-            const uint4 w = *(const uint4*)((const uint16_t*)p + at);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[2 * i] = bf16lo(u[i]);
-                f[2 * i + 1] = bf16hi(u[i]);
-            }
-        } else if constexpr (BF16) {
-            const uint2 w = *(const uint2*)((const uint16_t*)p + at);
-            f[0] = bf16lo(w.x); f[1] = bf16hi(w.x);
-            f[2] = bf16lo(w.y); f[3] = bf16hi(w.y);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                const float4 w = *(const float4*)((const float*)p + at + i);
-                f[i] = w.x; f[i + 1] = w.y; f[i + 2] = w.z; f[i + 3] = w.w;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            f[i] = 0.0f;
-            if (i < left)
-                f[i] = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[at + i] << 16) : ((const float*)p)[at + i];
-        }
-    }
+// Pieces of 8 and 16 bytes at any element's address: global memory takes them
+// at any alignment, so rows need none beyond their elements'.
+typedef unsigned int u32x2v __attribute__((ext_vector_type(2), aligned(2)));
+typedef unsigned int u32x4v __attribute__((ext_vector_type(4), aligned(2)));
+
+// STREAM: the accesses bypass what the caches hold (non-temporal).
+template <bool STREAM, class T>
+__device__ __forceinline__ T load_piece(const void* p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load((const T*)p);
+    else return *(const T*)p;
+}
+template <bool STREAM, class T>
+__device__ __forceinline__ void store_piece(void* p, T v) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, (T*)p);
+    else *(T*)p = v;
 }
 
-template <bool BF16, int V, bool VEC>
-__device__ __forceinline__ void store_v(void* p, int64_t at, int64_t left, const float* f) {
-    if constexpr (VEC) {
-        if constexpr (BF16) {
-            uint32_t u[V / 2];
+// V consecutive elements of a row, as they are in memory.
+template <bool BF16, int V>
+struct Piece {
+    uint32_t u[BF16 ? V / 2 : V];
+
+    // Without FULL the row ends after `left` of them (then element by element,
+    // and 0 past it).
+    template <bool FULL, bool STREAM>
+    __device__ __forceinline__ void load(const void* p, int64_t at, int64_t left) {
+        constexpr int W = BF16 ? V / 2 : V;
+        const char* q = (const char*)p + at * (BF16 ? 2 : 4);
+        if constexpr (!FULL) {
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) u[i] = f32_to_bf16_rne(f[2 * i]) | f32_to_bf16_rne(f[2 * i + 1]) << 16;
-            if constexpr (V == 8) *(uint4*)((uint16_t*)p + at) = make_uint4(u[0], u[1], u[2], u[3]);
-            else *(uint2*)((uint16_t*)p + at) = make_uint2(u[0], u[1]);
+            for (int i = 0; i < W; ++i) u[i] = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (i >= left) continue;
+                if constexpr (BF16) u[i / 2] |= (uint32_t)((const uint16_t*)q)[i] << (i % 2 * 16);
+                else u[i] = ((const uint32_t*)q)[i];
+            }
+        } else if constexpr (W == 2) {
+            const u32x2v w = load_piece<STREAM, u32x2v>(q);
+            u[0] = w.x; u[1] = w.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < V; i += 4)
-                *(float4*)((float*)p + at + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+            for (int i = 0; i < W; i += 4) {
+                const u32x4v w = load_piece<STREAM, u32x4v>(q + 4 * i);
+                u[i] = w.x; u[i + 1] = w.y; u[i + 2] = w.z; u[i + 3] = w.w;
+            }
         }
-    } else {
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (BF16) return i % 2 ? bf16hi(u[i / 2]) : bf16lo(u[i / 2]);
+        else return __uint_as_float(u[i]);
+    }
+};
+
+template <bool BF16, int V, bool FULL, bool STREAM>
+__device__ __forceinline__ void store_v(void* p, int64_t at, int64_t left, const float* f) {
+    if constexpr (!FULL) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (i >= left) continue;
             if constexpr (BF16) ((uint16_t*)p)[at + i] = (uint16_t)f32_to_bf16_rne(f[i]);
             else ((float*)p)[at + i] = f[i];
         }
+    } else if constexpr (BF16) {
+        uint32_t u[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) u[i] = f32_to_bf16_rne(f[2 * i]) | f32_to_bf16_rne(f[2 * i + 1]) << 16;
+        if constexpr (V == 8) store_piece<STREAM>((uint16_t*)p + at, (u32x4v){u[0], u[1], u[2], u[3]});
+        else store_piece<STREAM>((uint16_t*)p + at, (u32x2v){u[0], u[1]});
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            store_piece<STREAM>((float*)p + at + i, (u32x4v){__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
+                                                             __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3])});
     }
 }
 
-// One wave: 64 V columns of one token.
-template <bool YB, bool OB, bool VEC>
+// Up to FLIGHT assignments of a token, whose rows are read at once.  Each lane
+// fetches one, and they are handed round as scalars, so that all are there
+// after one round trip; the loads of the rows are then issued without waiting
+// for each other, and widened only when all are under way.
+constexpr int FLIGHT = 4;
+
+struct Flight {
+    int slot[FLIGHT];
+    float weight[FLIGHT];
+
+    // those from j0 on; a slot outside [0, rows) becomes -1
+    __device__ __forceinline__ void load(const int32_t* slots, const float* weights, int64_t t, int top_k, int j0,
+                                         int64_t rows) {
+        const int j = j0 + (threadIdx.x & (FLIGHT - 1));
+        const bool in = j < top_k;
+        int s = in ? slots[t * top_k + j] : -1;
+        const float w = in && weights ? weights[t * top_k + j] : 1.0f;
+        s = s < rows ? s : -1;
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) {
+            slot[i] = __builtin_amdgcn_readlane(s, i);
+            weight[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), i));
+        }
+    }
+};
+
+// out[t] = residual[t] + sum_j w_tj y[slot_tj].  Bound by memory: each row of
+// y is read once, each token written once.
+// One wave: 64 V columns of one token; a row's waves follow one another, so
+// the waves of a workgroup read neighbouring pieces of the same rows.  One
+// wave for a whole token was slower (117 against 107 us at the size below).
+// 16384 tokens of 4 rows, 2880 bf16 columns, with a residual: 83-86 us, 6.6 to
+// 6.8 TB/s (a copy of that size: 5.5).
+template <bool YB, bool OB, bool STREAM, bool FULL>
+__device__ __forceinline__ void combine_piece(const CombineArgs& a, int64_t t, int64_t col, Flight& n) {
+    constexpr int V = YB ? 8 : 4;
+    const int64_t left = a.cols - col;
+    float acc[V];
+    Piece<OB, V> r;
+    if (a.residual) r.template load<FULL, false>(a.residual, t * a.res_ld + col, left);
+    for (int j0 = 0;;) {
+        Piece<YB, V> f[FLIGHT];
+#pragma unroll
+        for (int j = 0; j < FLIGHT; ++j)
+            if (n.slot[j] >= 0) f[j].template load<FULL, STREAM>(a.y, n.slot[j] * a.y_ld + col, left);
+        if (j0 == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = a.residual ? r[i] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < FLIGHT; ++j) {
+            if (n.slot[j] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(n.weight[j], f[j][i], acc[i]);
+        }
+        j0 += FLIGHT;
+        if (j0 >= a.top_k) break;
+        n.load(a.slot, a.weights, t, a.top_k, j0, a.rows);
+    }
+    store_v<OB, V, FULL, STREAM>(a.out, t * a.out_ld + col, left, acc);
+}
+
+template <bool YB, bool OB, bool STREAM>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     constexpr int V = YB ? 8 : 4;
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t t = w / a.chunks;
+    if (t >= a.tokens) return;
+    Flight n;
+    n.load(a.slot, a.weights, t, a.top_k, 0, a.rows);
     const int64_t col = (w % a.chunks * 64 + (threadIdx.x & 63)) * V;
-    if (t >= a.tokens || col >= a.cols) return;
-    const int64_t left = a.cols - col;
-    float acc[V];
-    if (a.residual) {
-        load_v<OB, V, VEC>(a.residual, t * a.res_ld + col, left, acc);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    }
-    for (int j = 0; j < a.top_k; ++j) {
-        const int64_t s = a.slot[t * a.top_k + j];
-        if (s < 0 || s >= a.rows) continue;
-        const float wt = a.weights ? a.weights[t * a.top_k + j] : 1.0f;
-        float f[V];
-        load_v<YB, V, VEC>(a.y, s * a.y_ld + col, left, f);
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(wt, f[i], acc[i]);
-    }
-    store_v<OB, V, VEC>(a.out, t * a.out_ld + col, left, acc);
+    if (col >= a.cols) return;
+    if (a.cols - col >= V) combine_piece<YB, OB, STREAM, true>(a, t, col, n);
+    else combine_piece<YB, OB, STREAM, false>(a, t, col, n);
 }
 
 struct CombineBwdArgs {
@@ -126,51 +193,86 @@ struct CombineBwdArgs {
     float* dweights;
 };
 
-// One workgroup of two waves: one token.  Beyond the tokens the workgroups
-// clear the rows of dy past the used ones.
-constexpr int BWD_THREADS = 128;
+// dy[slot_tj] = w_tj dout[t] and dw_tj = <dout[t], y[slot_tj]> from one read of
+// dout and y.  Bound by memory.
+// One workgroup: one token, its waves side by side along the columns, at most
+// MAX_WAVES of them (one wave a token: 154 us at the size below, two 149, four
+// 146).  Beyond the tokens the workgroups clear the rows of dy past the used
+// ones.  16384 tokens of 4 rows, 2880 bf16 columns: 147 us, 5.8 TB/s.
+constexpr int MAX_WAVES = 4;
 
-template <bool DB, bool YB, bool VEC>
-__global__ __launch_bounds__(BWD_THREADS) void combine_bwd_kernel(CombineBwdArgs a) {
+template <bool DB, bool YB, bool STREAM, bool FULL>
+__device__ __forceinline__ void bwd_piece(const CombineBwdArgs& a, int64_t t, int64_t col, const Flight& n,
+                                          float* dot) {
     constexpr int V = YB ? 8 : 4;
-    __shared__ float part[BWD_THREADS / 64];
-    const int tid = threadIdx.x;
+    const int64_t left = a.cols - col;
+    Piece<DB, V> d;
+    Piece<YB, V> f[FLIGHT];
+    d.template load<FULL, false>(a.dout, t * a.dout_ld + col, left);
+    if (a.dweights) {
+#pragma unroll
+        for (int j = 0; j < FLIGHT; ++j)
+            if (n.slot[j] >= 0) f[j].template load<FULL, STREAM>(a.y, n.slot[j] * a.y_ld + col, left);
+    }
+    float g[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = d[i];
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j) {
+        if (n.slot[j] < 0) continue;
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = n.weight[j] * g[i];
+        store_v<YB, V, FULL, STREAM>(a.dy, n.slot[j] * a.dy_ld + col, left, v);
+    }
+    if (a.dweights) {
+#pragma unroll
+        for (int j = 0; j < FLIGHT; ++j) {
+            if (n.slot[j] < 0) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(g[i], f[j][i], dot[j]);
+        }
+    }
+}
+
+template <bool DB, bool YB, bool STREAM>
+__global__ __launch_bounds__(64 * MAX_WAVES) void combine_bwd_kernel(CombineBwdArgs a) {
+    constexpr int V = YB ? 8 : 4;
+    __shared__ float part[MAX_WAVES][FLIGHT];
+    const int tid = threadIdx.x, threads = blockDim.x;
     const int64_t used = a.used_rows ? min(max((int64_t)*a.used_rows, (int64_t)0), a.rows) : a.rows;
     if ((int64_t)blockIdx.x >= a.tokens) {
         const float zero[V] = {};
         for (int64_t r = used + blockIdx.x - a.tokens; r < a.rows; r += gridDim.x - a.tokens)
-            for (int64_t col = tid * V; col < a.cols; col += BWD_THREADS * V)
-                store_v<YB, V, VEC>(a.dy, r * a.dy_ld + col, a.cols - col, zero);
+            for (int64_t col = tid * V; col < a.cols; col += threads * V) {
+                if (a.cols - col >= V) store_v<YB, V, true, STREAM>(a.dy, r * a.dy_ld + col, V, zero);
+                else store_v<YB, V, false, STREAM>(a.dy, r * a.dy_ld + col, a.cols - col, zero);
+            }
         return;
     }
     const int64_t t = blockIdx.x;
-    for (int j = 0; j < a.top_k; ++j) {
-        const int64_t s = a.slot[t * a.top_k + j];
-        const bool there = s >= 0 && s < used;
-        float dot = 0.0f;
-        if (there) {
-            const float wt = a.weights ? a.weights[t * a.top_k + j] : 1.0f;
-            for (int64_t col = tid * V; col < a.cols; col += BWD_THREADS * V) {
-                const int64_t left = a.cols - col;
-                float g[V], f[V];
-                load_v<DB, V, VEC>(a.dout, t * a.dout_ld + col, left, g);
-                if (a.dweights) {
-                    load_v<YB, V, VEC>(a.y, s * a.y_ld + col, left, f);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) dot = __builtin_fmaf(g[i], f[i], dot);
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = wt * g[i];
-                store_v<YB, V, VEC>(a.dy, s * a.dy_ld + col, left, f);
-            }
-        }
+    for (int j0 = 0; j0 < a.top_k; j0 += FLIGHT) {
+        Flight n;
+        n.load(a.slot, a.weights, t, a.top_k, j0, used);
+        float dot[FLIGHT] = {};
+        int64_t col = tid * V;
+        for (; col <= a.cols - V; col += threads * V) bwd_piece<DB, YB, STREAM, true>(a, t, col, n, dot);
+        if (col < a.cols) bwd_piece<DB, YB, STREAM, false>(a, t, col, n, dot);
         if (!a.dweights) continue;
 #pragma unroll
-        for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
+        for (int j = 0; j < FLIGHT; ++j)
+#pragma unroll
+            for (int d = 32; d; d >>= 1) dot[j] += __shfl_xor(dot[j], d);
         __syncthreads();
-        if ((tid & 63) == 0) part[tid >> 6] = dot;
+        if ((tid & 63) == 0)
+#pragma unroll
+            for (int j = 0; j < FLIGHT; ++j) part[tid >> 6][j] = dot[j];
         __syncthreads();
-        if (tid == 0) a.dweights[t * a.top_k + j] = there ? part[0] + part[1] : 0.0f;
+        if (tid < FLIGHT && j0 + tid < a.top_k) {
+            float sum = 0.0f;
+            for (int w = 0; w < threads / 64; ++w) sum += part[w][tid];
+            a.dweights[t * a.top_k + j0 + tid] = sum;
+        }
     }
 }
 
@@ -183,10 +285,14 @@ mx_status check_combine(mx_dtype yt, mx_dtype ot, int64_t rows, int64_t cols, in
     return MX_OK;
 }
 
-// Rows that start at whole 16-byte (or, for the narrower of two types, 8-byte)
-// pieces and hold a whole number of them.
-bool vector_rows(const void* p, mx_dtype t, int64_t ld, int v) {
-    return ld % v == 0 && aligned_to(p, v * type_bytes(t));
+// Whether the experts' rows are more than half of the 256 MB Infinity Cache:
+// the rows and the output then bypass the caches, which could not keep them
+// for a neighbouring call.  Measured on bf16 rows of 2880, 4 a token, cached /
+// bypassing: forward 10.7 / 11.4 us at 47 MB of rows, 19.6 / 20.6 at 94,
+// 31.6 / 29.5 at 142, 107 / 86 at 377; gradient 19.8 / 21.9, 37.4 / 39.5,
+// 55.9 / 56.0, 163 / 147.
+bool streams(int64_t rows, int64_t cols, mx_dtype yt) {
+    return (double)rows * (double)cols * (double)type_bytes(yt) > 128e6;
 }
 
 }  // namespace
@@ -207,18 +313,17 @@ mx_status mx_combine(const void* y, mx_dtype yt, int64_t rows, int64_t cols, int
     CombineArgs a{y, rows, cols, y_ld ? y_ld : cols, slot, weights, tokens, top_k, residual,
                   residual_ld ? residual_ld : cols, out, out_ld ? out_ld : cols, 0};
     const int v = yt == MX_BF16 ? 8 : 4;
-    if (cols > (int64_t)INT32_MAX * 64) return MX_ERR_SHAPE;
-    a.chunks = (int)ceil_div(cols, 64 * v);
-    const int64_t blocks = ceil_div(tokens * a.chunks, 4);
-    if (blocks > ((int64_t)1 << 24) - 1) return MX_ERR_SHAPE;
-    const bool vec = cols % v == 0 && vector_rows(y, yt, a.y_ld, v) && vector_rows(out, ot, a.out_ld, v) &&
-                     (!residual || vector_rows(residual, ot, a.res_ld, v));
+    if (tokens > ((int64_t)1 << 24)) return MX_ERR_SHAPE;
+    a.chunks = ceil_div(cols, 64 * v);
+    if (a.chunks > ((int64_t)1 << 25) / tokens) return MX_ERR_SHAPE;
+    const dim3 grid((uint32_t)ceil_div(tokens * a.chunks, 4));
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-#define MX_COMBINE(YB, OB)                                                                                    \
-    do {                                                                                                      \
-        if (vec) hipLaunchKernelGGL((combine_kernel<YB, OB, true>), dim3((uint32_t)blocks), dim3(256), 0, s, a);   \
-        else hipLaunchKernelGGL((combine_kernel<YB, OB, false>), dim3((uint32_t)blocks), dim3(256), 0, s, a);      \
+    const bool through = streams(tokens * top_k, cols, yt);
+#define MX_COMBINE(YB, OB)                                                                                  \
+    do {                                                                                                    \
+        if (through) hipLaunchKernelGGL((combine_kernel<YB, OB, true>), grid, dim3(256), 0, s, a);          \
+        else hipLaunchKernelGGL((combine_kernel<YB, OB, false>), grid, dim3(256), 0, s, a);                 \
     } while (0)
     if (yt == MX_BF16) {
         if (ot == MX_BF16) MX_COMBINE(true, true);
@@ -248,16 +353,17 @@ mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const v
     const int v = yt == MX_BF16 ? 8 : 4;
     const int64_t clear = used_rows && rows > 0 ? min(rows, (int64_t)1024) : 0;
     if (tokens + clear == 0) return MX_OK;
-    if (tokens + clear > ((int64_t)1 << 24)) return MX_ERR_SHAPE;
-    const bool vec = cols % v == 0 && vector_rows(dout, dt, a.dout_ld, v) && vector_rows(dy, yt, a.dy_ld, v) &&
-                     (!dweights || vector_rows(y, yt, a.y_ld, v));
-    const dim3 grid((uint32_t)(tokens + clear));
+    if (tokens + clear >= ((int64_t)1 << 23)) return MX_ERR_SHAPE;     // 512 threads a workgroup at most
+    // as few passes over the columns as MAX_WAVES waves allow, and as few waves as these passes need
+    const int64_t chunks = ceil_div(cols, 64 * v), waves = ceil_div(chunks, ceil_div(chunks, MAX_WAVES));
+    const dim3 grid((uint32_t)(tokens + clear)), block((uint32_t)(64 * waves));
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-#define MX_COMBINE_BWD(DB, YB)                                                                                  \
-    do {                                                                                                        \
-        if (vec) hipLaunchKernelGGL((combine_bwd_kernel<DB, YB, true>), grid, dim3(BWD_THREADS), 0, s, a);      \
-        else hipLaunchKernelGGL((combine_bwd_kernel<DB, YB, false>), grid, dim3(BWD_THREADS), 0, s, a);         \
+    const bool through = streams(tokens * top_k, cols, yt);
+#define MX_COMBINE_BWD(DB, YB)                                                                              \
+    do {                                                                                                    \
+        if (through) hipLaunchKernelGGL((combine_bwd_kernel<DB, YB, true>), grid, block, 0, s, a);          \
+        else hipLaunchKernelGGL((combine_bwd_kernel<DB, YB, false>), grid, block, 0, s, a);                 \
     } while (0)
     if (dt == MX_BF16) {
         if (yt == MX_BF16) MX_COMBINE_BWD(true, true);

@@ -14,8 +14,9 @@ using namespace mx;
 // Tensors of one launch: their table travels in the kernel's arguments (no
 // copy to the device, nothing kept between calls).
 constexpr int TABLE = 96;
-constexpr int CHUNK_BYTES = 64 * 1024;      // of one tensor, a workgroup's unit of work
 constexpr int THREADS = 256;
+constexpr int FLIGHT = 4;                   // 16-byte pieces a thread reads at once
+constexpr int CHUNK_BYTES = 16 * THREADS * FLIGHT;      // of one tensor, a workgroup's unit of work
 constexpr int MAX_PARTIALS = 2048;          // workgroups of a launch
 
 struct GradTable {
@@ -67,21 +68,27 @@ __global__ __launch_bounds__(THREADS) void square_kernel(GradTable g, int chunks
         const int64_t begin = (int64_t)(c - g.first[t]) * per, n = min(per, g.numel[t] - begin);
         const int v = bf ? 8 : 4;
         const char* p = (const char*)g.src[t] + begin * (bf ? 2 : 4);
-        const int64_t whole = ((uintptr_t)p & 15) ? 0 : n / v;
-        for (int64_t i = threadIdx.x; i < whole; i += THREADS) {
-            const uint4 w = ((const uint4*)p)[i];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const int whole = ((uintptr_t)p & 15) ? 0 : (int)(n / v);
+        uint4 w[FLIGHT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < FLIGHT; ++k) {
+            const int i = k * THREADS + (int)threadIdx.x;
+            w[k] = i < whole ? ((const uint4*)p)[i] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < FLIGHT; ++k) {
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
                 if (bf) {
-                    add_square(s, bf16lo(u[k]));
-                    add_square(s, bf16hi(u[k]));
+                    add_square(s, bf16lo(u[m]));
+                    add_square(s, bf16hi(u[m]));
                 } else {
-                    add_square(s, __uint_as_float(u[k]));
+                    add_square(s, __uint_as_float(u[m]));
                 }
             }
         }
-        for (int64_t i = whole * v + threadIdx.x; i < n; i += THREADS)
+        for (int64_t i = (int64_t)whole * v + threadIdx.x; i < n; i += THREADS)
             add_square(s, bf ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i]);
     }
     s = block_sum<THREADS>(s);
@@ -106,7 +113,8 @@ __global__ __launch_bounds__(THREADS) void scale_kernel(GradTable g, int chunks,
     const double ratio = (double)max_norm / (total + 1e-6);
     // a norm that is not finite leaves the gradients as they are
     const float coef = total - total == 0.0 && ratio < 1.0 ? (float)ratio : 1.0f;
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    // from the end back: what the norm pass read last is still in the cache
+    for (int c = chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         const int t = tensor_of(g, c);
         if (coef == 1.0f && g.src[t] == g.dst[t]) continue;
         const bool bf = (g.bf16[t >> 5] >> (t & 31)) & 1;
@@ -116,17 +124,25 @@ __global__ __launch_bounds__(THREADS) void scale_kernel(GradTable g, int chunks,
         const int v = bf ? 8 : 4;
         const char* p = (const char*)g.src[t] + begin * size;
         char* q = (char*)g.dst[t] + begin * size;
-        const int64_t whole = (((uintptr_t)p | (uintptr_t)q) & 15) ? 0 : n_el / v;
-        for (int64_t i = threadIdx.x; i < whole; i += THREADS) {
-            const uint4 w = ((const uint4*)p)[i];
-            uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const int whole = (((uintptr_t)p | (uintptr_t)q) & 15) ? 0 : (int)(n_el / v);
+        uint4 w[FLIGHT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                u[k] = bf ? f32_to_bf16_rne(coef * bf16lo(u[k])) | f32_to_bf16_rne(coef * bf16hi(u[k])) << 16
-                          : __float_as_uint(coef * __uint_as_float(u[k]));
+        for (int k = 0; k < FLIGHT; ++k) {
+            const int i = k * THREADS + (int)threadIdx.x;
+            if (i < whole) w[k] = ((const uint4*)p)[i];
+        }
+#pragma unroll
+        for (int k = 0; k < FLIGHT; ++k) {
+            const int i = k * THREADS + (int)threadIdx.x;
+            if (i >= whole) continue;
+            uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                u[m] = bf ? f32_to_bf16_rne(coef * bf16lo(u[m])) | f32_to_bf16_rne(coef * bf16hi(u[m])) << 16
+                          : __float_as_uint(coef * __uint_as_float(u[m]));
             ((uint4*)q)[i] = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        for (int64_t i = whole * v + threadIdx.x; i < n_el; i += THREADS) {
+        for (int64_t i = (int64_t)whole * v + threadIdx.x; i < n_el; i += THREADS) {
             if (bf) ((uint16_t*)q)[i] = (uint16_t)f32_to_bf16_rne(coef * __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16));
             else ((float*)q)[i] = coef * ((const float*)p)[i];
         }

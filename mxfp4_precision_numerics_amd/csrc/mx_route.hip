@@ -194,28 +194,42 @@ __device__ __forceinline__ float renormalised(float l, bool there, bool softmax,
 // lanes scanning neighbouring groups meet different banks; 2^n lanes share the
 // scan of a group, as many as there are.  A group's place is the number of
 // groups before it.  Rows lie within a wave, so its own order is enough.
+// QUADS: groups are whole chunks of four experts.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
 
-template <int L, int C>
-__device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, float* keys, int lane, const float* v) {
+// The two best of (b1 >= b2) and x: the median of the three is the new second.
+// A NaN x changes neither.
+__device__ __forceinline__ void best_two(float& b1, float& b2, float x) {
+    b2 = __builtin_amdgcn_fmed3f(b1, b2, x);
+    b1 = fmaxf(b1, x);
+}
+
+__device__ __forceinline__ int group_of(int e, float inv) { return (int)(((float)e + 0.5f) * inv); }
+
+template <int L, int C, bool QUADS>
+__device__ __forceinline__ void drop_groups(const RouteArgs& a, float* keys, int lane, float* v) {
+    const float none = -__builtin_inff();
     const int size = a.experts / a.groups;
     const float inv = 1.0f / (float)size;
-    float* score = keys + a.experts + 4 * a.groups;
-    if (size % 4 == 0) {
+    float* score = keys + ((a.experts + 4 * a.groups + 3) & ~3);
+    int own[C];                                            // QUADS: the group of each chunk
+    if constexpr (QUADS) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int e = 4 * (lane + L * c), g = (int)(((float)e + 0.5f) * inv);
-            if (e < a.experts) *(float4*)(keys + e + 4 * g) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            const int e = 4 * (lane + L * c);
+            own[c] = group_of(e, inv);
+            if (e < a.experts)
+                *(float4*)(keys + e + 4 * own[c]) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 4 * C; ++i) {
-            const int e = 4 * (lane + L * (i >> 2)) + (i & 3), g = (int)(((float)e + 0.5f) * inv);
-            if (e < a.experts) keys[e + 4 * g] = v[i];
+            const int e = 4 * (lane + L * (i >> 2)) + (i & 3);
+            if (e < a.experts) keys[e + 4 * group_of(e, inv)] = v[i];
         }
     }
     wave_fence();
@@ -223,19 +237,24 @@ __device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, float* keys,
     while (2 * share * a.groups <= L) share *= 2;
     for (int at = lane; at < a.groups * share; at += L) {
         const int g = at / share, part = at & (share - 1);
-        const float none = -__builtin_inff();
+        const float* of = keys + g * (size + 4);
         float b1 = none, b2 = none;
-        for (int i = part; i < size; i += share) {
-            const float x = keys[g * (size + 4) + i];
-            const float k = x != x ? -FLT_MAX : x;         // NaN counts as the lowest value
-            b2 = fmaxf(b2, fminf(b1, k));
-            b1 = fmaxf(b1, k);
+        if constexpr (QUADS) {
+            for (int i = 4 * part; i < size; i += 4 * share) {
+                const float4 x = *(const float4*)(of + i);
+                best_two(b1, b2, x.x);
+                best_two(b1, b2, x.y);
+                best_two(b1, b2, x.z);
+                best_two(b1, b2, x.w);
+            }
+        } else {
+            for (int i = part; i < size; i += share) best_two(b1, b2, of[i]);
         }
         // (a group's lanes run the loop over `at` together)
         for (int o = 1; o < share; o *= 2) {
             const float p1 = __shfl_xor(b1, o), p2 = __shfl_xor(b2, o);
-            b2 = fmaxf(fminf(b1, p1), fmaxf(b2, p2));
-            b1 = fmaxf(b1, p1);
+            best_two(b1, b2, p1);
+            b2 = fmaxf(b2, p2);
         }
         // a sum of two lowest values stays above the score of an empty group
         if (part == 0) score[g] = a.group_best > 1 && b2 != none ? fmaxf(b1 + b2, -FLT_MAX) : b1;
@@ -247,15 +266,37 @@ __device__ __forceinline__ uint64_t groups_kept(const RouteArgs& a, float* keys,
         const int g = g0 + lane;
         const float mine = score[min(g, a.groups - 1)];
         int before = 0;
-        for (int h = 0; h < a.groups; ++h) {
-            const float s = score[h];
-            before += s > mine || (s == mine && h < g);
+        for (int h = 0; h < a.groups; h += 4) {            // (the scores' end is filled up to a float4)
+            const float4 s = *(const float4*)(score + h);
+            const float q[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                before += h + i < a.groups && (h + i < g ? q[i] >= mine : q[i] > mine);
         }
         uint64_t m = __ballot(g < a.groups && before < a.top_groups) >> shift;
         if constexpr (L < 64) m &= (1ull << L) - 1;
         kept |= m << g0;
     }
-    return kept;
+    const bool wide = a.groups > 32;
+    const uint32_t low = (uint32_t)kept, high = (uint32_t)(kept >> 32);
+    auto stays = [&](int g) { return ((wide && g >= 32 ? high : low) >> (g & 31)) & 1; };
+    if constexpr (QUADS) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const bool yes = stays(own[c]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * c + i] = yes ? v[4 * c + i] : none;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * C; ++i)
+            if (!stays(group_of(4 * (lane + L * (i >> 2)) + (i & 3), inv))) v[i] = none;
+    }
+}
+
+// LDS floats of a row: keys with their spare words, scores.
+__host__ __device__ inline int group_floats(int experts, int groups) {
+    return ((experts + 4 * groups + 3) & ~3) + ((groups + 3) & ~3);
 }
 
 // ---------------------------------------------------------------------------
@@ -355,13 +396,9 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         }
     }
     if (a.groups > 1) {
-        const uint64_t kept = groups_kept<L, C>(a, (float*)smem + r * (a.experts + 5 * a.groups + 3 & ~3), lane, v);
-        const float inv = (float)a.groups / (float)a.experts;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = 4 * (lane + L * (i >> 2)) + (i & 3), g = (int)(((float)e + 0.5f) * inv);
-            if (!(kept >> (g & 63) & 1)) v[i] = -__builtin_inff();
-        }
+        float* keys = (float*)smem + r * group_floats(a.experts, a.groups);
+        if (a.experts / a.groups % 4 == 0) drop_groups<L, C, true>(a, keys, lane, v);
+        else drop_groups<L, C, false>(a, keys, lane, v);
     }
 
     double key[N], mine = make_key(0u, 0);
@@ -634,7 +671,7 @@ int64_t plan_chunk(int64_t assignments) {
 template <bool B, int L, int C>
 void launch_route(const RouteArgs& a, hipStream_t s) {
     constexpr int ROWS = 256 / L;
-    const size_t lds = a.groups > 1 ? sizeof(float) * ROWS * (size_t)((a.experts + 5 * a.groups + 3) & ~3) : 0;
+    const size_t lds = a.groups > 1 ? sizeof(float) * ROWS * (size_t)group_floats(a.experts, a.groups) : 0;
     const dim3 grid((uint32_t)ceil_div(a.tokens, ROWS));
     if (a.top_k >= 5 && a.top_k <= 8) hipLaunchKernelGGL((route_kernel<B, L, C, 8>), grid, dim3(256), lds, s, a);
     else hipLaunchKernelGGL((route_kernel<B, L, C, 0>), grid, dim3(256), lds, s, a);

@@ -44,8 +44,8 @@ def group_scores(key, groups, group_best):
     out = np.full(groups, -np.inf)
     size = len(key) // groups
     for g in range(groups):
-        low = -float(np.finfo(np.float32).max)             # NaN counts as the lowest value
-        k = [low if np.isnan(x) else x for x in key[g * size:(g + 1) * size] if not np.isneginf(x)]
+        low = -float(np.finfo(np.float32).max)
+        k = [x for x in key[g * size:(g + 1) * size] if not np.isneginf(x) and not np.isnan(x)]
         if k:
             out[g] = max(sum(sorted(k)[-group_best:]), low)
     return out
