@@ -452,7 +452,7 @@ mx_status mx_route_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t 
  *     assignments without an expert, so every entry is a valid row.
  *   slot [tokens x top_k]: the grouped position of each assignment, -1
  *     without an expert: what mx_combine reads.
- * workspace: mx_route_plan_workspace(tokens, top_k, experts) bytes, 4-byte
+ * workspace: mx_route_plan_workspace(tokens, top_k, experts) bytes, 16-byte
  * aligned, its contents irrelevant before and after; where that is 0, NULL
  * will do.
  * experts <= 1024, tokens * top_k < 2^31.  Errors: MX_ERR_SHAPE, MX_ERR_NULL,

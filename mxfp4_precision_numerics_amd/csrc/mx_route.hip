@@ -24,6 +24,9 @@ struct RouteArgs {
     const float* bias;        // or null
     int score;                // MX_SOFTMAX, MX_SIGMOID
     int groups, top_groups, group_best;
+    int group_size, share_log2;   // experts of a group; lanes that scan one together
+    float group_inv;              // 1 / group_size
+    int row_floats, score_at;     // LDS of a row, and where its groups' scores begin
     int top_k, renorm;
     float scale;
     int vec, vec_bias;        // rows, the bias can be read four experts at a time
@@ -95,11 +98,14 @@ struct MinD {
 
 __device__ __forceinline__ double make_key(uint32_t u, int e) {
     const uint32_t hi = __builtin_amdgcn_alignbit(1u, u, 3);       // 001 and the upper 29 bits
-    const uint32_t lo = (u << 29) | (uint32_t)(MAX_EXPERTS - 1 - e);
+    const uint32_t lo = (u << 29) | (uint32_t)((MAX_EXPERTS - 1) ^ e);
     return __hiloint2double((int)hi, (int)lo);
 }
+// The key is the result of an addition: not -0, which would sort below 0, and
+// no signalling NaN, so the plain instruction turns NaN into -inf.
 __device__ __forceinline__ double pack_key(float key, int e) {
-    const uint32_t b = __float_as_uint(fmaxf(key, -__builtin_inff()) + 0.0f);    // NaN: -inf; -0: 0
+    uint32_t b;
+    asm("v_max_f32 %0, %1, %2" : "=v"(b) : "s"(0xFF800000u), "v"(key));
     const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
     return make_key(key == -__builtin_inff() ? 0u : u, e);
 }
@@ -117,31 +123,43 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 }
 
 // A lane's experts of a row: C chunks of four, chunk c at 4 (lane + L c).
-// Beyond the row's end: -inf.
+// Lanes past the row's end read its last experts again and take -inf: loads
+// without branches are all under way at once.  vec: experts % 4 == 0 and
+// aligned rows, a chunk is one load.
 template <bool BF16, int L, int C>
 __device__ __forceinline__ void load_row(const void* logits, int64_t base, int experts, int vec, int lane, float* v) {
+    if (vec) {
+        if constexpr (BF16) {
+            uint2 w[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int e = 4 * (lane + L * c);
-        if (vec && e < experts) {              // whole chunks only: experts % 4 == 0
-            if constexpr (BF16) {
-                const uint2 w = *(const uint2*)((const uint16_t*)logits + base + e);
-                v[4 * c + 0] = bf16lo(w.x);
-                v[4 * c + 1] = bf16hi(w.x);
-                v[4 * c + 2] = bf16lo(w.y);
-                v[4 * c + 3] = bf16hi(w.y);
-            } else {
-                const float4 w = *(const float4*)((const float*)logits + base + e);
+            for (int c = 0; c < C; ++c)
+                w[c] = *(const uint2*)((const uint16_t*)logits + base + min(4 * (lane + L * c), experts - 4));
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                v[4 * c + 0] = bf16lo(w[c].x);
+                v[4 * c + 1] = bf16hi(w[c].x);
+                v[4 * c + 2] = bf16lo(w[c].y);
+                v[4 * c + 3] = bf16hi(w[c].y);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float4 w = *(const float4*)((const float*)logits + base + min(4 * (lane + L * c), experts - 4));
                 v[4 * c + 0] = w.x;
                 v[4 * c + 1] = w.y;
                 v[4 * c + 2] = w.z;
                 v[4 * c + 3] = w.w;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[4 * c + i] = e + i < experts ? load_logit<BF16>(logits, base + e + i) : -__builtin_inff();
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4 * C; ++i)
+            v[i] = load_logit<BF16>(logits, base + min(4 * (lane + L * (i >> 2)) + (i & 3), experts - 1));
+    }
+    if (experts < 4 * L * C) {
+#pragma unroll
+        for (int i = 0; i < 4 * C; ++i)
+            v[i] = 4 * (lane + L * (i >> 2)) + (i & 3) < experts ? v[i] : -__builtin_inff();
     }
 }
 
@@ -190,11 +208,12 @@ __device__ __forceinline__ float renormalised(float l, bool there, bool softmax,
 
 // ---------------------------------------------------------------------------
 // Group scores and the mask of the groups that stay (bit g).  The lanes of a
-// row put their keys into LDS, each group behind four spare words so that
-// lanes scanning neighbouring groups meet different banks; 2^n lanes share the
-// scan of a group, as many as there are.  A group's place is the number of
-// groups before it.  Rows lie within a wave, so its own order is enough.
-// QUADS: groups are whole chunks of four experts.
+// row put their keys into LDS, or where groups are whole chunks of four
+// experts (QUADS) only the two best of each chunk.  Each group has four spare
+// words behind it, so that lanes scanning neighbouring groups meet different
+// banks; 2^n lanes share the scan of a group, as many as there are.  A group's
+// place is the number of groups before it.  Rows lie within a wave, so its own
+// order is enough.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -212,18 +231,19 @@ __device__ __forceinline__ int group_of(int e, float inv) { return (int)(((float
 
 template <int L, int C, bool QUADS>
 __device__ __forceinline__ void drop_groups(const RouteArgs& a, float* keys, int lane, float* v) {
-    const float none = -__builtin_inff();
-    const int size = a.experts / a.groups;
-    const float inv = 1.0f / (float)size;
-    float* score = keys + ((a.experts + 4 * a.groups + 3) & ~3);
+    const float none = -__builtin_inff(), inv = a.group_inv;
+    const int size = a.group_size, share = 1 << a.share_log2;
+    float* score = keys + a.score_at;
     int own[C];                                            // QUADS: the group of each chunk
     if constexpr (QUADS) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int e = 4 * (lane + L * c);
             own[c] = group_of(e, inv);
-            if (e < a.experts)
-                *(float4*)(keys + e + 4 * own[c]) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            float b1 = none, b2 = none;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) best_two(b1, b2, v[4 * c + i]);
+            if (e < a.experts) *(float2*)(keys + e / 2 + 4 * own[c]) = make_float2(b1, b2);
         }
     } else {
 #pragma unroll
@@ -233,21 +253,18 @@ __device__ __forceinline__ void drop_groups(const RouteArgs& a, float* keys, int
         }
     }
     wave_fence();
-    int share = 1;
-    while (2 * share * a.groups <= L) share *= 2;
     for (int at = lane; at < a.groups * share; at += L) {
-        const int g = at / share, part = at & (share - 1);
-        const float* of = keys + g * (size + 4);
+        const int g = at >> a.share_log2, part = at & (share - 1);
         float b1 = none, b2 = none;
         if constexpr (QUADS) {
-            for (int i = 4 * part; i < size; i += 4 * share) {
-                const float4 x = *(const float4*)(of + i);
+            const float* of = keys + g * (size / 2 + 4);
+            for (int i = 2 * part; i < size / 2; i += 2 * share) {
+                const float2 x = *(const float2*)(of + i);
                 best_two(b1, b2, x.x);
-                best_two(b1, b2, x.y);
-                best_two(b1, b2, x.z);
-                best_two(b1, b2, x.w);
+                b2 = fmaxf(b2, x.y);
             }
         } else {
+            const float* of = keys + g * (size + 4);
             for (int i = part; i < size; i += share) best_two(b1, b2, of[i]);
         }
         // (a group's lanes run the loop over `at` together)
@@ -290,13 +307,8 @@ __device__ __forceinline__ void drop_groups(const RouteArgs& a, float* keys, int
     } else {
 #pragma unroll
         for (int i = 0; i < 4 * C; ++i)
-            if (!stays(group_of(4 * (lane + L * (i >> 2)) + (i & 3), inv))) v[i] = none;
+            v[i] = stays(group_of(4 * (lane + L * (i >> 2)) + (i & 3), inv)) ? v[i] : none;
     }
-}
-
-// LDS floats of a row: keys with their spare words, scores.
-__host__ __device__ inline int group_floats(int experts, int groups) {
-    return ((experts + 4 * groups + 3) & ~3) + ((groups + 3) & ~3);
 }
 
 // ---------------------------------------------------------------------------
@@ -362,7 +374,11 @@ __device__ __forceinline__ void row_largest(double* key, double* list) {
     if constexpr (L >= 64) keep_larger<K>(list, [](double d) { return __shfl_xor(d, 32); });
 }
 
-// K = 8: five to eight experts by the merged lists; K = 0: any number, one row
+// Bound by the vector units: for 256 experts in groups about 190 instructions
+// a row, of which the keys' sort is a third.  65536 tokens, top 8 of 256 fp32
+// in 8 groups: 29 us (2.4 TB/s read; 21 us of it the instructions alone);
+// without bias and groups 17 us (4.1 TB/s).  16384 tokens, top 4 of 32: 3.6 us.
+// K = 8: up to eight experts by the merged lists; K = 0: any number, one row
 // maximum after the other.
 template <bool BF16, int L, int C, int K>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
@@ -394,10 +410,13 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
             const float s = softmax ? quick_exp(v[i] - top) * inv : quick_sigmoid(v[i]);
             v[i] = v[i] == -__builtin_inff() ? v[i] : s + b[i];
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += 0.0f;          // -0 counts as 0
     }
     if (a.groups > 1) {
-        float* keys = (float*)smem + r * group_floats(a.experts, a.groups);
-        if (a.experts / a.groups % 4 == 0) drop_groups<L, C, true>(a, keys, lane, v);
+        float* keys = (float*)smem + r * a.row_floats;
+        if (a.group_size % 4 == 0) drop_groups<L, C, true>(a, keys, lane, v);
         else drop_groups<L, C, false>(a, keys, lane, v);
     }
 
@@ -446,7 +465,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 //   sigmoid          dl_j = ds_j s_j (1 - s_j)
 //   sigmoid, renorm  dl_j = p_j (1 - s_j)(ds_j - sum_m ds_m p_m)
 // Only the first reads a whole row of logits.  The dense row is put together
-// in LDS and written once.
+// in LDS and written once.  Bound by memory: the write, and the lines that the
+// chosen logits lie in.  65536 tokens, top 8 of 256 fp32: 19 us.
 // ---------------------------------------------------------------------------
 struct RouteBwdArgs {
     const void* logits;
@@ -533,22 +553,26 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
 // by expert.  Assignments without an expert sort into one more bin behind the
 // last group.
 //
-// Within a wave the lanes with the same expert find each other by comparing
-// the bits of the expert's number (one ballot a bit); an assignment's place is
-// its group's start, plus its expert's count in the workgroups, waves and
-// lanes before it.  All counts are integers: the result is the same every run.
+// One launch counts each workgroup's share by expert, a second one places it:
+// an assignment goes to its group's start, plus its expert's count in the
+// workgroups, waves and rounds of 64 before it, plus its rank in its own
+// round, where the lanes with the same expert find each other by comparing
+// the bits of its number (one ballot a bit).  All are integers: the result is
+// the same every run.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024, PLAN_WAVES = PLAN_THREADS / 64;
-constexpr int PLAN_BINS = MAX_EXPERTS + 1;
-constexpr int PLAN_ALONE = 4;               // tiles that one workgroup sorts by itself
+constexpr int PLAN_BINS = MAX_EXPERTS + 4;   // rounded up to whole 16-byte pieces
+constexpr int PLAN_ALONE = 2048;             // assignments that one workgroup sorts by itself
+constexpr int PLAN_AHEAD = 8;                // loads of counts in flight
 
 struct PlanArgs {
     const int32_t* ids;
     int64_t assignments;
     int top_k, experts;
-    int64_t chunk;            // assignments of a workgroup, a multiple of PLAN_THREADS
+    int pitch;                // words of a workgroup's counts, a multiple of 4
+    int64_t chunk;            // assignments of a workgroup, a multiple of a tile
     int blocks;               // workgroups with assignments
-    int32_t* counts;          // [workgroups][experts + 1]
+    int32_t* counts;          // [workgroups][pitch]
     int32_t *offsets, *row_index, *slot;
 };
 
@@ -559,63 +583,78 @@ __device__ __forceinline__ int plan_bin(const PlanArgs& a, int64_t i) {
 
 __global__ __launch_bounds__(PLAN_THREADS) void plan_count_kernel(PlanArgs a) {
     __shared__ int hist[PLAN_BINS];
-    for (int e = threadIdx.x; e <= a.experts; e += PLAN_THREADS) hist[e] = 0;
+    for (int e = threadIdx.x; e < a.pitch; e += PLAN_THREADS) hist[e] = 0;
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(begin + a.chunk, a.assignments);
-    for (int64_t i = begin + threadIdx.x; i < end; i += PLAN_THREADS) atomicAdd(&hist[plan_bin(a, i)], 1);
+    for (int64_t i = begin + threadIdx.x; i < end; i += 2 * PLAN_THREADS) {
+        const int64_t j = i + PLAN_THREADS;
+        const int e = plan_bin(a, i), f = j < end ? plan_bin(a, j) : -1;
+        atomicAdd(&hist[e], 1);
+        if (f >= 0) atomicAdd(&hist[f], 1);
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e <= a.experts; e += PLAN_THREADS)
-        a.counts[(int64_t)blockIdx.x * (a.experts + 1) + e] = hist[e];
+    for (int e = threadIdx.x; e < a.pitch; e += PLAN_THREADS) a.counts[(int64_t)blockIdx.x * a.pitch + e] = hist[e];
 }
 
-// Exclusive prefix sums of n counts in LDS, by one wave.
+// Exclusive prefix sums of n counts in LDS, by one wave: each lane sums a run
+// of its own, the lanes' sums are scanned, and the run is added up again.
 __device__ __forceinline__ void wave_scan(const int* in, int* out, int n) {
-    int run = 0;
-    for (int at = 0; at < n; at += 64) {
-        const int i = at + (int)threadIdx.x;
-        const int own = i < n ? in[i] : 0;
-        int x = own;
+    const int lane = threadIdx.x & 63, per = (n + 63) / 64;
+    const int begin = min(n, lane * per), end = min(n, begin + per);
+    int own = 0;
+    for (int i = begin; i < end; ++i) own += in[i];
+    int x = own;
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int y = __shfl_up(x, d);
-            if ((int)threadIdx.x >= d) x += y;
-        }
-        if (i < n) out[i] = run + x - own;
-        run += __shfl(x, 63);
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(x, d);
+        x += lane >= d ? y : 0;
+    }
+    int run = x - own;
+    for (int i = begin; i < end; ++i) {
+        const int c = in[i];
+        out[i] = run;
+        run += c;
     }
 }
 
+// A tile is Q rounds of 64 assignments for each wave.
+template <int Q>
 __global__ __launch_bounds__(PLAN_THREADS) void plan_scatter_kernel(PlanArgs a) {
     __shared__ int total[PLAN_BINS], before[PLAN_BINS], base[PLAN_BINS];
     __shared__ uint16_t wave_count[PLAN_WAVES][PLAN_BINS];
+    constexpr int TILE = PLAN_THREADS * Q;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int bins = a.experts + 1;
-    for (int e = tid; e < bins; e += PLAN_THREADS) total[e] = before[e] = 0;
+    for (int e = tid; e < a.pitch; e += PLAN_THREADS) total[e] = before[e] = 0;
     __syncthreads();
-    // the counts of all workgroups, and of those before this one: several
-    // threads share a bin when there are fewer bins than threads
-    const int share = max(1, PLAN_THREADS / bins);
-    if (a.blocks <= 1)                        // one workgroup counts for itself
+    if (a.blocks <= 1) {                      // one workgroup counts for itself
         for (int64_t i = tid; i < a.assignments; i += PLAN_THREADS) atomicAdd(&total[plan_bin(a, i)], 1);
-    else for (int at = tid; at < bins * share; at += PLAN_THREADS) {
-        const int e = at % bins;
-        int all = 0, mine = 0;
-        constexpr int AHEAD = 16;             // loads in flight: each takes an L2 round trip
-        for (int b0 = at / bins; b0 < a.blocks; b0 += AHEAD * share) {
-            int n[AHEAD];
+    } else {
+        // the counts of all workgroups and of those before this one, four bins
+        // a thread; the threads left over take other workgroups
+        const int quads = a.pitch / 4, share = PLAN_THREADS / quads, part = tid / quads;
+        const int4* counts = (const int4*)a.counts + (tid - part * quads);
+        int4 all = {0, 0, 0, 0}, mine = {0, 0, 0, 0};
+        for (int b0 = part < share ? part : a.blocks; b0 < a.blocks; b0 += PLAN_AHEAD * share) {
+            int4 n[PLAN_AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int b = b0 + i * share;
-                n[i] = b < a.blocks ? a.counts[(int64_t)b * bins + e] : 0;
-            }
+            for (int i = 0; i < PLAN_AHEAD; ++i)
+                n[i] = b0 + i * share < a.blocks ? counts[(int64_t)(b0 + i * share) * quads] : make_int4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                all += n[i];
-                mine += b0 + i * share < (int)blockIdx.x ? n[i] : 0;
+            for (int i = 0; i < PLAN_AHEAD; ++i) {
+                all.x += n[i].x; all.y += n[i].y; all.z += n[i].z; all.w += n[i].w;
+                if (b0 + i * share < (int)blockIdx.x) {
+                    mine.x += n[i].x; mine.y += n[i].y; mine.z += n[i].z; mine.w += n[i].w;
+                }
             }
         }
-        atomicAdd(&total[e], all);
-        atomicAdd(&before[e], mine);
+        if (part < share) {
+            const int e = 4 * (tid - part * quads);
+            atomicAdd(&total[e], all.x); atomicAdd(&total[e + 1], all.y);
+            atomicAdd(&total[e + 2], all.z); atomicAdd(&total[e + 3], all.w);
+            atomicAdd(&before[e], mine.x); atomicAdd(&before[e + 1], mine.y);
+            atomicAdd(&before[e + 2], mine.z); atomicAdd(&before[e + 3], mine.w);
+        }
     }
     __syncthreads();
     if (wave == 0) wave_scan(total, base, bins);
@@ -625,55 +664,88 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_scatter_kernel(PlanArgs a) 
         base[e] += before[e];
     }
     const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(begin + a.chunk, a.assignments);
-    for (int64_t at = begin; at < end; at += PLAN_THREADS) {
-        for (int e = lane; e < bins; e += 64) wave_count[wave][e] = 0;
-        __syncthreads();
-        const int64_t i = at + tid;
-        const bool live = i < end;
-        const int e = live ? plan_bin(a, i) : 0;
-        uint64_t same = __ballot(live);
-        for (int bit = 1; bit <= a.experts; bit <<= 1) {
-            const uint64_t set = __ballot((e & bit) != 0);
-            same &= (e & bit) ? set : ~set;
+    for (int64_t at = begin; at < end; at += TILE) {
+        const int64_t first = at + wave * 64 * Q + lane;
+        int e[Q], rank[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) e[q] = first + 64 * q < end ? plan_bin(a, first + 64 * q) : 0;
+        uint16_t* count = wave_count[wave];
+        for (int b = lane; b < bins; b += 64) count[b] = 0;
+        wave_fence();
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const bool live = first + 64 * q < end;
+            uint64_t same = __ballot(live);
+            for (int bit = 1; bit <= a.experts; bit <<= 1) {
+                const uint64_t set = __ballot((e[q] & bit) != 0);
+                same &= (e[q] & bit) ? set : ~set;
+            }
+            const int ahead = __popcll(same & ((1ull << lane) - 1)), held = count[e[q]];
+            rank[q] = held + ahead;
+            wave_fence();
+            if (live && ahead == 0) count[e[q]] = (uint16_t)(held + __popcll(same));
+            wave_fence();
         }
-        const int rank = __popcll(same & ((1ull << lane) - 1));
-        if (live && rank == 0) wave_count[wave][e] = (uint16_t)__popcll(same);
         __syncthreads();
         for (int b = tid; b < bins; b += PLAN_THREADS) {
-            int run = 0;
+            int n[PLAN_WAVES], run = 0;
+#pragma unroll
+            for (int w = 0; w < PLAN_WAVES; ++w) n[w] = wave_count[w][b];
 #pragma unroll
             for (int w = 0; w < PLAN_WAVES; ++w) {
-                const int n = wave_count[w][b];
                 wave_count[w][b] = (uint16_t)run;
-                run += n;
+                run += n[w];
             }
-            before[b] = run;                  // this tile's count
+            total[b] = run;                   // this tile's count
         }
         __syncthreads();
-        if (live) {
-            const int pos = base[e] + wave_count[wave][e] + rank;
-            a.row_index[pos] = (int)(i / a.top_k);
-            a.slot[i] = e < a.experts ? pos : -1;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int64_t i = first + 64 * q;
+            if (i >= end) continue;
+            const int pos = base[e[q]] + count[e[q]] + rank[q];
+            a.row_index[pos] = (int)((uint32_t)i / (uint32_t)a.top_k);
+            a.slot[i] = e[q] < a.experts ? pos : -1;
         }
         __syncthreads();
-        for (int b = tid; b < bins; b += PLAN_THREADS) base[b] += before[b];
+        for (int b = tid; b < bins; b += PLAN_THREADS) base[b] += total[b];
     }
 }
 
-// Assignments of a workgroup: all, while one workgroup is done with them
-// before two launches would be; otherwise a tile, or as many as keep the
-// workgroups at 256.
-int64_t plan_chunk(int64_t assignments) {
-    const int64_t tiles = max((int64_t)1, ceil_div(assignments, PLAN_THREADS));
-    return PLAN_THREADS * (tiles <= PLAN_ALONE ? tiles : ceil_div(tiles, 256));
+// Rounds of a wave in a tile and assignments of a workgroup.  A few
+// assignments are sorted by one workgroup in one launch, before two launches
+// would be done; more are spread in small tiles until there are enough
+// workgroups, since each of them adds up the counts of all.
+struct PlanShape {
+    int rounds;
+    int64_t chunk, blocks;
+};
+PlanShape plan_shape(int64_t n) {
+    const int rounds = (n > PLAN_THREADS && n <= PLAN_ALONE) || n > 256 * PLAN_THREADS ? 2 : 1;
+    const int64_t tile = rounds * PLAN_THREADS, tiles = max((int64_t)1, ceil_div(n, tile));
+    const int64_t chunk = tile * (n <= PLAN_ALONE ? tiles : ceil_div(tiles, 256));
+    return {rounds, chunk, ceil_div(n, chunk)};
 }
+int plan_pitch(int experts) { return (experts + 1 + 3) & ~3; }
 
 template <bool B, int L, int C>
-void launch_route(const RouteArgs& a, hipStream_t s) {
+void launch_route(RouteArgs a, hipStream_t s) {
     constexpr int ROWS = 256 / L;
-    const size_t lds = a.groups > 1 ? sizeof(float) * ROWS * (size_t)group_floats(a.experts, a.groups) : 0;
+    size_t lds = 0;
+    if (a.groups > 1) {
+        a.group_size = a.experts / a.groups;
+        a.group_inv = 1.0f / (float)a.group_size;
+        while ((2 << a.share_log2) * a.groups <= L) ++a.share_log2;
+        const int words = a.group_size % 4 == 0 ? a.experts / 2 : a.experts;
+        a.score_at = (words + 4 * a.groups + 3) & ~3;
+        a.row_floats = a.score_at + ((a.groups + 3) & ~3);
+        lds = sizeof(float) * ROWS * (size_t)a.row_floats;
+    }
     const dim3 grid((uint32_t)ceil_div(a.tokens, ROWS));
-    if (a.top_k >= 5 && a.top_k <= 8) hipLaunchKernelGGL((route_kernel<B, L, C, 8>), grid, dim3(256), lds, s, a);
+    // merged lists cost the same for any number up to 8, a row maximum each time the same again.
+    // 65536 tokens, both directions, maxima / lists: 32 experts, top 4: 9.5 / 10.2 us; 128: 20.5 / 19.8
+    // (top 3: 19.5 / 19.5); 256: 35.1 / 32.9 (top 3: 33.0 / 32.1, top 2: 30.9 / 31.5)
+    if (a.top_k >= (C >= 4 ? 4 : 5) && a.top_k <= 8) hipLaunchKernelGGL((route_kernel<B, L, C, 8>), grid, dim3(256), lds, s, a);
     else hipLaunchKernelGGL((route_kernel<B, L, C, 0>), grid, dim3(256), lds, s, a);
 }
 template <bool B, int L, int C>
@@ -683,11 +755,21 @@ void launch_route(const RouteBwdArgs& a, hipStream_t s) {
 }
 
 // The lanes that share a row and the chunks of four experts each holds: enough
-// for the experts, and a lane for each chosen one.
+// for the experts, and a lane for each chosen one.  With many tokens eight
+// lanes take a row: of the steps between lanes there is one less, for twice
+// the rows.  With few tokens 16 lanes, whose waves are done sooner.  Both
+// directions, 16 / 8 lanes, top 8 of 256: 6.7 / 7.7 us at 4096 tokens,
+// 8.7 / 8.5 at 8192, 36.9 / 35.9 at 65536; of 64: 18.1 / 14.4 there.
+constexpr int64_t MANY_TOKENS = 8192;
+
 template <bool B, class A>
 void dispatch_route(const A& a, hipStream_t s) {
     const int e = a.experts, k = a.top_k;
+    const bool many = a.tokens >= MANY_TOKENS && k <= 8;
     if (e <= 32 && k <= 8) launch_route<B, 8, 1>(a, s);
+    else if (e <= 64 && many) launch_route<B, 8, 2>(a, s);
+    else if (e <= 128 && many) launch_route<B, 8, 4>(a, s);
+    else if (e <= 256 && many) launch_route<B, 8, 8>(a, s);
     else if (e <= 64 && k <= 16) launch_route<B, 16, 1>(a, s);
     else if (e <= 128 && k <= 16) launch_route<B, 16, 2>(a, s);
     else if (e <= 256 && k <= 16) launch_route<B, 16, 4>(a, s);
@@ -725,9 +807,21 @@ mx_status mx_route(const void* logits, mx_dtype lt, int64_t tokens, int32_t expe
     if (!logits || !ids || !weights) return MX_ERR_NULL;
     if (!aligned_to(logits, type_bytes(lt)) || !aligned_to(bias, 4) || !aligned_to(ids, 4) || !aligned_to(weights, 4))
         return MX_ERR_ALIGN;
-    RouteArgs a{logits, tokens, logits_ld ? logits_ld : experts, experts, bias, score, groups, top_groups, group_best,
-                top_k, renorm != 0, scale, 0, 0, ids, weights};
-    if (groups == top_groups) a.groups = 1;   // every group stays
+    RouteArgs a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.ld = logits_ld ? logits_ld : experts;
+    a.experts = experts;
+    a.bias = bias;
+    a.score = score;
+    a.groups = groups == top_groups ? 1 : groups;      // every group stays
+    a.top_groups = top_groups;
+    a.group_best = group_best;
+    a.top_k = top_k;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.ids = ids;
+    a.weights = weights;
     a.vec = experts % 4 == 0 && a.ld % 4 == 0 && aligned_to(logits, 4 * type_bytes(lt));
     a.vec_bias = experts % 4 == 0 && aligned_to(bias, 16);
     (void)hipGetLastError();
@@ -760,8 +854,8 @@ mx_status mx_route_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t 
 int64_t mx_route_plan_workspace(int64_t tokens, int32_t top_k, int32_t experts) {
     if (tokens < 0 || top_k < 1 || experts < 1 || experts > MAX_EXPERTS || tokens > (int64_t)INT32_MAX / top_k)
         return 0;
-    const int64_t n = tokens * top_k, blocks = ceil_div(n, plan_chunk(n));
-    return blocks <= 1 ? 0 : 4 * blocks * (experts + 1);
+    const int64_t blocks = plan_shape(tokens * top_k).blocks;
+    return blocks <= 1 ? 0 : 4 * blocks * plan_pitch(experts);
 }
 
 mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32_t experts, int32_t* offsets,
@@ -770,17 +864,20 @@ mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32
     if (tokens > (int64_t)INT32_MAX / top_k) return MX_ERR_SHAPE;
     if (!offsets) return MX_ERR_NULL;
     const int64_t n = tokens * top_k;
-    const int64_t chunk = plan_chunk(n), blocks = ceil_div(n, chunk);
-    if (n > 0 && (!ids || !row_index || !slot || (blocks > 1 && !workspace))) return MX_ERR_NULL;
+    const PlanShape shape = plan_shape(n);
+    if (n > 0 && (!ids || !row_index || !slot || (shape.blocks > 1 && !workspace))) return MX_ERR_NULL;
     if (!aligned_to(ids, 4) || !aligned_to(offsets, 4) || !aligned_to(row_index, 4) || !aligned_to(slot, 4) ||
-        !aligned_to(workspace, 4))
+        !aligned_to(workspace, 16))
         return MX_ERR_ALIGN;
-    PlanArgs a{ids, n, top_k, experts, chunk, (int)blocks, (int32_t*)workspace, offsets, row_index, slot};
+    PlanArgs a{ids, n, top_k, experts, plan_pitch(experts), shape.chunk, (int)shape.blocks, (int32_t*)workspace,
+               offsets, row_index, slot};
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (blocks > 1) hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(PLAN_THREADS), 0, s, a);
+    if (a.blocks > 1) hipLaunchKernelGGL(plan_count_kernel, dim3(a.blocks), dim3(PLAN_THREADS), 0, s, a);
     // with nothing to sort one workgroup writes the offsets, all 0
-    hipLaunchKernelGGL(plan_scatter_kernel, dim3(max(a.blocks, 1)), dim3(PLAN_THREADS), 0, s, a);
+    const dim3 grid(max(a.blocks, 1));
+    if (shape.rounds == 2) hipLaunchKernelGGL(plan_scatter_kernel<2>, grid, dim3(PLAN_THREADS), 0, s, a);
+    else hipLaunchKernelGGL(plan_scatter_kernel<1>, grid, dim3(PLAN_THREADS), 0, s, a);
     return launch_status();
 }
 

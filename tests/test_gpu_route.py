@@ -225,6 +225,54 @@ def test_many_rows():
     assert (dl - want).abs().max() <= D_TOL * 2.0 * dw.abs().max()
 
 
+@pytest.mark.parametrize("experts,k", [(32, 8), (61, 3), (64, 4), (64, 7), (100, 5), (128, 2), (200, 4), (256, 8), (256, 1)])
+@pytest.mark.parametrize("groups,best", [(1, 1), (4, 2)])
+def test_many_tokens(experts, k, groups, best):
+    """The variants for many tokens, with a bias, groups and masked experts,
+    against a vectorised 64-bit form; rows that fp32 cannot order are left
+    out, the others must agree."""
+    tt = torch()
+    if experts % groups:
+        groups, best = 1, 1
+    gen = tt.Generator("cuda").manual_seed(experts + k)
+    x = tt.randn((8200, experts), device="cuda", generator=gen)
+    x[::7, ::3] = -INF
+    x[5] = -INF
+    bias = 0.001 * tt.randint(-60, 61, (experts,), device="cuda", generator=gen)
+    top_groups = max(1, groups // 2)
+    k = min(k, top_groups * experts // groups)
+    ids, w = mx.route(x, k, score=mx.SIGMOID, bias=bias, groups=groups, top_groups=top_groups, group_best=best)
+    key = tt.where(x == -INF, -INF, tt.sigmoid(x.double()) + bias.double())
+    sure = tt.ones(8200, dtype=tt.bool, device="cuda")
+
+    def apart(v, n):
+        v = v.sort(dim=1, descending=True).values[:, :n + 1]
+        d = v[:, :-1] - v[:, 1:]
+        return ((d > KEY_TOL) | tt.isnan(d) | (v[:, :-1] == -INF)).all(1)
+
+    if groups > 1:
+        part = key.view(8200, groups, -1).sort(dim=2, descending=True).values[:, :, :best]
+        of = tt.where(part == -INF, 0.0, part).sum(2)
+        of = tt.where(part[:, :, 0] == -INF, -INF, of)
+        sure &= apart(of, top_groups)
+        drop = tt.ones_like(of, dtype=tt.bool)
+        drop.scatter_(1, of.sort(dim=1, descending=True, stable=True).indices[:, :top_groups], False)
+        key = tt.where(drop[:, :, None], -INF, key.view(8200, groups, -1)).view(8200, experts)
+    sure &= apart(key, k)
+    best_k = key.sort(dim=1, descending=True, stable=True)
+    want = tt.where(best_k.values[:, :k] == -INF, -1, best_k.indices[:, :k])
+    assert sure.float().mean() > 0.9 and tt.equal(ids[sure].long(), want[sure])
+    s = tt.where(ids < 0, 0.0, tt.sigmoid(x.double()).gather(1, ids.long().clamp(min=0)))
+    p = s / s.sum(1, keepdim=True).clamp(min=1e-300)
+    assert ((w - p).abs() <= W_RTOL * p).all()
+    dw = tt.randn((8200, k), device="cuda", generator=gen)
+    dl = mx.route_bwd(x, ids, dw, score=mx.SIGMOID)
+    g = tt.where(ids < 0, 0.0, dw.double())
+    d = p * (1 - s) * (g - (g * p).sum(1, keepdim=True))
+    want = tt.zeros((8200, experts), device="cuda", dtype=tt.float64).scatter_add_(1, ids.long().clamp(min=0), d)
+    assert (dl - want).abs().max() <= D_TOL * dw.abs().max()
+
+
 @pytest.mark.parametrize("tokens,k", [(0, 2), (1, 1), (1, 4), (9, 7), (63, 1), (16, 4), (65, 1), (341, 3), (1025, 1),
                                       (700, 3), (5000, 4), (40000, 8)])
 @pytest.mark.parametrize("experts", [1, 3, 32, 33, 256, 1024])
