@@ -510,7 +510,7 @@ mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const v
  * (outs gets copies): the caller sees it in *norm and drops the step.
  * max_norm >= 0.  workspace: mx_grad_workspace(count) bytes, 8-byte aligned,
  * contents irrelevant before and after.  Outputs may not overlap other
- * tensors.  At most 2^40 elements in all.
+ * tensors.  At most 2^37 elements in all and 64 GB in one tensor.
  * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
  * MX_ERR_LAUNCH. */
 int64_t mx_grad_workspace(int32_t count);

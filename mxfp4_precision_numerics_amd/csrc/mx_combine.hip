@@ -30,16 +30,17 @@ struct CombineArgs {
 typedef unsigned int u32x2v __attribute__((ext_vector_type(2), aligned(2)));
 typedef unsigned int u32x4v __attribute__((ext_vector_type(4), aligned(2)));
 
-// STREAM: the accesses bypass what the caches hold (non-temporal).
+// STREAM: past the caches (non-temporal).  Stores always are: no dirty lines
+// are left to write back when the kernel ends (the gradient of 1024 tokens of
+// 4 rows of 2880 took 12.1 us without, 10.0 with them; never slower).
 template <bool STREAM, class T>
 __device__ __forceinline__ T load_piece(const void* p) {
     if constexpr (STREAM) return __builtin_nontemporal_load((const T*)p);
     else return *(const T*)p;
 }
-template <bool STREAM, class T>
+template <class T>
 __device__ __forceinline__ void store_piece(void* p, T v) {
-    if constexpr (STREAM) __builtin_nontemporal_store(v, (T*)p);
-    else *(T*)p = v;
+    __builtin_nontemporal_store(v, (T*)p);
 }
 
 // V consecutive elements of a row, as they are in memory.
@@ -79,7 +80,7 @@ struct Piece {
     }
 };
 
-template <bool BF16, int V, bool FULL, bool STREAM>
+template <bool BF16, int V, bool FULL>
 __device__ __forceinline__ void store_v(void* p, int64_t at, int64_t left, const float* f) {
     if constexpr (!FULL) {
 #pragma unroll
@@ -92,12 +93,12 @@ __device__ __forceinline__ void store_v(void* p, int64_t at, int64_t left, const
         uint32_t u[V / 2];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) u[i] = f32_to_bf16_rne(f[2 * i]) | f32_to_bf16_rne(f[2 * i + 1]) << 16;
-        if constexpr (V == 8) store_piece<STREAM>((uint16_t*)p + at, (u32x4v){u[0], u[1], u[2], u[3]});
-        else store_piece<STREAM>((uint16_t*)p + at, (u32x2v){u[0], u[1]});
+        if constexpr (V == 8) store_piece((uint16_t*)p + at, (u32x4v){u[0], u[1], u[2], u[3]});
+        else store_piece((uint16_t*)p + at, (u32x2v){u[0], u[1]});
     } else {
 #pragma unroll
         for (int i = 0; i < V; i += 4)
-            store_piece<STREAM>((float*)p + at + i, (u32x4v){__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
+            store_piece((float*)p + at + i, (u32x4v){__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
                                                              __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3])});
     }
 }
@@ -161,7 +162,7 @@ __device__ __forceinline__ void combine_piece(const CombineArgs& a, int64_t t, i
         if (j0 >= a.top_k) break;
         n.load(a.slot, a.weights, t, a.top_k, j0, a.rows);
     }
-    store_v<OB, V, FULL, STREAM>(a.out, t * a.out_ld + col, left, acc);
+    store_v<OB, V, FULL>(a.out, t * a.out_ld + col, left, acc);
 }
 
 template <bool YB, bool OB, bool STREAM>
@@ -195,11 +196,27 @@ struct CombineBwdArgs {
 
 // dy[slot_tj] = w_tj dout[t] and dw_tj = <dout[t], y[slot_tj]> from one read of
 // dout and y.  Bound by memory.
-// One workgroup: one token, its waves side by side along the columns, at most
-// MAX_WAVES of them (one wave a token: 154 us at the size below, two 149, four
-// 146).  Beyond the tokens the workgroups clear the rows of dy past the used
-// ones.  16384 tokens of 4 rows, 2880 bf16 columns: 147 us, 5.8 TB/s.
-constexpr int MAX_WAVES = 4;
+// One workgroup: one token, its waves side by side along the columns (one wave
+// a token: 5% slower at the size below).  Beyond the tokens the workgroups
+// clear the rows of dy past the used ones.  16384 tokens of 4 rows, 2880 bf16
+// columns: 141 us, 6.0 TB/s.
+constexpr int MAX_WAVES = 8;
+
+// The sums over a wave of FLIGHT values, in a fixed order: lanes 16 j .. 16 j + 15
+// get that of value j.  In each of the first two steps a lane hands on the half
+// of the values that it does not keep.
+__device__ __forceinline__ float wave_sums(const float (&v)[FLIGHT]) {
+    static_assert(FLIGHT == 4, "two halvings");
+    const bool b5 = threadIdx.x & 32, b4 = threadIdx.x & 16;
+    const float x = (b5 ? v[2] : v[0]) + __shfl_xor(b5 ? v[0] : v[2], 32);
+    const float y = (b5 ? v[3] : v[1]) + __shfl_xor(b5 ? v[1] : v[3], 32);
+    float s = (b4 ? y : x) + __shfl_xor(b4 ? x : y, 16);
+    s += quad_xor1(s);
+    s += quad_xor2(s);
+    s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x141, 0xF, 0xF, false));   // other quad
+    s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x140, 0xF, 0xF, false));   // other eight
+    return s;
+}
 
 template <bool DB, bool YB, bool STREAM, bool FULL>
 __device__ __forceinline__ void bwd_piece(const CombineBwdArgs& a, int64_t t, int64_t col, const Flight& n,
@@ -223,7 +240,7 @@ __device__ __forceinline__ void bwd_piece(const CombineBwdArgs& a, int64_t t, in
         float v[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = n.weight[j] * g[i];
-        store_v<YB, V, FULL, STREAM>(a.dy, n.slot[j] * a.dy_ld + col, left, v);
+        store_v<YB, V, FULL>(a.dy, n.slot[j] * a.dy_ld + col, left, v);
     }
     if (a.dweights) {
 #pragma unroll
@@ -245,8 +262,8 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void combine_bwd_kernel(CombineBwdA
         const float zero[V] = {};
         for (int64_t r = used + blockIdx.x - a.tokens; r < a.rows; r += gridDim.x - a.tokens)
             for (int64_t col = tid * V; col < a.cols; col += threads * V) {
-                if (a.cols - col >= V) store_v<YB, V, true, STREAM>(a.dy, r * a.dy_ld + col, V, zero);
-                else store_v<YB, V, false, STREAM>(a.dy, r * a.dy_ld + col, a.cols - col, zero);
+                if (a.cols - col >= V) store_v<YB, V, true>(a.dy, r * a.dy_ld + col, V, zero);
+                else store_v<YB, V, false>(a.dy, r * a.dy_ld + col, a.cols - col, zero);
             }
         return;
     }
@@ -259,14 +276,9 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void combine_bwd_kernel(CombineBwdA
         for (; col <= a.cols - V; col += threads * V) bwd_piece<DB, YB, STREAM, true>(a, t, col, n, dot);
         if (col < a.cols) bwd_piece<DB, YB, STREAM, false>(a, t, col, n, dot);
         if (!a.dweights) continue;
-#pragma unroll
-        for (int j = 0; j < FLIGHT; ++j)
-#pragma unroll
-            for (int d = 32; d; d >>= 1) dot[j] += __shfl_xor(dot[j], d);
+        const float sum = wave_sums(dot);
         __syncthreads();
-        if ((tid & 63) == 0)
-#pragma unroll
-            for (int j = 0; j < FLIGHT; ++j) part[tid >> 6][j] = dot[j];
+        if ((tid & 15) == 0) part[tid >> 6][(tid >> 4) & 3] = sum;
         __syncthreads();
         if (tid < FLIGHT && j0 + tid < a.top_k) {
             float sum = 0.0f;
@@ -286,9 +298,9 @@ mx_status check_combine(mx_dtype yt, mx_dtype ot, int64_t rows, int64_t cols, in
 }
 
 // Whether the experts' rows are more than half of the 256 MB Infinity Cache:
-// the rows and the output then bypass the caches, which could not keep them
-// for a neighbouring call.  Measured on bf16 rows of 2880, 4 a token, cached /
-// bypassing: forward 10.7 / 11.4 us at 47 MB of rows, 19.6 / 20.6 at 94,
+// they are then read past the caches, which could not keep them for a
+// neighbouring call.  Measured on bf16 rows of 2880, 4 a token, cached / past
+// the caches: forward 10.7 / 11.4 us at 47 MB of rows, 19.6 / 20.6 at 94,
 // 31.6 / 29.5 at 142, 107 / 86 at 377; gradient 19.8 / 21.9, 37.4 / 39.5,
 // 55.9 / 56.0, 163 / 147.
 bool streams(int64_t rows, int64_t cols, mx_dtype yt) {
@@ -354,8 +366,11 @@ mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const v
     const int64_t clear = used_rows && rows > 0 ? min(rows, (int64_t)1024) : 0;
     if (tokens + clear == 0) return MX_OK;
     if (tokens + clear >= ((int64_t)1 << 23)) return MX_ERR_SHAPE;     // 512 threads a workgroup at most
-    // as few passes over the columns as MAX_WAVES waves allow, and as few waves as these passes need
-    const int64_t chunks = ceil_div(cols, 64 * v), waves = ceil_div(chunks, ceil_div(chunks, MAX_WAVES));
+    // as few passes over the columns as the waves allow, and as few waves as these passes need; more waves
+    // where there are few tokens (three / six for rows of 2880 bf16: 64 tokens 5.9 / 4.9 us, 256 6.4 / 5.4,
+    // 1024 9.3 / 10.3, 16384 141 / 141)
+    const int64_t most = tokens <= 512 ? MAX_WAVES : 4;
+    const int64_t chunks = ceil_div(cols, 64 * v), waves = ceil_div(chunks, ceil_div(chunks, most));
     const dim3 grid((uint32_t)(tokens + clear)), block((uint32_t)(64 * waves));
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();

@@ -711,7 +711,7 @@ def grad_norm(grads, norm=None, workspace=None):
 
 def grad_clip(grads, max_norm: float, outs=None, norm=None, workspace=None):
     """Scales the tensors in grads by min(1, max_norm / (norm + 1e-6)), in
-    place or into the tensors of outs (same types and shapes), and returns
+    place or into the tensors of outs (same types and sizes), and returns
     their norm before that as a 0-dim fp32 device tensor.  A norm that is not
     finite leaves the values as they are (see mx_grad_clip)."""
     return _grad_call("mx_grad_clip", grads, outs, float(max_norm), norm, workspace)
@@ -722,9 +722,9 @@ def _grad_call(fn, grads, outs, max_norm, norm, workspace):
     grads, types, numels, ptrs = _grad_list(grads, "grads")
     n, outs_at = len(grads), None
     if outs is not None:
-        outs, out_types, _, out_ptrs = _grad_list(outs, "outs")
-        if out_types != types or [g.shape for g in grads] != [o.shape for o in outs]:
-            raise ValueError("outs must match grads in number, types and shapes")
+        outs, out_types, out_numels, out_ptrs = _grad_list(outs, "outs")
+        if out_types != types or out_numels != numels:
+            raise ValueError("outs must match grads in number, types and sizes")
         outs_at = out_ptrs.buffer_info()[0]
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
