@@ -446,7 +446,9 @@ mx_status mx_route_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t 
  * [0, experts) means no expert and sorts behind the last group.
  *   offsets [experts + 1]: group starts, [0] = 0, [experts] = the number of
  *     assignments that have an expert: the group_offsets of
- *     mx_quantize_1d and mx_grouped_gemm.
+ *     mx_quantize_1d and mx_grouped_gemm.  Where that is less than tokens *
+ *     top_k, the rows past it are in no group: the column-wise quantizer
+ *     skips them, the grouped GEMM leaves its output there as it is.
  *   row_index [tokens * top_k]: the token of each grouped position: their
  *     row_index.  Positions past offsets[experts] hold the tokens of the
  *     assignments without an expert, so every entry is a valid row.

@@ -1308,7 +1308,7 @@ mx_status launch_col(const ColArgs& a, bool bf, bool rh, bool sr, int rowq, hipS
 
 extern "C" {
 
-int mx_version(void) { return 1; }
+int mx_version(void) { return 2; }
 
 const char* mx_status_str(mx_status s) {
     switch (s) {

@@ -522,6 +522,22 @@ def grouped_gemm_q(a_codes, a_scales, b_codes, b_scales, group_offsets, M, N, K,
 # ---------------------------------------------------------------------------
 # Routing, the experts' rows back into tokens, gradient clipping
 # ---------------------------------------------------------------------------
+# These calls can be as short as their launch, so what they allocate and check
+# takes the quickest way there is.
+def _new(device, dtype, rows, cols):
+    return _torch().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _new_vector(device, dtype, n):
+    return _torch().empty_strided((n,), (1,), dtype=dtype, device=device)
+
+
+def _same(t, shape, dtype, name):
+    """_shaped, one comparison where all is well."""
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _shaped(t, shape, dtype, name)
+
+
 def _rows(t, name, shape=None, dtype=None):
     """A device matrix with contiguous rows any pitch apart; returns the pitch
     in elements (0 when the rows are contiguous)."""
@@ -550,15 +566,15 @@ def route(logits, top_k: int, score: int = SOFTMAX, bias=None, groups: int = 1, 
     ld = _rows(logits, "logits")
     tokens, experts = logits.shape
     if bias is not None:
-        _shaped(bias, (experts,), torch.float32, "bias")
+        _same(bias, (experts,), torch.float32, "bias")
     if ids is None:
-        ids = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
+        ids = _new(logits.device, torch.int32, tokens, top_k)
     else:
-        _shaped(ids, (tokens, top_k), torch.int32, "ids")
+        _same(ids, (tokens, top_k), torch.int32, "ids")
     if weights is None:
-        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
+        weights = torch.empty_like(ids, dtype=torch.float32)
     else:
-        _shaped(weights, (tokens, top_k), torch.float32, "weights")
+        _same(weights, (tokens, top_k), torch.float32, "weights")
     _check("mx_route", lib().mx_route(
         _ptr(logits), _dtype_code(logits), tokens, experts, ld, _ptr(bias), score, groups, top_groups, group_best,
         top_k, int(bool(renorm)), scale, _ptr(ids), _ptr(weights), _stream()))
@@ -575,11 +591,13 @@ def route_bwd(logits, ids, dweights, score: int = SOFTMAX, renorm: bool = True, 
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top_k]")
     top_k = ids.shape[1]
-    _shaped(ids, (tokens, top_k), torch.int32, "ids")
-    _shaped(dweights, (tokens, top_k), torch.float32, "dweights")
+    _same(ids, (tokens, top_k), torch.int32, "ids")
+    _same(dweights, (tokens, top_k), torch.float32, "dweights")
+    dld = 0
     if dlogits is None:
-        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-    dld = _rows(dlogits, "dlogits", (tokens, experts), logits.dtype)
+        dlogits = _new(logits.device, logits.dtype, tokens, experts)
+    else:
+        dld = _rows(dlogits, "dlogits", (tokens, experts), logits.dtype)
     _check("mx_route_bwd", lib().mx_route_bwd(
         _ptr(logits), _dtype_code(logits), tokens, experts, ld, score, top_k, int(bool(renorm)), scale, _ptr(ids),
         _ptr(dweights), _ptr(dlogits), dld, _stream()))
@@ -600,17 +618,17 @@ def route_plan(ids, num_experts: int, offsets=None, row_index=None, slot=None, w
     tokens, top_k = ids.shape
     dev, i32 = ids.device, torch.int32
     if offsets is None:
-        offsets = torch.empty(num_experts + 1, dtype=i32, device=dev)
+        offsets = _new_vector(dev, i32, num_experts + 1)
     else:
-        _shaped(offsets, (num_experts + 1,), i32, "offsets")
+        _same(offsets, (num_experts + 1,), i32, "offsets")
     if row_index is None:
-        row_index = torch.empty(tokens * top_k, dtype=i32, device=dev)
+        row_index = _new_vector(dev, i32, tokens * top_k)
     else:
-        _shaped(row_index, (tokens * top_k,), i32, "row_index")
+        _same(row_index, (tokens * top_k,), i32, "row_index")
     if slot is None:
-        slot = torch.empty((tokens, top_k), dtype=i32, device=dev)
+        slot = torch.empty_like(ids)
     else:
-        _shaped(slot, (tokens, top_k), i32, "slot")
+        _same(slot, (tokens, top_k), i32, "slot")
     need = lib().mx_route_plan_workspace(tokens, top_k, num_experts)
     workspace = _workspace(workspace, need, dev)
     _check("mx_route_plan", lib().mx_route_plan(
@@ -623,7 +641,7 @@ def _workspace(t, need, device):
     """A uint8 device buffer of at least `need` bytes."""
     torch = _torch()
     if t is None:
-        return None if need == 0 else torch.empty(need, dtype=torch.uint8, device=device)
+        return None if need == 0 else _new_vector(device, torch.uint8, need)
     if t.dtype != torch.uint8 or t.numel() < need:
         raise ValueError("workspace must be uint8 of at least %d bytes" % need)
     return _dev(t, "workspace")
@@ -634,9 +652,9 @@ def _slots(slot, weights):
     if slot.dim() != 2:
         raise ValueError("slot must be [tokens, top_k]")
     tokens, top_k = slot.shape
-    _shaped(slot, (tokens, top_k), torch.int32, "slot")
+    _same(slot, (tokens, top_k), torch.int32, "slot")
     if weights is not None:
-        _shaped(weights, (tokens, top_k), torch.float32, "weights")
+        _same(weights, (tokens, top_k), torch.float32, "weights")
     return tokens, top_k
 
 
@@ -649,9 +667,11 @@ def combine(y, slot, weights=None, residual=None, out_dtype=None, out=None):
     tokens, top_k = _slots(slot, weights)
     y_ld = _rows(y, "y")
     rows, cols = y.shape
+    out_ld = 0
     if out is None:
-        out = torch.empty((tokens, cols), dtype=out_dtype or y.dtype, device=y.device)
-    out_ld = _rows(out, "out", (tokens, cols), out_dtype)
+        out = _new(y.device, out_dtype or y.dtype, tokens, cols)
+    else:
+        out_ld = _rows(out, "out", (tokens, cols), out_dtype)
     res_ld = _rows(residual, "residual", (tokens, cols), out.dtype) if residual is not None else 0
     _check("mx_combine", lib().mx_combine(
         _ptr(y), _dtype_code(y), rows, cols, y_ld, _ptr(slot), _ptr(weights), tokens, top_k, _ptr(residual), res_ld,
@@ -673,13 +693,15 @@ def combine_bwd(dout, y, slot, weights=None, used_rows=None, dy=None, dweights=N
     dout_ld = _rows(dout, "dout", (tokens, cols))
     if used_rows is not None:
         _index_vector(used_rows, "used_rows", min_numel=1)
+    dy_ld = 0
     if dy is None:
-        dy = torch.empty((rows, cols), dtype=y.dtype, device=y.device)
-    dy_ld = _rows(dy, "dy", (rows, cols), y.dtype)
+        dy = _new(y.device, y.dtype, rows, cols)
+    else:
+        dy_ld = _rows(dy, "dy", (rows, cols), y.dtype)
     if dweights is not None:
-        _shaped(dweights, (tokens, top_k), torch.float32, "dweights")
+        _same(dweights, (tokens, top_k), torch.float32, "dweights")
     elif need_dweights:
-        dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=y.device)
+        dweights = torch.empty_like(slot, dtype=torch.float32)
     _check("mx_combine_bwd", lib().mx_combine_bwd(
         _ptr(dout), _dtype_code(dout), dout_ld, _ptr(y), _dtype_code(y), rows, cols, y_ld, _ptr(slot),
         _ptr(weights), tokens, top_k, _ptr(used_rows), _ptr(dy), dy_ld, _ptr(dweights), _stream()))

@@ -101,6 +101,22 @@ def test_a_norm_that_is_not_finite_leaves_the_values(bad):
         assert tt.equal(tt.nan_to_num(g, nan=123.0), tt.nan_to_num(k, nan=123.0))
 
 
+def test_offsets_past_32_bits():
+    """One tensor of more than 2^32 bytes and 2^31 elements."""
+    tt = torch()
+    n = 2 ** 31 + 12_345
+    g = tt.zeros(n, dtype=tt.bfloat16, device="cuda")
+    at = [0, 2 ** 30 + 1, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 4097, n - 1]
+    for i, a in enumerate(at):
+        g[a] = float(i + 1)
+    norm = math.sqrt(sum((i + 1) ** 2 for i in range(len(at))))
+    out = tt.full_like(g, 7.0)
+    assert abs(float(mx.grad_clip([g], norm / 2, outs=[out])) - norm) <= 2.0 ** -23 * norm
+    assert int((out != 0).sum()) == len(at)
+    for i, a in enumerate(at):
+        assert abs(float(out[a]) - (i + 1) * 0.5) <= 2.0 ** -8 * (i + 1)
+
+
 @pytest.mark.parametrize("bf16", [0, 1])
 def test_views_off_their_alignment(bf16):
     tt = torch()

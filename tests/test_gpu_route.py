@@ -273,6 +273,26 @@ def test_many_tokens(experts, k, groups, best):
     assert (dl - want).abs().max() <= D_TOL * dw.abs().max()
 
 
+@pytest.mark.parametrize("experts,groups,top_groups,k", [(192, 64, 20, 8), (255, 51, 7, 6), (250, 50, 50, 3),
+                                                         (256, 64, 9, 8), (96, 48, 3, 4), (66, 33, 2, 4),
+                                                         (48, 12, 5, 7), (256, 2, 1, 5)])
+def test_many_and_few_tokens_agree(experts, groups, top_groups, k):
+    """The variants for many and for few tokens choose alike, bit for bit, up
+    to the largest number of groups."""
+    tt = torch()
+    x = tt.randn((8300, experts), device="cuda", generator=tt.Generator("cuda").manual_seed(groups))
+    x[::5, ::2] = -INF
+    bias = tt.linspace(-0.05, 0.05, experts, device="cuda")
+    for best in (1, 2):
+        kw = dict(score=mx.SIGMOID, bias=bias, groups=groups, top_groups=top_groups, group_best=best)
+        ids, w = mx.route(x, k, **kw)
+        parts = [mx.route(part, k, **kw) for part in (x[:4000], x[4000:])]
+        assert tt.equal(ids, tt.cat([p[0] for p in parts])) and tt.equal(w, tt.cat([p[1] for p in parts]))
+        of = ids.clamp(min=0) // (experts // groups)
+        taken = tt.zeros((8300, groups), dtype=tt.bool, device="cuda").scatter_(1, of.long(), ids >= 0)
+        assert (taken.sum(1) <= top_groups).all()
+
+
 @pytest.mark.parametrize("tokens,k", [(0, 2), (1, 1), (1, 4), (9, 7), (63, 1), (16, 4), (65, 1), (341, 3), (1025, 1),
                                       (700, 3), (5000, 4), (40000, 8)])
 @pytest.mark.parametrize("experts", [1, 3, 32, 33, 256, 1024])
