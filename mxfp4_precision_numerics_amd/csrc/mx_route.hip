@@ -567,15 +567,15 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
 // the same every run.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024, PLAN_WAVES = PLAN_THREADS / 64;
-constexpr int PLAN_BINS = MAX_EXPERTS + 4;   // rounded up to whole 16-byte pieces
+constexpr int PLAN_BINS = MAX_EXPERTS + 1;
 constexpr int PLAN_ALONE = 2048;             // assignments that one workgroup sorts by itself
-constexpr int PLAN_AHEAD = 8;                // loads of counts in flight
+constexpr int PLAN_AHEAD = 16;               // loads of counts in flight
 
 struct PlanArgs {
     const int32_t* ids;
     int64_t assignments;
     int top_k, experts;
-    int pitch;                // words of a workgroup's counts, a multiple of 4
+    int pitch;                // words of a workgroup's counts: experts, rounded up to a multiple of 4
     int64_t chunk;            // assignments of a workgroup, a multiple of a tile
     int blocks;               // workgroups with assignments
     int32_t* counts;          // [workgroups][pitch]
@@ -589,7 +589,7 @@ __device__ __forceinline__ int plan_bin(const PlanArgs& a, int64_t i) {
 
 __global__ __launch_bounds__(PLAN_THREADS) void plan_count_kernel(PlanArgs a) {
     __shared__ int hist[PLAN_BINS];
-    for (int e = threadIdx.x; e < a.pitch; e += PLAN_THREADS) hist[e] = 0;
+    for (int e = threadIdx.x; e <= a.experts; e += PLAN_THREADS) hist[e] = 0;
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(begin + a.chunk, a.assignments);
     for (int64_t i = begin + threadIdx.x; i < end; i += 2 * PLAN_THREADS) {
@@ -599,7 +599,8 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_count_kernel(PlanArgs a) {
         if (f >= 0) atomicAdd(&hist[f], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.pitch; e += PLAN_THREADS) a.counts[(int64_t)blockIdx.x * a.pitch + e] = hist[e];
+    for (int e = threadIdx.x; e < a.pitch; e += PLAN_THREADS)
+        a.counts[(int64_t)blockIdx.x * a.pitch + e] = e < a.experts ? hist[e] : 0;
 }
 
 // Exclusive prefix sums of n counts in LDS, by one wave: each lane sums a run
@@ -626,48 +627,67 @@ __device__ __forceinline__ void wave_scan(const int* in, int* out, int n) {
 // A tile is Q rounds of 64 assignments for each wave.
 template <int Q>
 __global__ __launch_bounds__(PLAN_THREADS) void plan_scatter_kernel(PlanArgs a) {
-    __shared__ int total[PLAN_BINS], before[PLAN_BINS], base[PLAN_BINS];
-    __shared__ uint16_t wave_count[PLAN_WAVES][PLAN_BINS];
+    __shared__ int total[PLAN_BINS], before[PLAN_BINS], base[PLAN_BINS], before_all;
+    union Scratch {
+        uint16_t wave_count[PLAN_WAVES][PLAN_BINS + 3];
+        int4 sums[2][PLAN_WAVES][64];         // of 256 experts: over all workgroups, over those before this one
+    };
+    __shared__ Scratch scratch;
+    auto& wave_count = scratch.wave_count;
     constexpr int TILE = PLAN_THREADS * Q;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int bins = a.experts + 1;
-    for (int e = tid; e < a.pitch; e += PLAN_THREADS) total[e] = before[e] = 0;
+    for (int e = tid; e < bins; e += PLAN_THREADS) total[e] = before[e] = 0;
     __syncthreads();
     if (a.blocks <= 1) {                      // one workgroup counts for itself
         for (int64_t i = tid; i < a.assignments; i += PLAN_THREADS) atomicAdd(&total[plan_bin(a, i)], 1);
     } else {
-        // the counts of all workgroups and of those before this one, four bins
-        // a thread; the threads left over take other workgroups
-        const int quads = a.pitch / 4, share = PLAN_THREADS / quads, part = tid / quads;
-        const int4* counts = (const int4*)a.counts + (tid - part * quads);
-        int4 all = {0, 0, 0, 0}, mine = {0, 0, 0, 0};
-        for (int b0 = part < share ? part : a.blocks; b0 < a.blocks; b0 += PLAN_AHEAD * share) {
-            int4 n[PLAN_AHEAD];
+        // a wave takes every 16th workgroup's counts, four experts a lane, with
+        // PLAN_AHEAD of them under way at once; then the waves' sums are added
+        const int quads = a.pitch / 4;
+        for (int q0 = 0; q0 < quads; q0 += 64) {
+            const int quad = min(q0 + lane, quads - 1);
+            int4 all = {0, 0, 0, 0}, mine = {0, 0, 0, 0};
+            for (int b0 = wave; b0 < a.blocks; b0 += PLAN_AHEAD * PLAN_WAVES) {
+                int4 n[PLAN_AHEAD];
 #pragma unroll
-            for (int i = 0; i < PLAN_AHEAD; ++i)
-                n[i] = b0 + i * share < a.blocks ? counts[(int64_t)(b0 + i * share) * quads] : make_int4(0, 0, 0, 0);
+                for (int i = 0; i < PLAN_AHEAD; ++i)
+                    n[i] = ((const int4*)a.counts)[(int64_t)min(b0 + i * PLAN_WAVES, a.blocks - 1) * quads + quad];
 #pragma unroll
-            for (int i = 0; i < PLAN_AHEAD; ++i) {
-                all.x += n[i].x; all.y += n[i].y; all.z += n[i].z; all.w += n[i].w;
-                if (b0 + i * share < (int)blockIdx.x) {
+                for (int i = 0; i < PLAN_AHEAD; ++i) {
+                    const int b = b0 + i * PLAN_WAVES;
+                    if (b >= a.blocks) continue;
+                    all.x += n[i].x; all.y += n[i].y; all.z += n[i].z; all.w += n[i].w;
+                    if (b >= (int)blockIdx.x) continue;
                     mine.x += n[i].x; mine.y += n[i].y; mine.z += n[i].z; mine.w += n[i].w;
                 }
             }
-        }
-        if (part < share) {
-            const int e = 4 * (tid - part * quads);
-            atomicAdd(&total[e], all.x); atomicAdd(&total[e + 1], all.y);
-            atomicAdd(&total[e + 2], all.z); atomicAdd(&total[e + 3], all.w);
-            atomicAdd(&before[e], mine.x); atomicAdd(&before[e + 1], mine.y);
-            atomicAdd(&before[e + 2], mine.z); atomicAdd(&before[e + 3], mine.w);
+            scratch.sums[0][wave][lane] = all;
+            scratch.sums[1][wave][lane] = mine;
+            __syncthreads();
+            const int which = tid >> 8, e = 4 * q0 + (tid & 255);
+            if (which < 2 && e < a.experts) {
+                int sum = 0;
+#pragma unroll
+                for (int w = 0; w < PLAN_WAVES; ++w) sum += ((const int*)scratch.sums[which][w])[tid & 255];
+                (which ? before : total)[e] = sum;
+            }
+            __syncthreads();
         }
     }
     __syncthreads();
     if (wave == 0) wave_scan(total, base, bins);
+    if (wave == 1) {                          // what is not some expert's lies in the last bin
+        int sum = 0;
+        for (int e = lane; e < a.experts; e += 64) sum += before[e];
+#pragma unroll
+        for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+        if (lane == 0) before_all = sum;
+    }
     __syncthreads();
     for (int e = tid; e < bins; e += PLAN_THREADS) {
         if (blockIdx.x == 0) a.offsets[e] = base[e];
-        base[e] += before[e];
+        base[e] += e < a.experts ? before[e] : (int)((int64_t)blockIdx.x * a.chunk) - before_all;
     }
     const int64_t begin = (int64_t)blockIdx.x * a.chunk, end = min(begin + a.chunk, a.assignments);
     for (int64_t at = begin; at < end; at += TILE) {
@@ -732,7 +752,7 @@ PlanShape plan_shape(int64_t n) {
     const int64_t chunk = tile * (n <= PLAN_ALONE ? tiles : ceil_div(tiles, 256));
     return {rounds, chunk, ceil_div(n, chunk)};
 }
-int plan_pitch(int experts) { return (experts + 1 + 3) & ~3; }
+int plan_pitch(int experts) { return (experts + 3) & ~3; }
 
 template <bool B, int L, int C>
 void launch_route(RouteArgs a, hipStream_t s) {

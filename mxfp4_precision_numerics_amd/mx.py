@@ -543,13 +543,13 @@ def _rows(t, name, shape=None, dtype=None):
     in elements (0 when the rows are contiguous)."""
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError("%s: expected shape %s, got %s" % (name, shape or "[rows, cols]", tuple(t.shape)))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
-    rows, cols = t.shape
-    if rows == 0:
+    if t.is_contiguous():
         return 0
+    rows, cols = t.shape
     ld = t.stride(0)
     if (cols > 1 and t.stride(1) != 1) or (rows > 1 and ld < cols):
         raise ValueError("%s must have contiguous rows that do not overlap" % name)
