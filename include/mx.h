@@ -472,8 +472,10 @@ mx_status mx_route_plan(const int32_t* ids, int64_t tokens, int32_t top_k, int32
  * 1 (the gradient of the gather of tokens into grouped order).  residual
  * [tokens x cols] of out's type, or NULL; it may be out itself.  out
  * [tokens x cols], ot fp32 or bf16 whatever y's type.
- * Any cols >= 1 and any pitch; rows <= 2^31 - 1, tokens * top_k <
- * 2^31.  Device pointers owned by the caller, aligned to their elements.
+ * Any cols >= 1 and any pitch; rows <= 2^31 - 1, tokens * top_k < 2^31, and
+ * at most 2^25 pieces of 1 KiB in y's type over the tokens' rows (5.5 million
+ * tokens of 2880 bf16 columns).  Device pointers owned by the caller,
+ * aligned to their elements.
  * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
  * MX_ERR_LAUNCH.  tokens == 0 launches nothing. */
 mx_status mx_combine(const void* y, mx_dtype yt, int64_t rows, int64_t cols, int64_t y_ld, const int32_t* slot,
@@ -492,7 +494,7 @@ mx_status mx_combine(const void* y, mx_dtype yt, int64_t rows, int64_t cols, int
  * used_rows (DEVICE int32[1], or NULL): rows of dy from *used_rows on are set
  * to 0, and a slot that names one of them counts as none (pass the plan's
  * offsets + experts); with NULL rows that no slot names are not written.
- * Errors as mx_combine. */
+ * tokens < 2^23.  Errors as mx_combine. */
 mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const void* y, mx_dtype yt, int64_t rows,
                          int64_t cols, int64_t y_ld, const int32_t* slot, const float* weights, int64_t tokens,
                          int32_t top_k, const int32_t* used_rows, void* dy, int64_t dy_ld, float* dweights,

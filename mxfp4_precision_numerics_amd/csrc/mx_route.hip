@@ -35,9 +35,10 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------------------
-// Reductions over the L lanes (8, 16, 32 or 64) that share a row.  Within 16
-// lanes a rotation by a DPP row costs one move; between the 16-lane rows of a
-// wave a shuffle.  Every lane gets the result, in a fixed order.
+// Reductions over the L lanes (8, 16, 32 or 64) that share a row: exchanges
+// with the neighbour, the other pair, the other quad and the other eight are
+// DPP moves, the wider ones shuffles.  Every lane gets the result, in a fixed
+// order.
 // ---------------------------------------------------------------------------
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
@@ -376,7 +377,7 @@ __device__ __forceinline__ void row_largest(double* key, double* list) {
 
 // Bound by the vector units: for 256 experts in groups about 190 instructions
 // a row, of which the keys' sort is a third.  65536 tokens, top 8 of 256 fp32
-// in 8 groups: 29 us (2.4 TB/s read; 21 us of it the instructions alone);
+// in 8 groups: 28 us (2.4 TB/s read; 21 us of it the instructions alone);
 // without bias and groups 17 us (4.1 TB/s).  16384 tokens, top 4 of 32: 3.6 us.
 // K = 8: up to eight experts by the merged lists; K = 0: any number, one row
 // maximum after the other.

@@ -102,9 +102,17 @@ def _check(fn, code):
 # ---------------------------------------------------------------------------
 # torch plumbing
 # ---------------------------------------------------------------------------
+_torch_module = _dtype_codes = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported at the first call that needs it."""
+    global _torch_module, _dtype_codes
+    if _torch_module is None:
+        import torch
+        _dtype_codes = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -114,17 +122,16 @@ def _ptr(t):
 def _stream():
     # the current device's current stream as a handle; building a
     # torch.cuda.Stream for it would take ten times as long
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    C = _torch()._C
+    return C._cuda_getCurrentRawStream(C._cuda_getDevice())
 
 
 def _dtype_code(t):
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return MX_F32
-    if t.dtype == torch.bfloat16:
-        return MX_BF16
-    raise TypeError("expected float32 or bfloat16, got %s" % t.dtype)
+    _torch()
+    try:
+        return _dtype_codes[t.dtype]
+    except KeyError:
+        raise TypeError("expected float32 or bfloat16, got %s" % t.dtype) from None
 
 
 def _dev(t, name):
@@ -711,8 +718,7 @@ def combine_bwd(dout, y, slot, weights=None, used_rows=None, dy=None, dweights=N
 def _grad_list(grads, name):
     """The host arrays of a gradient list (any shapes, contiguous, fp32 and
     bf16 mixed)."""
-    torch = _torch()
-    codes = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}
+    codes = _dtype_codes
     grads = list(grads)
     if not all([g.is_cuda and g.is_contiguous() for g in grads]):
         raise ValueError("%s must be contiguous device tensors" % name)

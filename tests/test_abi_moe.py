@@ -79,7 +79,7 @@ def test_combine_validation(L):
                   rld=0, out=FAKE, ot=mx.MX_F32, old=0, s=None)
     assert call(yt=5) == DTYPE and call(ot=-1) == DTYPE
     for bad in (dict(rows=-1), dict(rows=2 ** 31), dict(cols=0), dict(yld=63), dict(t=-1), dict(k=0), dict(rld=1),
-                dict(old=63), dict(t=2 ** 30, k=2)):
+                dict(old=63), dict(t=2 ** 30, k=2), dict(t=2 ** 26, k=1), dict(t=2 ** 20, cols=2 ** 15)):
         assert call(**bad) == SHAPE, bad
     for name in ("y", "slot", "out"):
         assert call(**{name: None}) == NULL
@@ -92,7 +92,8 @@ def test_combine_bwd_validation(L):
     call = caller(L.mx_combine_bwd, do=FAKE, dt=mx.MX_BF16, dld=0, y=FAKE, yt=mx.MX_BF16, rows=16, cols=64, yld=0,
                   slot=FAKE, w=FAKE, t=4, k=4, used=None, dy=FAKE, dyld=0, dw=FAKE, s=None)
     assert call(dt=9) == DTYPE and call(yt=9) == DTYPE
-    for bad in (dict(rows=-1), dict(cols=0), dict(yld=63), dict(dld=63), dict(dyld=63), dict(t=-1), dict(k=0)):
+    for bad in (dict(rows=-1), dict(cols=0), dict(yld=63), dict(dld=63), dict(dyld=63), dict(t=-1), dict(k=0),
+                dict(t=2 ** 23)):
         assert call(**bad) == SHAPE, bad
     for name in ("do", "y", "slot", "dy"):
         assert call(**{name: None}) == NULL
@@ -107,7 +108,7 @@ def test_grad_validation(L):
         return ((ctypes.c_void_p * n)(*ptrs), (ctypes.c_int * n)(*types), (ctypes.c_int64 * n)(*numels), n)
 
     good = arrays([0, 1], [5, 6], [FAKE, FAKE])
-    outs = (ctypes.c_void_p * 2)(FAKE, FAKE)
+    outs = (ctypes.c_void_p * 9)(*[FAKE] * 9)
 
     def norm(a=good, ws=FAKE, out=FAKE):
         return L.mx_grad_norm(*a, ws, out, None)
@@ -120,6 +121,8 @@ def test_grad_validation(L):
         assert call(a=arrays([0, 0], [5, -1], [FAKE, FAKE])) == SHAPE
         assert call(a=arrays([0, 0], [2 ** 40, 1], [FAKE, FAKE])) == SHAPE
         assert call(a=arrays([0, 0], [2 ** 62, 2 ** 62], [FAKE, FAKE])) == SHAPE
+        assert call(a=arrays([0], [2 ** 34 + 1], [FAKE])) == SHAPE          # over 64 GB in one tensor
+        assert call(a=arrays([1] * 9, [2 ** 34] * 9, [FAKE] * 9)) == SHAPE  # over 2^37 elements
         assert call(a=arrays([0, 0], [5, 6], [FAKE, None])) == NULL
         assert call(a=arrays([0, 1], [5, 6], [FAKE + 2, FAKE])) == ALIGN
         assert call(a=(None, good[1], good[2], 2)) == NULL
