@@ -143,6 +143,16 @@ def test_rows_that_no_token_names_do_not_matter():
     assert np.isnan(out).all()
 
 
+def test_no_tokens():
+    tt = torch()
+    y = tt.ones((6, 40), device="cuda")
+    slot = tt.zeros((0, 4), dtype=tt.int32, device="cuda")
+    assert mx.combine(y, slot).shape == (0, 40)
+    dy, dw = mx.combine_bwd(tt.zeros((0, 40), device="cuda"), y, slot, used_rows=dev(np.array([2], np.int32)),
+                            dy=tt.full((6, 40), 7.0, device="cuda"))
+    assert dw.shape == (0, 4) and (dy[:2] == 7.0).all() and not dy[2:].any()
+
+
 def test_gradient_of_the_token_gather():
     """weights None sums the gradients that the experts' copies of a token
     send back; against the plan that gathered them."""

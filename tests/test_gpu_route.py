@@ -316,6 +316,29 @@ def test_plan(tokens, k, experts):
             assert np.array_equal(a, b)
 
 
+def test_no_tokens():
+    tt = torch()
+    x = tt.zeros((0, 32), device="cuda")
+    ids, w = mx.route(x, 4)
+    assert ids.shape == (0, 4) and w.shape == (0, 4)
+    assert mx.route_bwd(x, ids, w).shape == (0, 32)
+
+
+@pytest.mark.parametrize("tokens", [5, 9000])
+@pytest.mark.parametrize("experts", [64, 100, 256])
+def test_bias_off_its_alignment(tokens, experts):
+    tt = torch()
+    gen = tt.Generator("cuda").manual_seed(experts)
+    x = tt.randn((tokens, experts), device="cuda", generator=gen)
+    bias = 0.1 * tt.randn(experts + 3, device="cuda", generator=gen)
+    for at in (1, 2, 3):
+        part = bias[at:at + experts]
+        assert part.data_ptr() % 16
+        for score in (0, 1):
+            a, b = (mx.route(x, 6, score=score, bias=v) for v in (part, part.clone()))
+            assert tt.equal(a[0], b[0]) and tt.equal(a[1], b[1])
+
+
 def test_plan_of_one_expert_and_of_none():
     for value in (-1, 0, 31):
         ids = np.full((3000, 2), value, dtype=np.int32)
