@@ -488,9 +488,9 @@ mx_status mx_combine(const void* y, mx_dtype yt, int64_t rows, int64_t cols, int
  * mx_quantize_1d and mx_quantize_1d_dual read; and dweights[t][j] =
  * <dout[t], y[s]> summed in fp32 in a fixed order (0 without a slot).
  * dout [tokens x cols] (dt), y and dy [rows x cols] (yt), pitches in
- * elements, 0 = cols.  dweights may be NULL (y is then not read and may be
- * NULL); weights may be NULL for 1.  Slots of different assignments are
- * different, as mx_route_plan makes them.
+ * elements, 0 = cols.  dy may be y itself, at the same pitch.  dweights may
+ * be NULL (y is then not read and may be NULL); weights may be NULL for 1.
+ * Slots of different assignments are different, as mx_route_plan makes them.
  * used_rows (DEVICE int32[1], or NULL): rows of dy from *used_rows on are set
  * to 0, and a slot that names one of them counts as none (pass the plan's
  * offsets + experts); with NULL rows that no slot names are not written.

@@ -227,6 +227,7 @@ __device__ __forceinline__ void bwd_piece(const CombineBwdArgs& a, int64_t t, in
     Piece<YB, V> f[FLIGHT];
     d.template load<FULL, false>(a.dout, t * a.dout_ld + col, left);
     if (a.dweights) {
+        // (before any store: dy may be y)
 #pragma unroll
         for (int j = 0; j < FLIGHT; ++j)
             if (n.slot[j] >= 0) f[j].template load<FULL, STREAM>(a.y, n.slot[j] * a.y_ld + col, left);
@@ -281,9 +282,9 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void combine_bwd_kernel(CombineBwdA
         if ((tid & 15) == 0) part[tid >> 6][(tid >> 4) & 3] = sum;
         __syncthreads();
         if (tid < FLIGHT && j0 + tid < a.top_k) {
-            float sum = 0.0f;
-            for (int w = 0; w < threads / 64; ++w) sum += part[w][tid];
-            a.dweights[t * a.top_k + j0 + tid] = sum;
+            float total = 0.0f;
+            for (int w = 0; w < threads / 64; ++w) total += part[w][tid];
+            a.dweights[t * a.top_k + j0 + tid] = total;
         }
     }
 }

@@ -691,7 +691,7 @@ def combine_bwd(dout, y, slot, weights=None, used_rows=None, dy=None, dweights=N
     [tokens, top_k]) from dout [tokens, cols] (see mx_combine_bwd).
     used_rows: an int32 device tensor of one element, the number of rows that
     slots name (the plan's offsets[-1:]); the rows of dy after it become 0.
-    Without it rows that no slot names are left unwritten.
+    Without it rows that no slot names are left unwritten.  dy may be y.
     need_dweights=False: dweights is None and y is not read."""
     torch = _torch()
     tokens, top_k = _slots(slot, weights)

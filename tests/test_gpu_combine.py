@@ -143,6 +143,20 @@ def test_rows_that_no_token_names_do_not_matter():
     assert np.isnan(out).all()
 
 
+@pytest.mark.parametrize("cols", [96, 2880, 1001])
+def test_gradient_in_place_of_y(cols):
+    tt = torch()
+    _, y = values((420, cols), tt.bfloat16, 20)
+    _, dout = values((100, cols), tt.bfloat16, 21)
+    slot = dev(slots_of(100, 4, 400, 22))
+    w = dev(np.random.default_rng(23).normal(size=(100, 4)).astype(np.float32))
+    used = dev(np.array([400], np.int32))
+    named = host(slot)[(host(slot) >= 0) & (host(slot) < 400)]
+    dy, dw = mx.combine_bwd(dout, y, slot, w, used_rows=used)
+    same, dw2 = mx.combine_bwd(dout, y, slot, w, used_rows=used, dy=y)
+    assert same is y and tt.equal(dw, dw2) and tt.equal(y[named], dy[named]) and not y[400:].any()
+
+
 def test_no_tokens():
     tt = torch()
     y = tt.ones((6, 40), device="cuda")
