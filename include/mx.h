@@ -1,6 +1,6 @@
 /*
  * mx.h -- C ABI of libmx355, the MXFP4 quantize-then-contract path on AMD
- * MI355X (gfx950).
+ * MI355X (gfx950), and the routing, combine and clipping operators around it.
  *
  * The path is the one the pages train a mixture-of-experts LLM with
  * ("Training an MoE LLM in MXFP4: How We Closed the Gap to BF16", Abstract):
