@@ -78,6 +78,12 @@ CASES = [
     (13, 513, 4, "f32", 0, False, 1, 1, 1, True, 1.0, 1),
     (11, 1000, 32, "f32", 1, True, 4, 2, 2, False, 1.0, 0),
     (11, 1024, 12, "bf16", 0, True, 16, 5, 2, True, 1.0, 0),
+    (19, 300, 6, "f32", 1, False, 1, 1, 1, True, 1.0, 0),
+    (19, 384, 8, "bf16", 0, True, 8, 3, 2, False, 1.0, 8),
+    (19, 512, 4, "f32", 0, False, 1, 1, 1, False, 1.0, 2),
+    (10, 1024, 8, "bf16", 1, True, 1, 1, 1, True, 1.0, 0),
+    (10, 777, 5, "f32", 0, False, 7, 3, 1, True, 1.0, 0),
+    (23, 128, 1, "bf16", 1, False, 1, 1, 1, False, 1.0, 0),
 ]
 
 
@@ -294,7 +300,7 @@ def test_many_and_few_tokens_agree(experts, groups, top_groups, k):
 
 
 @pytest.mark.parametrize("tokens,k", [(0, 2), (1, 1), (1, 4), (9, 7), (63, 1), (16, 4), (65, 1), (341, 3), (1025, 1),
-                                      (700, 3), (5000, 4), (40000, 8)])
+                                      (700, 3), (5000, 4), (40000, 8), (100001, 8)])
 @pytest.mark.parametrize("experts", [1, 3, 32, 33, 256, 1024])
 def test_plan(tokens, k, experts):
     rng = np.random.default_rng(tokens * 1000 + experts)
