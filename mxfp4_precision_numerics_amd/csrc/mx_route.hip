@@ -788,11 +788,12 @@ void launch_route(const RouteBwdArgs& a, hipStream_t s) {
 }
 
 // The lanes that share a row and the chunks of four experts each holds: enough
-// for the experts, and a lane for each chosen one.  With many tokens eight
-// lanes take a row: of the steps between lanes there is one less, for twice
-// the rows.  With few tokens 16 lanes, whose waves are done sooner.  Both
-// directions, 16 / 8 lanes, top 8 of 256: 6.7 / 7.7 us at 4096 tokens,
-// 8.7 / 8.5 at 8192, 36.9 / 35.9 at 65536; of 64: 18.1 / 14.4 there.
+// for the experts, and a lane for each chosen one.  With many tokens half as
+// many lanes take a row: there is one step less between lanes, for twice the
+// rows.  With few tokens twice the waves are done sooner.  Both directions,
+// few / many tokens' lanes, top 8 of 256: 6.7 / 7.7 us at 4096 tokens,
+// 8.7 / 8.5 at 8192, 36.9 / 35.9 at 65536; there of 64: 18.1 / 14.4, of 512:
+// 58.4 / 52.7, of 1024: 114 / 100.
 constexpr int64_t MANY_TOKENS = 8192;
 
 template <bool B, class A>
@@ -803,6 +804,8 @@ void dispatch_route(const A& a, hipStream_t s) {
     else if (e <= 64 && many) launch_route<B, 8, 2>(a, s);
     else if (e <= 128 && many) launch_route<B, 8, 4>(a, s);
     else if (e <= 256 && many) launch_route<B, 8, 8>(a, s);
+    else if (e <= 512 && many) launch_route<B, 16, 8>(a, s);
+    else if (many) launch_route<B, 32, 8>(a, s);
     else if (e <= 64 && k <= 16) launch_route<B, 16, 1>(a, s);
     else if (e <= 128 && k <= 16) launch_route<B, 16, 2>(a, s);
     else if (e <= 256 && k <= 16) launch_route<B, 16, 4>(a, s);

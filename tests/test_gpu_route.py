@@ -231,7 +231,8 @@ def test_many_rows():
     assert (dl - want).abs().max() <= D_TOL * 2.0 * dw.abs().max()
 
 
-@pytest.mark.parametrize("experts,k", [(32, 8), (61, 3), (64, 4), (64, 7), (100, 5), (128, 2), (200, 4), (256, 8), (256, 1)])
+@pytest.mark.parametrize("experts,k", [(32, 8), (61, 3), (64, 4), (64, 7), (100, 5), (128, 2), (200, 4), (256, 8), (256, 1),
+                                       (300, 5), (512, 8), (512, 2), (516, 4), (1024, 8), (1000, 3)])
 @pytest.mark.parametrize("groups,best", [(1, 1), (4, 2)])
 def test_many_tokens(experts, k, groups, best):
     """The variants for many tokens, with a bias, groups and masked experts,
@@ -281,7 +282,8 @@ def test_many_tokens(experts, k, groups, best):
 
 @pytest.mark.parametrize("experts,groups,top_groups,k", [(192, 64, 20, 8), (255, 51, 7, 6), (250, 50, 50, 3),
                                                          (256, 64, 9, 8), (96, 48, 3, 4), (66, 33, 2, 4),
-                                                         (48, 12, 5, 7), (256, 2, 1, 5)])
+                                                         (48, 12, 5, 7), (256, 2, 1, 5), (448, 64, 11, 8),
+                                                         (512, 64, 30, 3), (960, 64, 5, 8), (1023, 33, 4, 5)])
 def test_many_and_few_tokens_agree(experts, groups, top_groups, k):
     """The variants for many and for few tokens choose alike, bit for bit, up
     to the largest number of groups."""
