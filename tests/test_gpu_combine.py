@@ -130,6 +130,22 @@ def test_combine_gradient(case, cleared):
         assert tt.equal(again.cpu()[mine], expect[mine])
 
 
+# more rows a token than a wave reads at once, over columns that leave its last piece ragged or only one to three of
+# its lanes with a piece (8 bf16 or 4 fp32 elements each, 64 lanes)
+MANY = ([(k, cols, "bf16") for k in (5, 8, 9, 17) for cols in (1, 7, 8, 24, 513, 520, 1001, 2056)] +
+        [(k, cols, "f32") for k in (5, 8, 9, 17) for cols in (1, 3, 4, 12, 257, 260, 1001, 1028)])
+
+
+@pytest.mark.parametrize("k,cols,dtype", MANY)
+@pytest.mark.parametrize("residual", [False, True])
+def test_many_rows_a_token(k, cols, dtype, residual):
+    rows = 13 * k - (9 if residual else 0)
+    out = {"bf16": "f32", "f32": "bf16"}[dtype] if residual else dtype
+    case = (13, k, rows, cols, dtype, out, k != 9, residual, cols % 3)
+    test_combine(case)
+    test_combine_gradient(case, cleared=residual)
+
+
 def test_rows_that_no_token_names_do_not_matter():
     tt = torch()
     y = tt.randn((8, 64), device="cuda", generator=tt.Generator("cuda").manual_seed(1))
