@@ -510,8 +510,9 @@ mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const v
  * mx_grad_clip: also multiplies by c = min(1, max_norm / (norm + 1e-6))
  * (rounded to fp32; each product rounded once to the tensor's type) into
  * outs[i], of the same type and count; outs NULL, or outs[i] == grads[i]:
- * in place.  A norm that is NaN or infinite leaves the values as they are
- * (outs gets copies): the caller sees it in *norm and drops the step.
+ * in place.  Where *norm is NaN or infinite, also because the norm of finite
+ * values passes fp32's range, the values stay as they are (outs gets copies):
+ * the caller sees it in *norm and drops the step.
  * max_norm >= 0.  workspace: mx_grad_workspace(count) bytes, 8-byte aligned,
  * contents irrelevant before and after.  Outputs may not overlap other
  * tensors.  At most 2^37 elements in all and 64 GB in one tensor.

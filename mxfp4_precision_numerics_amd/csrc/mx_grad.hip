@@ -206,10 +206,11 @@ template <bool STREAM>
 __global__ __launch_bounds__(THREADS) void scale_kernel(GradTable g, const double* partials, int n,
                                                         float max_norm, float* norm) {
     const double total = sqrt(sum_partials(partials, n));
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+    const float seen = (float)total;        // the norm that the caller gets
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = seen;
     const double ratio = (double)max_norm / (total + 1e-6);
-    // a norm that is not finite leaves the gradients as they are
-    const float coef = total - total == 0.0 && ratio < 1.0 ? (float)ratio : 1.0f;
+    // a norm that is not finite in fp32 leaves the gradients as they are
+    const float coef = seen - seen == 0.0f && ratio < 1.0 ? (float)ratio : 1.0f;
     const int c = xcd_order(blockIdx.x, gridDim.x), t = tensor_of(g, c);
     if (coef == 1.0f && g.src[t] == g.dst[t]) return;
     scale_chunk<STREAM>(Chunk(g, t, c), coef);

@@ -101,6 +101,24 @@ def test_a_norm_that_is_not_finite_leaves_the_values(bad):
         assert tt.equal(tt.nan_to_num(g, nan=123.0), tt.nan_to_num(k, nan=123.0))
 
 
+@pytest.mark.parametrize("count", [2, 9_000_000])
+def test_a_norm_past_fp32_leaves_the_values(count):
+    """Finite gradients whose norm is not: *norm is infinite, so the values
+    stay; the largest norm that fp32 holds still clips."""
+    tt = torch()
+    grads = [tt.full((count,), -1e34, device="cuda"), tt.tensor([3e38, 3e38], device="cuda"),
+             tt.tensor([1.0, 2.0 ** 127], dtype=tt.bfloat16, device="cuda")]
+    kept = [g.clone() for g in grads]
+    outs = [tt.zeros_like(g) for g in grads]
+    for max_norm in (1.0, 1e38):
+        assert float(mx.grad_clip(grads, max_norm, outs=outs)) == math.inf == float(mx.grad_norm(grads))
+        assert float(mx.grad_clip(grads, max_norm)) == math.inf
+        assert all(tt.equal(o, k) and tt.equal(g, k) for o, g, k in zip(outs, grads, kept))
+    most = tt.tensor([float(tt.finfo(tt.float32).max)], device="cuda")
+    assert float(mx.grad_clip([most], 1.0)) == float(tt.finfo(tt.float32).max)
+    assert abs(float(most) - 1.0) <= 2.0 ** -22
+
+
 def test_offsets_past_32_bits():
     """One tensor of more than 2^32 bytes and 2^31 elements."""
     tt = torch()
