@@ -389,7 +389,8 @@ mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const v
     const int v = yt == MX_BF16 ? 8 : 4;
     const int64_t clear = used_rows && rows > 0 ? min(rows, (int64_t)1024) : 0;
     if (tokens + clear == 0) return MX_OK;
-    if (tokens + clear >= ((int64_t)1 << 23)) return MX_ERR_SHAPE;     // 512 threads a workgroup at most
+    // (more than 512 tokens: at most 256 threads a workgroup, so with the clearing ones fewer than 2^32)
+    if (tokens >= ((int64_t)1 << 23)) return MX_ERR_SHAPE;
     // as few passes over the columns as the waves allow, and as few waves as these passes need; more waves
     // where there are few tokens (three / six for rows of 2880 bf16: 64 tokens 5.9 / 4.9 us, 256 6.4 / 5.4,
     // 1024 9.3 / 10.3, 16384 141 / 141)

@@ -238,6 +238,26 @@ def test_offsets_past_32_bits():
         assert (dy[r] == i + 2).all()
 
 
+def test_most_tokens_of_the_gradient():
+    """2^23 - 1 tokens, with rows to clear; one more is refused."""
+    tt = torch()
+    t, rows = 2 ** 23 - 1, 2 ** 23 + 5000
+    slot = (tt.arange(t, dtype=tt.int32, device="cuda") + 7).view(t, 1)
+    y = (tt.arange(rows, dtype=tt.float32, device="cuda") % 1024).view(rows, 1)
+    dout = (tt.arange(t, dtype=tt.float32, device="cuda") % 31).view(t, 1)
+    used = dev(np.array([t + 7 - 3], np.int32))            # the last three slots count as none
+    dy, dw = mx.combine_bwd(dout, y, slot, used_rows=used, dy=tt.full_like(y, 7.0))
+    want = tt.full_like(y, 7.0)
+    want[7:7 + t] = dout
+    want[t + 4:] = 0
+    assert tt.equal(dy, want)
+    want = dout * y[7:7 + t]
+    want[-3:] = 0
+    assert tt.equal(dw, want)
+    with pytest.raises(mx.MXError):
+        mx.combine_bwd(tt.zeros((t + 1, 1), device="cuda"), y, tt.zeros((t + 1, 1), dtype=tt.int32, device="cuda"))
+
+
 def test_other_stream_and_graph():
     tt = torch()
     gen = tt.Generator("cuda").manual_seed(8)
