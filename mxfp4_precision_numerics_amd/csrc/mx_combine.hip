@@ -349,9 +349,8 @@ mx_status mx_combine(const void* y, mx_dtype yt, int64_t rows, int64_t cols, int
     CombineArgs a{y, rows, cols, y_ld ? y_ld : cols, slot, weights, tokens, top_k, residual,
                   residual_ld ? residual_ld : cols, out, out_ld ? out_ld : cols, 0};
     const int v = yt == MX_BF16 ? 8 : 4;
-    if (tokens > ((int64_t)1 << 24)) return MX_ERR_SHAPE;
     a.chunks = ceil_div(cols, 64 * v);
-    if (a.chunks > ((int64_t)1 << 25) / tokens) return MX_ERR_SHAPE;
+    if (a.chunks > ((int64_t)1 << 25) / tokens) return MX_ERR_SHAPE;    // 2^31 threads at most
     const dim3 grid((uint32_t)ceil_div(tokens * a.chunks, 4));
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();

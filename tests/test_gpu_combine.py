@@ -238,6 +238,18 @@ def test_offsets_past_32_bits():
         assert (dy[r] == i + 2).all()
 
 
+def test_most_pieces():
+    """2^25 pieces of 1 KiB, one a token; one more is refused."""
+    tt = torch()
+    t = 2 ** 25
+    y = tt.arange(1, 1001, dtype=tt.float32, device="cuda").view(1000, 1)
+    slot = (tt.arange(t, dtype=tt.int32, device="cuda") % 1001).view(t, 1)     # (1000 names no row)
+    out = mx.combine(y, slot)
+    assert tt.equal(out.view(-1), tt.where(slot.view(-1) < 1000, slot.view(-1) + 1, 0).float())
+    with pytest.raises(mx.MXError):
+        mx.combine(y, tt.zeros((t + 1, 1), dtype=tt.int32, device="cuda"))
+
+
 def test_most_tokens_of_the_gradient():
     """2^23 - 1 tokens, with rows to clear; one more is refused."""
     tt = torch()
