@@ -222,9 +222,14 @@ __device__ __forceinline__ void wave_fence() {
 }
 
 // The two best of (b1 >= b2) and x: the median of the three is the new second.
-// A NaN x changes neither.
+// A NaN x (a quiet one: keys are results of additions) changes neither: the
+// instruction gives the least of the three but NaN.  The builtin will not do:
+// with a constant -inf as b2 the compiler makes it the minimum of b1 and x,
+// which is b1 for a NaN.
 __device__ __forceinline__ void best_two(float& b1, float& b2, float x) {
-    b2 = __builtin_amdgcn_fmed3f(b1, b2, x);
+    float second;
+    asm("v_med3_f32 %0, %1, %2, %3" : "=v"(second) : "v"(b1), "v"(b2), "v"(x));
+    b2 = second;
     b1 = fmaxf(b1, x);
 }
 

@@ -180,6 +180,29 @@ def test_nan_and_infinite_logits():
         assert (np.sort(ids[:, :2], axis=1) == [30, 31]).all() and (ids[:, 2:] == -1).all()
 
 
+@pytest.mark.parametrize("tokens", [40, 8200])
+@pytest.mark.parametrize("experts,groups,best", [(64, 8, 2), (64, 16, 2), (60, 5, 2), (250, 10, 2), (256, 8, 2), (256, 8, 1),
+                                                 (512, 64, 2), (1024, 8, 2)])
+def test_nan_keys_add_nothing_to_their_groups(tokens, experts, groups, best):
+    """NaN logits in every place of a group, under sigmoid scores with a bias
+    of their own; rows whose 64-bit keys or group sums come closer than fp32
+    can order are left out."""
+    rng = np.random.default_rng(experts + groups)
+    x = rng.normal(size=(tokens, experts)).astype(np.float32)
+    x[rng.random(x.shape) < np.array([0.1, 0.5, 0.9])[np.arange(tokens) % 3, None]] = float("nan")
+    bias = (0.01 * rng.integers(-9, 10, experts)).astype(np.float32)
+    top = max(1, groups // 2)
+    k = min(8, top * (experts // groups))
+    ids = host(mx.route(dev(x), k, score=mx.SIGMOID, bias=dev(bias), groups=groups, top_groups=top, group_best=best)[0])
+    tested = 0
+    for r in range(40):
+        want, _, margin = moe.route_row(x[r].astype(np.float64), k, mx.SIGMOID, bias, groups, top, best)
+        if margin > KEY_TOL:
+            tested += 1
+            assert ids[r].tolist() == want.tolist(), r
+    assert tested >= 30
+
+
 def test_gradient_ignores_ids_out_of_range():
     tt = torch()
     x = tt.randn((4, 24), device="cuda", generator=tt.Generator("cuda").manual_seed(3))
