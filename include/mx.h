@@ -396,7 +396,8 @@ mx_status mx_grouped_gemm_q(const uint8_t* a_codes, int64_t a_ld, const uint8_t*
  *   - Scores: s = softmax(l) over the row (MX_SOFTMAX) or s_e =
  *     1 / (1 + exp(-l_e)) (MX_SIGMOID), in fp32.
  *   - Availability: a logit of -inf (a masked expert, a padding token) or a
- *     bias of -inf makes an expert unavailable.  The type's lowest finite
+ *     bias of -inf makes an expert unavailable, whatever its score, NaN
+ *     included.  The type's lowest finite
  *     value does not: such an expert is chosen after all others.
  *   - Keys order the choice: s_e + bias_e with a bias (fp32 [experts], or
  *     NULL; it only steers the choice, not the weights), s_e without.  Where

@@ -124,11 +124,12 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 }
 
 // A lane's experts of a row: C chunks of four, chunk c at 4 (lane + L c).
-// Lanes past the row's end read its last experts again and take -inf: loads
+// Lanes past the row's end read its last experts again and take `past`: loads
 // without branches are all under way at once.  vec: experts % 4 == 0 and
 // aligned rows, a chunk is one load.
 template <bool BF16, int L, int C>
-__device__ __forceinline__ void load_row(const void* logits, int64_t base, int experts, int vec, int lane, float* v) {
+__device__ __forceinline__ void load_row(const void* logits, int64_t base, int experts, int vec, int lane, float* v,
+                                         float past = -__builtin_inff()) {
     if (vec) {
         if constexpr (BF16) {
             uint2 w[C];
@@ -160,7 +161,7 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t base, int e
     if (experts < 4 * L * C) {
 #pragma unroll
         for (int i = 0; i < 4 * C; ++i)
-            v[i] = 4 * (lane + L * (i >> 2)) + (i & 3) < experts ? v[i] : -__builtin_inff();
+            v[i] = 4 * (lane + L * (i >> 2)) + (i & 3) < experts ? v[i] : past;
     }
 }
 
@@ -406,7 +407,19 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
         const float inv = 1.0f / sum;
         float b[N];
         if (a.bias) {
-            load_row<false, L, C>(a.bias, 0, a.experts, a.vec_bias, lane, b);
+            load_row<false, L, C>(a.bias, 0, a.experts, a.vec_bias, lane, b, 0.0f);
+            // A bias of -inf takes its expert away also where the score is NaN,
+            // which the sum does not do.  In bits -inf is above every number,
+            // so one maximum of all of them shows whether there is one to look
+            // for (a comparison at every expert: 44.1 us against 43.7 for
+            // both directions of the grouped size above).
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) most = max(most, __float_as_uint(b[i]));
+            if (__any(most >= 0xFF800000u)) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = b[i] == -__builtin_inff() ? b[i] : v[i];
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) b[i] = 0.0f;

@@ -30,8 +30,10 @@ def keys(l, bias, score, groups, group_best):
     if bias is None and (groups == 1 or group_best == 1):
         return l.copy()
     s = scores(l, score)
-    k = s if bias is None else s + np.asarray(bias, dtype=np.float64)
-    return np.where(np.isneginf(l), -np.inf, k)
+    if bias is None:
+        return np.where(np.isneginf(l), -np.inf, s)
+    b = np.asarray(bias, dtype=np.float64)
+    return np.where(np.isneginf(l) | np.isneginf(b), -np.inf, s + b)
 
 
 def _order(v):

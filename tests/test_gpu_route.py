@@ -203,6 +203,29 @@ def test_nan_keys_add_nothing_to_their_groups(tokens, experts, groups, best):
     assert tested >= 30
 
 
+@pytest.mark.parametrize("tokens", [9, 8200])
+@pytest.mark.parametrize("experts,groups,k", [(32, 1, 8), (64, 8, 4), (60, 5, 3), (256, 8, 8), (512, 1, 12)])
+def test_a_nan_score_does_not_bring_back_what_the_bias_takes_away(tokens, experts, groups, k):
+    """Rows with NaN and +inf logits (whose softmax is NaN throughout) under a
+    bias of -inf at a third of the experts: those are never chosen."""
+    rng = np.random.default_rng(experts)
+    x = rng.normal(size=(tokens, experts)).astype(np.float32)
+    x[::3, rng.permutation(experts)[:experts // 2]] = float("nan")
+    x[1::3, 5] = INF
+    bias = (0.01 * rng.integers(-9, 10, experts)).astype(np.float32)
+    gone = np.arange(experts) % 3 == 0
+    bias[gone] = -INF
+    for score in (mx.SOFTMAX, mx.SIGMOID):
+        for best in ((1, 2) if groups > 1 else (1,)):
+            kw = dict(score=score, bias=bias, groups=groups, top_groups=max(1, groups // 2), group_best=best)
+            ids = host(mx.route(dev(x), k, **dict(kw, bias=dev(bias)))[0])
+            assert not gone[ids[ids >= 0]].any()
+            for r in range(9):
+                want, _, margin = moe.route_row(x[r].astype(np.float64), k, **kw)
+                if margin > KEY_TOL:
+                    assert ids[r].tolist() == want.tolist()
+
+
 def test_gradient_ignores_ids_out_of_range():
     tt = torch()
     x = tt.randn((4, 24), device="cuda", generator=tt.Generator("cuda").manual_seed(3))

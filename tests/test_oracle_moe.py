@@ -27,6 +27,13 @@ def test_bias_steers_the_choice_and_not_the_weights():
     assert ids.tolist() == [0, 2, -1]
 
 
+def test_a_nan_score_does_not_bring_back_what_the_bias_takes_away():
+    nan = float("nan")
+    for score in (moe.SOFTMAX, moe.SIGMOID):
+        ids, _, _ = moe.route_row([nan, 1.0, nan, 0.0], 4, score=score, bias=[-INF, 0.0, 0.0, -INF])
+        assert ids.tolist() == [1, 2, -1, -1]
+
+
 def test_groups_by_hand():
     #        group 0      group 1       group 2
     l = [3.0, -9.0, 2.0, 1.9, 2.5, -INF]
