@@ -239,6 +239,25 @@ def test_gradient_ignores_ids_out_of_range():
                 assert np.allclose(got[r], want, rtol=0, atol=D_TOL)
 
 
+@pytest.mark.parametrize("tokens", [40, 8200])
+@pytest.mark.parametrize("experts", [24, 60, 128, 256, 500, 1024])
+def test_dense_gradient_entries(tokens, experts):
+    """Every entry that was not chosen, over that of an expert with the row's
+    largest logit, is exp of an integer difference, which fp32 holds exactly:
+    the exponential (1 ulp, 2^-23, and the rounding that ends it, 2^-24) and
+    the two products of each entry (2^-24 each) remain, 7 * 2^-24; 8 leaves
+    room for the products' own squares."""
+    rng = np.random.default_rng(experts)
+    x = -rng.integers(0, 81, (tokens, experts)).astype(np.float32)
+    x[:, :3] = 0.0                                         # two chosen, one to compare with
+    ids = np.tile(np.array([[0, 1]], np.int32), (tokens, 1))
+    for shift in (0.0, 7.0, -1000.0):
+        dl = host(mx.route_bwd(dev(x + np.float32(shift)), dev(ids), dev(np.ones((tokens, 2), np.float32)),
+                               renorm=False)).astype(np.float64)
+        want = np.exp(x[:, 3:].astype(np.float64))
+        assert (np.abs(dl[:, 3:] / dl[:, 2:3] - want) <= 8 * 2.0 ** -24 * want).all()
+
+
 @pytest.mark.parametrize("score", [0, 1])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_gradient_against_differences(score, renorm):
