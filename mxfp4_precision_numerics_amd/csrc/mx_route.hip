@@ -169,11 +169,12 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 
 // e^x and 1 / (1 + e^-x) by the exponential and reciprocal instructions, for
 // every expert of a row: e^x is off by |x| 2^-23 relative, which the sums and
-// keys it goes into hold at a share of e^x itself; as keys the scores are good
-// to 3e-7 absolute, and sums as good as with expf but for 5% (weights without
-// renormalisation, 64 normal logits: median 4.0e-8 off, with expf 3.7e-8, for
-// 20.4 us in place of 17.8 at 65536 x 256).  The weights of the chosen few use
-// expf and a division.
+// keys it goes into hold at a share of e^x itself.  Sigmoid keys, bias
+// included, are good to 3e-7 absolute; softmax ones too but for their sum's
+// rounding, which a row's keys share.  Sums are as good as with expf but for
+// 5% (weights without renormalisation, 64 normal logits: median 4.0e-8 off,
+// with expf 3.7e-8, for 20.4 us in place of 17.8 at 65536 x 256).  The weights
+// of the chosen few use expf and a division.
 __device__ __forceinline__ float quick_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 __device__ __forceinline__ float quick_sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.0f + quick_exp(-x));

@@ -126,6 +126,62 @@ def test_route_and_gradient(case):
         assert (np.abs(dl[r] - d) <= tol).all(), (r, np.abs(dl[r] - d).max())
 
 
+def near_tie_faults(key, ids, groups, top_groups, best, key_tol):
+    """Rows [tokens] whose ids are not a choice that errors of key_tol in each
+    key explain: distinct, in the order of the keys, from few enough groups,
+    none of them clearly behind a group left out, and no expert of a group
+    that is clearly kept clearly ahead of a chosen one.  A group's score, the
+    sum of two keys below 2, is rounded once more (2^-23).  Two values are
+    clearly apart beyond both their errors."""
+    t, e = key.shape
+    k, size = ids.shape[1], e // groups
+    rows = np.arange(t)[:, None]
+    chosen = np.zeros((t, e), bool)
+    chosen[rows, ids] = True
+    bad = (ids < 0).any(1) | (chosen.sum(1) != k)
+    mine = key[rows, ids]
+    bad |= (mine[:, :-1] < mine[:, 1:] - 2 * key_tol).any(1)
+    sure = np.ones((t, groups), bool)
+    if top_groups < groups:
+        of = np.sort(key.reshape(t, groups, size), axis=2)[:, :, -best:].sum(2)
+        far = 2 * (best * key_tol + 2.0 ** -23)
+        down = -np.sort(-of, axis=1)
+        sure = of > down[:, top_groups, None] + far        # ahead of the first one left out
+        used = chosen.reshape(t, groups, size).any(2)
+        bad |= (used & (of < down[:, top_groups - 1, None] - far)).any(1)
+        bad |= (used | sure).sum(1) > top_groups
+    missed = np.where(np.repeat(sure, size, axis=1) & ~chosen, key, -INF).max(1)
+    return bad | (missed > mine.min(1) + 2 * key_tol)
+
+
+def near_tie_logits(tokens, experts, seed):
+    """Logits and a bias whose sigmoid keys crowd within 5e-7 around a few
+    values, and their 64-bit keys."""
+    rng = np.random.default_rng(seed)
+    bias = (0.001 * rng.integers(-60, 61, experts)).astype(np.float32)
+    key = 0.25 + 0.1 * rng.integers(0, 6, (tokens, experts)) + rng.uniform(-5e-7, 5e-7, (tokens, experts))
+    s = key - bias.astype(np.float64)
+    x = np.log(s / (1 - s)).astype(np.float32)
+    return x, bias, 1 / (1 + np.exp(-x.astype(np.float64))) + bias.astype(np.float64)
+
+
+# The error of a key s + b, s = 1 / (1 + e^-x): the product x log2(e) and its constant are off by 7.3e-8 |x|, the
+# exponential by 1 ulp (2^-23); both reach s by the factor s (1 - s), so at most 0.224 * 7.3e-8 + 2^-25 = 4.7e-8.  The
+# sum 1 + e^-x (2^-24), the reciprocal (1 ulp, 2^-23) and the sum with b, below 2 (2^-24), add 2.4e-7.
+SIGMOID_KEY_TOL = 3e-7
+
+
+@pytest.mark.parametrize("tokens", [300, 8200])
+@pytest.mark.parametrize("experts,groups,top_groups,best,k", [(64, 8, 4, 2, 8), (64, 8, 4, 1, 6), (256, 8, 4, 2, 8),
+                                                              (60, 5, 2, 2, 4), (250, 10, 3, 2, 7), (32, 1, 1, 1, 4),
+                                                              (512, 64, 9, 2, 12), (1024, 16, 5, 2, 8)])
+def test_near_ties(experts, groups, top_groups, best, k, tokens):
+    x, bias, key = near_tie_logits(tokens, experts, experts + tokens)
+    ids = host(mx.route(dev(x), k, score=mx.SIGMOID, bias=dev(bias), groups=groups, top_groups=top_groups,
+                        group_best=best)[0])
+    assert not near_tie_faults(key, ids, groups, top_groups, best, SIGMOID_KEY_TOL).any()
+
+
 def test_equal_keys_go_to_the_lowest_index():
     tt = torch()
     rng = np.random.default_rng(0)
