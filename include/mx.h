@@ -397,8 +397,8 @@ mx_status mx_grouped_gemm_q(const uint8_t* a_codes, int64_t a_ld, const uint8_t*
  *     1 / (1 + exp(-l_e)) (MX_SIGMOID), in fp32.
  *   - Availability: a logit of -inf (a masked expert, a padding token) or a
  *     bias of -inf makes an expert unavailable, whatever its score, NaN
- *     included.  The type's lowest finite
- *     value does not: such an expert is chosen after all others.
+ *     included.  The type's lowest finite value does not: such an expert is
+ *     chosen after all others.
  *   - Keys order the choice: s_e + bias_e with a bias (fp32 [experts], or
  *     NULL; it only steers the choice, not the weights), s_e without.  Where
  *     neither a bias nor a sum of scores is involved the logits themselves
@@ -516,7 +516,7 @@ mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const v
  * the caller sees it in *norm and drops the step.
  * max_norm >= 0.  workspace: mx_grad_workspace(count) bytes, 8-byte aligned,
  * contents irrelevant before and after.  Outputs may not overlap other
- * tensors.  At most 2^37 elements in all and 64 GB in one tensor.
+ * tensors (in place: no tensor is in the list twice).  At most 2^37 elements in all and 64 GB in one tensor.
  * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
  * MX_ERR_LAUNCH. */
 int64_t mx_grad_workspace(int32_t count);

@@ -715,25 +715,29 @@ def combine_bwd(dout, y, slot, weights=None, used_rows=None, dy=None, dweights=N
     return dy, dweights
 
 
-def _grad_list(grads, name):
+def _grad_list(grads, name, device=None):
     """The host arrays of a gradient list (any shapes, contiguous, fp32 and
-    bf16 mixed)."""
+    bf16 mixed) and its device's index: all of one device, the given one if
+    there is one."""
     codes = _dtype_codes
     grads = list(grads)
-    if not all([g.is_cuda and g.is_contiguous() for g in grads]):
+    devices = {g.get_device() if g.is_contiguous() else -1 for g in grads}
+    if -1 in devices:
         raise ValueError("%s must be contiguous device tensors" % name)
+    if len(devices) > 1 or (device is not None and devices and device not in devices):
+        raise ValueError("%s must be on one device, that of the other arguments" % name)
     try:
         types = array.array("i", [codes[g.dtype] for g in grads])
     except KeyError as e:
         raise TypeError("%s: expected float32 or bfloat16, got %s" % (name, e.args[0])) from None
     return (grads, types, array.array("q", [g.numel() for g in grads]),
-            array.array("Q", [g.data_ptr() for g in grads]))
+            array.array("Q", [g.data_ptr() for g in grads]), devices.pop() if devices else None)
 
 
 def grad_norm(grads, norm=None, workspace=None):
-    """The L2 norm over all elements of the tensors in grads: a 0-dim fp32
-    device tensor (see mx_grad_norm).  workspace: uint8, at least
-    mx_grad_workspace bytes, or None to allocate it."""
+    """The L2 norm over all elements of the tensors in grads (contiguous, on
+    one device): a 0-dim fp32 device tensor (see mx_grad_norm).  workspace:
+    uint8, at least mx_grad_workspace bytes, or None to allocate it."""
     return _grad_call("mx_grad_norm", grads, None, None, norm, workspace)
 
 
@@ -741,23 +745,25 @@ def grad_clip(grads, max_norm: float, outs=None, norm=None, workspace=None):
     """Scales the tensors in grads by min(1, max_norm / (norm + 1e-6)), in
     place or into the tensors of outs (same types and sizes), and returns
     their norm before that as a 0-dim fp32 device tensor.  A norm that is not
-    finite leaves the values as they are (see mx_grad_clip)."""
+    finite leaves the values as they are (see mx_grad_clip).  All tensors are
+    contiguous and on one device.  What is written may not overlap another
+    tensor: in place no gradient may be in the list twice."""
     return _grad_call("mx_grad_clip", grads, outs, float(max_norm), norm, workspace)
 
 
 def _grad_call(fn, grads, outs, max_norm, norm, workspace):
     torch = _torch()
-    grads, types, numels, ptrs = _grad_list(grads, "grads")
+    if norm is not None:
+        _shaped(norm, (), torch.float32, "norm")
+    grads, types, numels, ptrs, device = _grad_list(grads, "grads", None if norm is None else norm.get_device())
     n, outs_at = len(grads), None
     if outs is not None:
-        outs, out_types, out_numels, out_ptrs = _grad_list(outs, "outs")
+        outs, out_types, out_numels, out_ptrs, _ = _grad_list(outs, "outs", device)
         if out_types != types or out_numels != numels:
             raise ValueError("outs must match grads in number, types and sizes")
         outs_at = out_ptrs.buffer_info()[0]
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
-    else:
-        _shaped(norm, (), torch.float32, "norm")
     workspace = _workspace(workspace, lib().mx_grad_workspace(n), norm.device)
     head = (ptrs.buffer_info()[0], types.buffer_info()[0], numels.buffer_info()[0], n)
     if fn == "mx_grad_norm":

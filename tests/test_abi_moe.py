@@ -136,6 +136,46 @@ def test_grad_validation(L):
     assert L.mx_grad_workspace(1000) >= L.mx_grad_workspace(1) > 0
 
 
+class FakeGrad:
+    """What the binding asks of a gradient, on a device of our choice."""
+
+    def __init__(self, device, contiguous=True):
+        import torch
+        self.dtype, self.device, self.contiguous = torch.float32, device, contiguous
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def numel(self):
+        return 4
+
+    def data_ptr(self):
+        return FAKE
+
+    @property
+    def is_cuda(self):
+        return self.device >= 0
+
+
+def test_gradients_of_two_devices_are_refused(L):
+    mx._torch()
+    grads = [FakeGrad(0), FakeGrad(0)]
+    assert list(mx._grad_list(grads, "grads")[2]) == [4, 4] and mx._grad_list(grads, "grads")[-1] == 0
+    for bad in ([FakeGrad(0), FakeGrad(1)], [FakeGrad(0), FakeGrad(-1)], [FakeGrad(0), FakeGrad(0, contiguous=False)]):
+        with pytest.raises(ValueError):
+            mx._grad_list(bad, "grads")
+        with pytest.raises(ValueError):
+            mx.grad_norm(bad)
+        with pytest.raises(ValueError):
+            mx.grad_clip(grads, 1.0, outs=bad)
+    with pytest.raises(ValueError):                        # outs elsewhere than grads
+        mx.grad_clip(grads, 1.0, outs=[FakeGrad(1), FakeGrad(1)])
+    assert mx._grad_list([], "grads", 0)[-1] is None
+
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CLANG_RT = (glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so") + [""])[0]
 
