@@ -156,8 +156,8 @@ struct Flight {
 // One wave: 64 V columns of one token; a row's waves follow one another, so
 // the waves of a workgroup read neighbouring pieces of the same rows.  One
 // wave for a whole token was slower (117 against 107 us at the size below).
-// 16384 tokens of 4 rows, 2880 bf16 columns, with a residual: 83-86 us, 6.6 to
-// 6.8 TB/s (a copy of that size: 5.5).
+// 16384 tokens of 4 rows, 2880 bf16 columns, with a residual: 77-80 us, 7.1 to
+// 7.3 TB/s (a copy of that size: 5.5); of 8 rows 138 us, 6.8 TB/s.
 template <bool YB, bool OB, bool STREAM, bool FULL>
 __device__ __forceinline__ void combine_piece(const CombineArgs& a, int64_t t, int64_t col, Flight& n) {
     constexpr int V = YB ? 8 : 4;
@@ -222,7 +222,7 @@ struct CombineBwdArgs {
 // One workgroup: one token, its waves side by side along the columns (one wave
 // a token: 5% slower at the size below).  Beyond the tokens the workgroups
 // clear the rows of dy past the used ones.  16384 tokens of 4 rows, 2880 bf16
-// columns: 141 us, 6.0 TB/s.
+// columns: 141 us, 6.0 TB/s; of 8 rows 288 us, 5.6 TB/s.
 constexpr int MAX_WAVES = 8;
 
 // The sums over a wave of FLIGHT values, in a fixed order: lanes 16 j .. 16 j + 15

@@ -399,12 +399,12 @@ __device__ __forceinline__ void row_largest(double* key, double* list) {
     if constexpr (L >= 64) keep_larger<K>(list, [](double d) { return __shfl_xor(d, 32); });
 }
 
-// Bound by the vector units: for 256 experts in groups about 190 instructions
-// a row, of which the keys' sort is a third.  65536 tokens, top 8 of 256 fp32
-// in 8 groups: 28 us (2.4 TB/s read; 21 us of it the instructions alone);
-// without bias and groups 17 us (4.1 TB/s).  16384 tokens, top 4 of 32: 3.6 us.
+// Bound by the vector units: for 256 experts in groups 196 instructions a row,
+// of which the keys' sort is a third.  65536 tokens, top 8 of 256 fp32 in 8
+// groups: 29 us (2.3 TB/s read; 22 us of it the instructions alone); without
+// bias and groups 17 us (4.1 TB/s).  16384 tokens, top 4 of 32: 3.5 us.
 // K = 8: up to eight experts by the merged lists; K = 0: any number, one row
-// maximum after the other.
+// maximum after the other (top 16 of 256 there 41 us, top 32 148).
 template <bool BF16, int L, int C, int K>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     constexpr int N = 4 * C, ROWS = 256 / L;
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 // for the kernel's end (both directions of 65536 x 256: 48.0 us without, 44.1
 // with them; of 16384 x 256: 12.9 and 10.3).  Bound by memory: the write, and
 // the lines that the chosen logits lie in.  65536 tokens, top 8 of 256 fp32:
-// 15 us.
+// 15 us; the dense one 24 us (5.9 TB/s).
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
