@@ -1,6 +1,7 @@
 /*
  * mx.h -- C ABI of libmx355, the MXFP4 quantize-then-contract path on AMD
- * MI355X (gfx950), and the routing, combine and clipping operators around it.
+ * MI355X (gfx950), the routing, combine and clipping operators around it, and
+ * a key/value cache held in the same format with the attention that reads it.
  *
  * The path is the one the pages train a mixture-of-experts LLM with
  * ("Training an MoE LLM in MXFP4: How We Closed the Gap to BF16", Abstract):
@@ -501,6 +502,48 @@ mx_status mx_combine_bwd(const void* dout, mx_dtype dt, int64_t dout_ld, const v
                          int32_t top_k, const int32_t* used_rows, void* dy, int64_t dy_ld, float* dweights,
                          mx_stream stream);
 
+/* The balance loss of a router over a batch of tokens, and the assignments of
+ * each expert.  With the scores s_te of mx_route (softmax; sigmoid scores are
+ * divided by their sum over the row), ids [tokens x top_k] as mx_route chose
+ * them and
+ *   c_e  the number of ids equal to e (an id out of [0, experts) counts
+ *        nowhere), n = sum c_e,
+ *   T    the number of tokens with an available expert (a logit other than
+ *        -inf),
+ * it writes
+ *   counts [experts] int32: c_e,
+ *   slope [experts] fp32: experts * c_e / (n T), 0 where n T is 0,
+ *   loss [1] fp32: sum_e slope_e sum_t s_te: 1 when every expert gets the same
+ *        share of the assignments and of the scores, `experts` when one expert
+ *        gets all of both.
+ * A token of -inf alone (padding) has no scores.  A NaN among a row's logits,
+ * or +inf under the softmax, makes the loss NaN, as the formula says.
+ * Scores are fp32; their sums over the tokens are fp32 within a workgroup and
+ * fp64 across workgroups, in a fixed order.
+ * logits as in mx_route; 1 <= top_k <= 1024.  workspace:
+ * mx_balance_workspace(tokens, experts) bytes, 16-byte aligned, its contents
+ * irrelevant before and after.
+ * Errors: MX_ERR_DTYPE, MX_ERR_UNSUPPORTED (score), MX_ERR_SHAPE, MX_ERR_NULL,
+ * MX_ERR_ALIGN, MX_ERR_LAUNCH.  tokens == 0 writes zeros. */
+int64_t mx_balance_workspace(int64_t tokens, int32_t experts);
+mx_status mx_balance(const void* logits, mx_dtype lt, int64_t tokens, int32_t experts, int64_t logits_ld,
+                     mx_score score, const int32_t* ids, int32_t top_k, int32_t* counts, float* slope, float* loss,
+                     void* workspace, mx_stream stream);
+
+/* Gradient of the balance loss with respect to the logits; the counts, and so
+ * the slope, have none:
+ *   dlogits_te = add_te + scale * dloss * s_te (slope_e - sum_j slope_j s_tj),
+ * under sigmoid scores times 1 - sigmoid(l_te); each rounded once to the
+ * logits' type.  slope [experts] as mx_balance writes it (or one made from
+ * counts of more tokens than these).  dloss: DEVICE fp32[1], or NULL for 1.
+ * add [tokens x experts] of the logits' type (the router's own gradient,
+ * mx_route_bwd), or NULL for 0; dlogits may be add itself, at the same pitch.
+ * Every element of dlogits is written; where s_te is 0 it is add_te.
+ * Errors as mx_balance; scale must be finite.  tokens == 0 launches nothing. */
+mx_status mx_balance_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_t experts, int64_t logits_ld,
+                         mx_score score, const float* slope, const float* dloss, float scale, const void* add,
+                         int64_t add_ld, void* dlogits, int64_t dlogits_ld, mx_stream stream);
+
 /* The L2 norm over all elements of `count` gradient tensors, and clipping by
  * it.  grads, types, numels (and outs) are HOST arrays of `count` entries:
  * device pointers, element types (fp32 and bf16 may be mixed) and element
@@ -524,6 +567,97 @@ mx_status mx_grad_norm(const void* const* grads, const mx_dtype* types, const in
                        double* workspace, float* norm, mx_stream stream);
 mx_status mx_grad_clip(const void* const* grads, const mx_dtype* types, const int64_t* numels, int32_t count,
                        void* const* outs, float max_norm, double* workspace, float* norm, mx_stream stream);
+
+/* A key/value cache held in MXFP4: 1x32 blocks along head_dim, 4.25 bits an
+ * element, in pages of page_size tokens.  All buffers are the caller's.
+ *   k_codes, v_codes [pages][heads][page_size][head_dim / 2]: element codes.
+ *   k_scales, v_scales [pages][heads][head_dim / 32][page_size]: scale bytes,
+ *     those of a block of consecutive tokens next to each other (the attention
+ *     reads eight tokens' at once).
+ *   slot: the place of a token, page * page_size + its offset in the page.
+ *   use_rht: what is held is the RHT (sign_mask) of the keys and values, which
+ *     spreads large channels over their block before they are rounded.  The
+ *     transform is orthogonal: queries transformed alike give the same scores,
+ *     and an output is transformed back once.
+ * head_dim: a multiple of 32 up to 256; page_size: a power of two from 16 to
+ * 4096; heads <= 1024; pages * page_size < 2^31.  All four buffers 16-byte
+ * aligned.  The struct is host memory and read during the call only. */
+typedef struct {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t pages;
+    int32_t heads, page_size, head_dim;
+    int32_t use_rht;
+    uint32_t sign_mask;
+} mx_cache;
+
+/* Quantizes the keys and values of `tokens` tokens into their slots: bit for
+ * bit the codes and scales of mx_quantize_1d (block_axis = 1, use_rht and
+ * sign_mask of the cache, MX_RNE).
+ * k, v [tokens][heads][head_dim] (type t), k_ld elements from one token to the
+ * next (0 = heads * head_dim) and k_head_ld from one head to the next (0 =
+ * head_dim); any order of the two (slices of a joint projection, heads first).
+ * slots (DEVICE int32[tokens]): a slot outside [0, pages * page_size) (-1:
+ * padding) is not written.  Slots of different tokens are different; of two
+ * tokens in one slot either's bytes may stay.
+ * tokens * heads * head_dim <= 2^33.
+ * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
+ * MX_ERR_LAUNCH.  tokens == 0 launches nothing. */
+mx_status mx_cache_write(const mx_cache* cache, const void* k, int64_t k_ld, int64_t k_head_ld, const void* v,
+                         int64_t v_ld, int64_t v_head_ld, mx_dtype t, int64_t tokens, const int32_t* slots,
+                         mx_stream stream);
+
+/* Reads tokens back: decoded, transformed back where the cache is transformed,
+ * rounded once to type t.  A slot outside the cache reads as 0.  k, v and their
+ * pitches as in mx_cache_write (rows may not overlap); either of k and v may be
+ * NULL.  Errors as mx_cache_write. */
+mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_head_ld, void* v, int64_t v_ld,
+                        int64_t v_head_ld, mx_dtype t, int64_t tokens, const int32_t* slots, mx_stream stream);
+
+/* Attention of `tokens` query rows over the cache:
+ *   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale <q_i, k_j>),
+ * k_j and v_j the cache's decoded values; with a sink logit of the query's head
+ * the denominator has exp(sink) more.
+ * q [tokens][q_heads][head_dim] (fp32 or bf16; q_ld, q_head_ld as k's in
+ * mx_cache_write); q_heads is a multiple of the cache's heads, and query head h
+ * reads cache head h / (q_heads / heads).
+ * Sequences: sequence s has the query rows q_offsets[s] .. q_offsets[s + 1] - 1
+ * (DEVICE int32[seqs + 1], non-decreasing, within [0, tokens]; NULL: one row
+ * each, tokens == seqs) and the keys 0 .. lengths[s] - 1 (DEVICE int32[seqs],
+ * taken as within [0, table_pages * page_size]): key j lies in page
+ * page_table[s * table_ld + j / page_size] (DEVICE int32; table_ld 0 =
+ * table_pages) at offset j % page_size.  Table entries past a sequence's length
+ * are not looked at; keys of an entry outside [0, pages) do not exist.
+ * Rows in no sequence are left as they are.
+ * causal != 0: the queries are the sequence's last tokens: the i-th of n sees
+ * the keys j <= lengths[s] - n + i, with window > 0 only the last `window` of
+ * these.  causal == 0: every key (window must be 0).
+ * A row that sees no key, or whose denominator is 0, gets out = 0.  Neither a key that a row does not see
+ * nor what lies in the cache behind a sequence's length reaches it, whatever
+ * its bytes; a non-finite key or value that it sees makes it NaN as the formula
+ * says (a value: in its block).
+ * sinks (DEVICE fp32[q_heads]) or NULL.  lse [tokens][q_heads] fp32 or NULL:
+ * the logarithm of the denominator (-inf where that is 0).
+ * out: q's type, out_ld and out_head_ld like q's; it overlaps no input.
+ * Scores, the softmax's statistics and sums are fp32.  bf16 queries enter the
+ * products as they are; fp32 ones, and transformed ones, as a sum of two bf16
+ * (2^-17 relative); exp(..) enters the product with v as bf16, for fp32 outputs
+ * as a sum of two.  Every sum has a fixed order, given the lengths.
+ * max_queries: the most rows that a sequence has, if the caller knows it (it
+ * only selects the kernel); 0: unknown.
+ * workspace: mx_cache_attention_workspace(...) bytes, 16-byte aligned, its
+ * contents irrelevant before and after; calls that may run at the same time
+ * need one each.
+ * scale > 0 and finite; tokens * q_heads < 2^31; seqs < 2^24; seqs > 0 where
+ * tokens > 0.
+ * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
+ * MX_ERR_LAUNCH.  tokens == 0 launches nothing. */
+int64_t mx_cache_attention_workspace(const mx_cache* cache, int64_t tokens, int32_t q_heads, int32_t max_queries);
+mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, int64_t tokens, int32_t q_heads,
+                             int64_t q_ld, int64_t q_head_ld, const int32_t* q_offsets, int32_t max_queries,
+                             int32_t seqs, const int32_t* page_table, int64_t table_ld, int32_t table_pages,
+                             const int32_t* lengths, float scale, int causal, int32_t window, const float* sinks,
+                             void* out, int64_t out_ld, int64_t out_head_ld, float* lse, void* workspace,
+                             mx_stream stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmx355.so")
-SOURCES = ["mx_quant.hip", "mx_gemm.hip", "mx_route.hip", "mx_combine.hip", "mx_grad.hip"]
+SOURCES = ["mx_quant.hip", "mx_gemm.hip", "mx_route.hip", "mx_combine.hip", "mx_grad.hip", "mx_balance.hip",
+           "mx_cache.hip", "mx_attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

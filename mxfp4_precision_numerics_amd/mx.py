@@ -79,10 +79,21 @@ def lib():
         L.mx_grad_workspace.restype = i64
         L.mx_grad_norm.argtypes = [P, P, P, i32, P, P, P]
         L.mx_grad_clip.argtypes = [P, P, P, i32, P, f32, P, P, P]
+        L.mx_balance_workspace.argtypes = [i64, i32]
+        L.mx_balance_workspace.restype = i64
+        L.mx_balance.argtypes = [P, c_int, i64, i32, i64, c_int, P, i32, P, P, P, P, P]
+        L.mx_balance_bwd.argtypes = [P, c_int, i64, i32, i64, c_int, P, P, f32, P, i64, P, i64, P]
+        L.mx_cache_write.argtypes = [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]
+        L.mx_cache_read.argtypes = [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]
+        L.mx_cache_attention_workspace.argtypes = [P, i64, i32, i32]
+        L.mx_cache_attention_workspace.restype = i64
+        L.mx_cache_attention.argtypes = [P, P, c_int, i64, i32, i64, i64, P, i32, i32, P, i64, i32, P, f32, c_int,
+                                         i32, P, P, i64, i64, P, P, P]
         for name in ("mx_rht", "mx_quantize_1d", "mx_quantize_2d", "mx_quantize_2d_deosc", "mx_dequantize",
                      "mx_quantize_1d_ex", "mx_dequantize_1d_ex", "mx_quantize_1d_dual",
                      "mx_grouped_gemm", "mx_grouped_gemm_q", "mx_route", "mx_route_bwd", "mx_route_plan",
-                     "mx_combine", "mx_combine_bwd", "mx_grad_norm", "mx_grad_clip"):
+                     "mx_combine", "mx_combine_bwd", "mx_grad_norm", "mx_grad_clip", "mx_balance", "mx_balance_bwd",
+                     "mx_cache_write", "mx_cache_read", "mx_cache_attention"):
             getattr(L, name).restype = c_int
         _lib = L
     return _lib
@@ -772,3 +783,235 @@ def _grad_call(fn, grads, outs, max_norm, norm, workspace):
         code = lib().mx_grad_clip(*head, outs_at, max_norm, _ptr(workspace), _ptr(norm), _stream())
     _check(fn, code)
     return norm
+
+
+# ---------------------------------------------------------------------------
+# The balance loss
+# ---------------------------------------------------------------------------
+def _here(device, **tensors):
+    """Refuses tensors that are not on this device (its index), and a device
+    other than the current one, whose stream the call would go to."""
+    if device != _torch()._C._cuda_getDevice():
+        raise ValueError("the tensors are not on the current device")
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError("%s is on another device" % name)
+
+
+def balance(logits, ids, score: int = SOFTMAX, counts=None, slope=None, loss=None, workspace=None):
+    """The balance loss of a router over its tokens (see mx_balance): (loss, a
+    0-dim fp32 device tensor, 1 for an even balance; counts int32 [experts],
+    the assignments of each expert in ids [tokens, top_k]; slope fp32
+    [experts], what balance_bwd needs).  logits [tokens, experts], fp32 or
+    bf16, rows may be padded.  workspace: uint8, at least
+    mx_balance_workspace bytes, or None to allocate it."""
+    torch = _torch()
+    ld = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    top_k = ids.shape[1]
+    _same(ids, (tokens, top_k), torch.int32, "ids")
+    dev = logits.device
+    if counts is None:
+        counts = _new_vector(dev, torch.int32, experts)
+    else:
+        _same(counts, (experts,), torch.int32, "counts")
+    if slope is None:
+        slope = _new_vector(dev, torch.float32, experts)
+    else:
+        _same(slope, (experts,), torch.float32, "slope")
+    if loss is None:
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+    else:
+        _shaped(loss, (), torch.float32, "loss")
+    workspace = _workspace(workspace, lib().mx_balance_workspace(tokens, experts), dev)
+    _here(logits.get_device(), ids=ids, counts=counts, slope=slope, loss=loss, workspace=workspace)
+    _check("mx_balance", lib().mx_balance(
+        _ptr(logits), _dtype_code(logits), tokens, experts, ld, score, _ptr(ids), top_k, _ptr(counts), _ptr(slope),
+        _ptr(loss), _ptr(workspace), _stream()))
+    return loss, counts, slope
+
+
+def balance_bwd(logits, slope, score: int = SOFTMAX, dloss=None, scale: float = 1.0, add=None, dlogits=None):
+    """Gradient of scale * dloss * balance with respect to the logits, plus add
+    (see mx_balance_bwd): dlogits [tokens, experts] of the logits' type.
+    dloss: an fp32 device tensor of one element, or None for 1.  add: the
+    router's own gradient (route_bwd); dlogits may be add, which then becomes
+    the sum."""
+    torch = _torch()
+    ld = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    _same(slope, (experts,), torch.float32, "slope")
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1):
+        raise ValueError("dloss must be one float32")
+    add_ld = _rows(add, "add", (tokens, experts), logits.dtype) if add is not None else 0
+    dld = 0
+    if dlogits is None:
+        dlogits = _new(logits.device, logits.dtype, tokens, experts)
+    else:
+        dld = _rows(dlogits, "dlogits", (tokens, experts), logits.dtype)
+    _here(logits.get_device(), slope=slope, dloss=dloss, add=add, dlogits=dlogits)
+    _check("mx_balance_bwd", lib().mx_balance_bwd(
+        _ptr(logits), _dtype_code(logits), tokens, experts, ld, score, _ptr(slope), _ptr(dloss), float(scale),
+        _ptr(add), add_ld, _ptr(dlogits), dld, _stream()))
+    return dlogits
+
+
+# ---------------------------------------------------------------------------
+# The key/value cache and the attention over it
+# ---------------------------------------------------------------------------
+class _CacheStruct(ctypes.Structure):
+    """mx_cache."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] +
+                [("pages", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("heads", "page_size", "head_dim", "use_rht")] +
+                [("sign_mask", ctypes.c_uint32)])
+
+
+class KVCache:
+    """A paged key/value cache in MXFP4 over four uint8 device tensors (see
+    mx_cache): codes [pages, heads, page_size, head_dim // 2] and scales
+    [pages, heads, head_dim // 32, page_size], of keys and of values.  With
+    use_rht what it holds is transformed (sign_mask)."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, use_rht: bool = False, sign_mask: int = 0):
+        torch = _torch()
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page_size, head_dim // 2]")
+        pages, heads, page_size, half = k_codes.shape
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            _shaped(t, (pages, heads, page_size, half), torch.uint8, name)
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _shaped(t, (pages, heads, half // 16, page_size), torch.uint8, name)
+        self.device_index = k_codes.get_device()
+        if any(t.get_device() != self.device_index for t in (k_scales, v_codes, v_scales)):
+            raise ValueError("the cache's tensors are on different devices")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
+        self.use_rht, self.sign_mask = bool(use_rht), int(sign_mask)
+        self._struct = _CacheStruct(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, heads,
+                                    page_size, 2 * half, self.use_rht, self.sign_mask)
+        self._at = ctypes.addressof(self._struct)
+
+
+def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, use_rht: bool = False, sign_mask: int = 0,
+             device="cuda"):
+    """A new KVCache; every slot reads as 0."""
+    torch = _torch()
+    shapes = ((pages, heads, page_size, head_dim // 2), (pages, heads, head_dim // 32, page_size)) * 2
+    return KVCache(*[torch.zeros(s, dtype=torch.uint8, device=device) for s in shapes], use_rht=use_rht,
+                   sign_mask=sign_mask)
+
+
+def _heads(t, name, shape=None, dtype=None, written=False):
+    """The pitches (token, head) of a device tensor [tokens, heads, dim] with
+    contiguous rows in any order, 0 for the default ones.  written: its rows
+    may not overlap."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError("%s: expected shape %s, got %s" % (name, shape or "[tokens, heads, dim]", tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if t.is_contiguous():
+        return 0, 0
+    (tokens, heads, dim), (ld, head_ld, one) = t.shape, t.stride()
+    ld, head_ld = ld if tokens > 1 else 0, head_ld if heads > 1 else 0
+    if one != 1 or (tokens > 1 and ld < dim) or (heads > 1 and head_ld < dim):
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    if written and tokens > 1 and heads > 1 and ld < (heads - 1) * head_ld + dim and head_ld < (tokens - 1) * ld + dim:
+        raise ValueError("%s must have rows that do not overlap" % name)
+    return ld, head_ld
+
+
+def _slot_vector(slots, tokens):
+    torch = _torch()
+    _same(slots, (tokens,), torch.int32, "slots")
+    return slots
+
+
+def cache_write(cache, k, v, slots):
+    """Quantizes the keys and values k, v [tokens, heads, head_dim] (fp32 or
+    bf16, any pitches) into the cache's slots (int32 [tokens]: page * page_size
+    + offset; -1 or another one outside the cache: not written).  See
+    mx_cache_write."""
+    k_ld, k_head = _heads(k, "k")
+    tokens = k.shape[0]
+    shape = (tokens, cache.heads, cache.head_dim)
+    if k.shape != shape:
+        raise ValueError("k: expected shape %s, got %s" % (shape, tuple(k.shape)))
+    v_ld, v_head = _heads(v, "v", shape, k.dtype)
+    _slot_vector(slots, tokens)
+    _here(cache.device_index, k=k, v=v, slots=slots)
+    _check("mx_cache_write", lib().mx_cache_write(
+        cache._at, _ptr(k), k_ld, k_head, _ptr(v), v_ld, v_head, _dtype_code(k), tokens, _ptr(slots), _stream()))
+
+
+def cache_read(cache, slots, out_dtype=None, k=None, v=None):
+    """The keys and values in the slots (int32 [tokens]), decoded: k, v
+    [tokens, heads, head_dim] of out_dtype (bf16 by default), zeros where a
+    slot is outside the cache.  k, v: tensors to write, any pitches.  See
+    mx_cache_read."""
+    torch = _torch()
+    if slots.dim() != 1:
+        raise ValueError("slots must be [tokens]")
+    tokens = slots.shape[0]
+    _slot_vector(slots, tokens)
+    shape = (tokens, cache.heads, cache.head_dim)
+    given = k if k is not None else v
+    out_dtype = out_dtype or (torch.bfloat16 if given is None else given.dtype)
+    pitches = []
+    for name, t in (("k", k), ("v", v)):
+        pitches.append((0, 0) if t is None else _heads(t, name, shape, out_dtype, written=True))
+    k = torch.empty(shape, dtype=out_dtype, device=slots.device) if k is None else k
+    v = torch.empty_like(k, memory_format=torch.contiguous_format) if v is None else v
+    _here(cache.device_index, k=k, v=v, slots=slots)
+    _check("mx_cache_read", lib().mx_cache_read(
+        cache._at, _ptr(k), *pitches[0], _ptr(v), *pitches[1], _dtype_code(k), tokens, _ptr(slots), _stream()))
+    return k, v
+
+
+def cache_attention(cache, q, page_table, lengths, scale=None, q_offsets=None, max_queries=None, causal: bool = True,
+                    window: int = 0, sinks=None, out=None, lse=None, need_lse: bool = False, workspace=None):
+    """Attention of the query rows q [tokens, q_heads, head_dim] (fp32 or bf16,
+    any pitches) over the cache: (out of q's shape and type, lse fp32 [tokens,
+    q_heads] or None).  page_table int32 [seqs, pages of a sequence], lengths
+    int32 [seqs]: the tokens of each sequence in the cache, its queries' own
+    included.  q_offsets int32 [seqs + 1]: the rows of each sequence; None: one
+    each.  scale: 1 / sqrt(head_dim) by default.  causal, window, sinks (fp32
+    [q_heads]) as in mx_cache_attention.  max_queries: the most rows of a
+    sequence, if known.  workspace: uint8, at least
+    mx_cache_attention_workspace bytes, or None to allocate it."""
+    torch = _torch()
+    q_ld, q_head = _heads(q, "q")
+    tokens, q_heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError("q: expected a head_dim of %d, got %d" % (cache.head_dim, dim))
+    table_ld = _rows(page_table, "page_table", None, torch.int32)
+    seqs, table_pages = page_table.shape
+    _same(lengths, (seqs,), torch.int32, "lengths")
+    if q_offsets is not None:
+        _same(q_offsets, (seqs + 1,), torch.int32, "q_offsets")
+    if max_queries is None:
+        max_queries = 1 if q_offsets is None else 0
+    if sinks is not None:
+        _same(sinks, (q_heads,), torch.float32, "sinks")
+    out_ld = out_head = 0
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        out_ld, out_head = _heads(out, "out", q.shape, q.dtype, written=True)
+    if lse is not None:
+        _same(lse, (tokens, q_heads), torch.float32, "lse")
+    elif need_lse:
+        lse = _new(q.device, torch.float32, tokens, q_heads)
+    workspace = _workspace(workspace, lib().mx_cache_attention_workspace(cache._at, tokens, q_heads, max_queries),
+                           q.device)
+    _here(cache.device_index, q=q, page_table=page_table, lengths=lengths, q_offsets=q_offsets, sinks=sinks, out=out,
+          lse=lse, workspace=workspace)
+    _check("mx_cache_attention", lib().mx_cache_attention(
+        cache._at, _ptr(q), _dtype_code(q), tokens, q_heads, q_ld, q_head, _ptr(q_offsets), max_queries, seqs,
+        _ptr(page_table), table_ld, table_pages, _ptr(lengths), dim ** -0.5 if scale is None else float(scale),
+        int(bool(causal)), window, _ptr(sinks), _ptr(out), out_ld, out_head, _ptr(lse), _ptr(workspace), _stream()))
+    return out, lse

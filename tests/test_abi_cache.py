@@ -1,0 +1,198 @@
+"""C-ABI checks of the cache, attention and balance entry points that need no
+GPU: every argument error is found on the host before any launch, under the
+sanitizers too."""
+import ctypes
+import glob
+import os
+import subprocess
+import sys
+import tempfile
+
+import pytest
+
+from mxfp4_precision_numerics_amd import build, mx
+
+FAKE = 0x1000   # aligned, never dereferenced (validation fails first)
+NULL, SHAPE, ALIGN, DTYPE, UNSUPPORTED = 1, 2, 3, 4, 5
+
+
+@pytest.fixture(scope="module")
+def L():
+    return mx.lib()
+
+
+def caller(fn, **ok):
+    def call(**kw):
+        assert set(kw) <= set(ok), kw
+        return fn(*dict(ok, **kw).values())
+    return call
+
+
+def cache(**kw):
+    args = dict(k_codes=FAKE, k_scales=FAKE, v_codes=FAKE, v_scales=FAKE, pages=4, heads=2, page_size=16, head_dim=64,
+                use_rht=0, sign_mask=0)
+    args.update(kw)
+    return mx._CacheStruct(**args)
+
+
+BAD_CACHES = [(dict(heads=0), SHAPE), (dict(heads=1025), SHAPE), (dict(page_size=8), SHAPE), (dict(page_size=24), SHAPE),
+              (dict(page_size=8192), SHAPE), (dict(page_size=0), SHAPE), (dict(page_size=-16), SHAPE),
+              (dict(head_dim=0), SHAPE), (dict(head_dim=48), SHAPE), (dict(head_dim=288), SHAPE), (dict(pages=-1), SHAPE),
+              (dict(pages=2 ** 27), SHAPE), (dict(pages=2 ** 62), SHAPE), (dict(k_codes=None), NULL),
+              (dict(v_scales=None), NULL), (dict(k_codes=FAKE + 8), ALIGN), (dict(v_codes=FAKE + 8), ALIGN),
+              (dict(k_scales=FAKE + 8), ALIGN), (dict(v_scales=FAKE + 1), ALIGN)]
+
+
+def test_symbols(L):
+    names = set(mx.declared_functions())
+    assert names >= {"mx_balance", "mx_balance_bwd", "mx_balance_workspace", "mx_cache_write", "mx_cache_read",
+                     "mx_cache_attention", "mx_cache_attention_workspace"}
+    for n in names:
+        assert hasattr(L, n), n
+
+
+def test_struct_layout():
+    """_CacheStruct is mx_cache as a C compiler lays it out."""
+    with tempfile.TemporaryDirectory() as d:
+        src, exe = os.path.join(d, "t.c"), os.path.join(d, "t")
+        fields = [n for n, _ in mx._CacheStruct._fields_]
+        with open(src, "w") as f:
+            f.write('#include <stddef.h>\n#include <stdio.h>\n#include "%s"\nint main(void) {\n' % mx.HEADER)
+            f.write("".join('printf("%%zu ", offsetof(mx_cache, %s));\n' % n for n in fields))
+            f.write('printf("%zu", sizeof(mx_cache));\nreturn 0;\n}\n')
+        subprocess.run(["gcc", src, "-o", exe], check=True)
+        got = [int(v) for v in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [getattr(mx._CacheStruct, n).offset for n in fields] + [ctypes.sizeof(mx._CacheStruct)]
+
+
+def test_write_validation(L):
+    c = cache()
+    call = caller(L.mx_cache_write, c=ctypes.addressof(c), k=FAKE, kld=0, khl=0, v=FAKE, vld=0, vhl=0, t=mx.MX_BF16, n=3,
+                  slots=FAKE, s=None)
+    for bad, code in BAD_CACHES:
+        b = cache(**bad)
+        assert call(c=ctypes.addressof(b)) == code, bad
+    assert call(c=None) == NULL and call(t=2) == DTYPE and call(t=-1) == DTYPE
+    for bad in (dict(n=-1), dict(n=2 ** 33), dict(kld=63), dict(khl=63), dict(vld=-1), dict(vhl=-64), dict(vhl=1)):
+        assert call(**bad) == SHAPE, bad
+    for name in ("k", "v", "slots"):
+        assert call(**{name: None}) == NULL and call(**{name: FAKE + 1}) == ALIGN
+    assert call(n=0, k=None, v=None, slots=None) == 0
+    b = cache(pages=0, k_codes=None, k_scales=None, v_codes=None, v_scales=None)
+    assert call(c=ctypes.addressof(b), n=0) == 0
+
+
+def test_read_validation(L):
+    c = cache()
+    call = caller(L.mx_cache_read, c=ctypes.addressof(c), k=FAKE, kld=0, khl=0, v=FAKE, vld=0, vhl=0, t=mx.MX_F32, n=3,
+                  slots=FAKE, s=None)
+    for bad, code in BAD_CACHES:
+        b = cache(**bad)
+        assert call(c=ctypes.addressof(b)) == code, bad
+    assert call(c=None) == NULL and call(t=2) == DTYPE
+    for bad in (dict(n=-1), dict(n=2 ** 33), dict(kld=63), dict(khl=63), dict(vld=-1), dict(vhl=-64)):
+        assert call(**bad) == SHAPE, bad
+    assert call(slots=None) == NULL and call(k=None, v=None) == 0 and call(n=0, slots=None) == 0
+    for name in ("k", "v", "slots"):
+        assert call(**{name: FAKE + 2}) == ALIGN
+
+
+def test_attention_validation(L):
+    c = cache()
+    call = caller(L.mx_cache_attention, c=ctypes.addressof(c), q=FAKE, qt=mx.MX_BF16, n=3, h=4, ld=0, hl=0, off=None, mq=1,
+                  seqs=3, table=FAKE, tld=0, pages=2, len=FAKE, scale=0.125, causal=1, window=0, sinks=None, out=FAKE,
+                  old=0, ohl=0, lse=None, ws=FAKE, s=None)
+    for bad, code in BAD_CACHES:
+        b = cache(**bad)
+        assert call(c=ctypes.addressof(b)) == code, bad
+    assert call(c=None) == NULL and call(qt=2) == DTYPE
+    for bad in (dict(n=-1), dict(h=0), dict(h=3), dict(n=2 ** 30), dict(ld=63), dict(hl=63), dict(old=-1), dict(ohl=8),
+                dict(seqs=-1), dict(seqs=2), dict(seqs=0, off=FAKE), dict(seqs=2 ** 24, off=FAKE), dict(pages=-1),
+                dict(tld=1), dict(tld=-5), dict(pages=2 ** 27), dict(mq=-1), dict(window=-1), dict(window=5, causal=0),
+                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan"))):
+        assert call(**bad) == SHAPE, bad
+    for name in ("q", "out", "len", "table"):
+        assert call(**{name: None}) == NULL, name
+    for name in ("q", "out", "len", "table", "sinks", "lse", "off"):
+        assert call(**{name: FAKE + 1}) == ALIGN, name
+    assert call(ws=FAKE + 8) == ALIGN
+    assert call(n=0, seqs=0, q=None, out=None, len=None, table=None, ws=None) == 0
+    assert call(n=0, seqs=5, off=FAKE) == 0
+
+
+def test_attention_workspace_validation(L):
+    ws, c = L.mx_cache_attention_workspace, cache()
+    at = ctypes.addressof(c)
+    assert ws(None, 3, 4, 1) == 0 and ws(at, 0, 4, 1) == 0 and ws(at, -3, 4, 1) == 0 and ws(at, 3, 3, 1) == 0
+    assert ws(at, 3, 0, 1) == 0 and ws(at, 2 ** 31, 4, 0) == 0
+    assert ws(at, 3, 4, 1) >= 0
+    for bad, _ in BAD_CACHES[:13]:
+        b = cache(**bad)
+        assert ws(ctypes.addressof(b), 3, 4, 1) == 0
+
+
+def test_balance_validation(L):
+    call = caller(L.mx_balance, l=FAKE, lt=mx.MX_F32, t=4, e=32, ld=0, score=0, ids=FAKE, k=4, counts=FAKE, slope=FAKE,
+                  loss=FAKE, ws=FAKE, s=None)
+    assert call(lt=2) == DTYPE and call(score=2) == UNSUPPORTED
+    for bad in (dict(t=-1), dict(t=2 ** 24 + 1), dict(e=0), dict(e=1025), dict(k=0), dict(k=1025), dict(ld=31), dict(ld=-1),
+                dict(t=2 ** 24, k=128)):
+        assert call(**bad) == SHAPE, bad
+    for name in ("l", "ids", "counts", "slope", "loss", "ws"):
+        assert call(**{name: None}) == NULL and call(**{name: FAKE + 2}) == ALIGN, name
+    assert call(t=0, loss=None) == NULL
+    ws = L.mx_balance_workspace
+    assert ws(0, 32) == 0 and ws(-1, 32) == 0 and ws(4, 0) == 0 and ws(4, 1025) == 0 and ws(4, 32) > 0
+    assert ws(2 ** 24, 1024) >= ws(4, 1024) > 0
+
+
+def test_balance_bwd_validation(L):
+    call = caller(L.mx_balance_bwd, l=FAKE, lt=mx.MX_F32, t=4, e=32, ld=0, score=0, slope=FAKE, dloss=None, scale=1.0,
+                  add=None, ald=0, dl=FAKE, dld=0, s=None)
+    assert call(lt=7) == DTYPE and call(score=-1) == UNSUPPORTED
+    for bad in (dict(t=-1), dict(e=1025), dict(ld=8), dict(dld=31), dict(ald=31), dict(scale=float("nan")),
+                dict(scale=float("inf"))):
+        assert call(**bad) == SHAPE, bad
+    for name in ("l", "slope", "dl"):
+        assert call(**{name: None}) == NULL
+    for name in ("l", "slope", "dl", "add", "dloss"):
+        assert call(**{name: FAKE + 2}) == ALIGN, name
+    assert call(t=0, l=None, slope=None, dl=None) == 0
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CLANG_RT = (glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so") + [""])[0]
+
+
+@pytest.mark.skipif(not os.path.exists(CLANG_RT), reason="no clang AddressSanitizer runtime")
+def test_host_code_under_sanitizers():
+    """This file's validation tests on a library whose host code has the
+    address and undefined-behaviour sanitizers on (host pass only: no kernel is
+    launched)."""
+    with tempfile.TemporaryDirectory() as d:
+        lib = os.path.join(d, "libmx355_asan.so")
+        cmd = ["/opt/rocm/bin/hipcc", "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-fPIC", "-shared",
+               "-ffp-contract=off", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+               "-Xarch_host", "-fsanitize=address,undefined",
+               # C callers may pass any int where the header says an enum
+               "-Xarch_host", "-fno-sanitize=enum",
+               "-Xarch_host", "-fno-sanitize-recover=all", "-o", lib]
+        cmd += [os.path.join(build.CSRC, n) for n in ("mx_balance.hip", "mx_cache.hip", "mx_attention.hip")]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-3000:]
+        names = ["mx_balance", "mx_balance_bwd", "mx_balance_workspace", "mx_cache_write", "mx_cache_read",
+                 "mx_cache_attention", "mx_cache_attention_workspace"]
+        code = ("import ctypes, sys; sys.path[:0] = [%r, %r]\n"
+                "from mxfp4_precision_numerics_amd import mx\n"
+                "import test_abi_cache as t\n"
+                "L, whole = ctypes.CDLL(%r), mx.lib()\n"
+                "for n in %r:\n"
+                "    getattr(L, n).argtypes, getattr(L, n).restype = getattr(whole, n).argtypes, getattr(whole, n).restype\n"
+                "for n, f in sorted(vars(t).items()):\n"
+                "    if n.startswith('test_') and n.endswith('_validation'): f(L); print(n)\n"
+                "print('library ok')\n") % (ROOT, os.path.join(ROOT, "tests"), lib, names)
+        env = dict(os.environ, LD_PRELOAD=CLANG_RT, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1",
+                   UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1", PYTHONPATH=ROOT)
+        r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=600)
+        out = r.stdout + r.stderr
+        assert r.returncode == 0 and "library ok" in out and "runtime error" not in out, out[-4000:]

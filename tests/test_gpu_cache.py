@@ -1,0 +1,510 @@
+"""GPU: the MXFP4 key/value cache and the attention over it, against the oracle
+(codes and scales bit for bit) and the 64-bit definitions of oracle/cache.py.
+
+Tolerances of the attention, for an element of a row (p: the softmax, a: the
+largest scale * sum |q_d k_d| over the keys that the row sees).
+  - A score is a sum of dim products in fp32: off by (dim + 8) 2^-24 a; queries
+    that enter as two bf16 terms add 2^-16 a (each term's half step is 2^-8 of
+    what it rounds), and the transform of q, five stages of fp32, 2^-19 a in
+    the worst of them.  The exponential's argument is rounded at 2^-23 of
+    itself (three roundings, at most 2 a log2(e) large, and the exponential
+    instruction's 2^-22).  With e the sum of these, every p is off by a factor
+    within 1 +- 2 e (numerator and sum).
+  - p enters the second product as bf16 (2^-8 relative), or for fp32 outputs
+    as two terms (2^-16); that product and the joins of partial sums are fp32:
+    2^-24 (n + 64) of sum p |v|.
+  - The result is rounded once, after the transform back: 2^-8 or 2^-24 of
+    itself (and five stages of 2^-24 of the block's norm).
+lse: e and the sum's own 2^-22, absolute, and 2^-23 of itself."""
+import numpy as np
+import pytest
+
+import oracle
+from mxfp4_precision_numerics_amd import mx
+from oracle import cache as ref
+from gpu_util import dev, host, torch
+
+pytestmark = pytest.mark.gpu
+
+MASK = 0x9A3C61E5
+
+
+def values(shape, dtype, seed, scale=1.0):
+    """(64-bit values, device tensor) representable in dtype."""
+    tt = torch()
+    x = tt.from_numpy((np.random.default_rng(seed).normal(size=shape) * scale).astype(np.float32)).to(dtype)
+    return x.double().numpy(), x.cuda()
+
+
+def quantized(x, rht):
+    """oracle.quantize_1d of [tokens, heads, dim] in the tensor's own type."""
+    rows = host(x.contiguous()).reshape(-1, x.shape[-1])
+    c, s = oracle.quantize_1d(rows, use_rht=rht, sign_mask=MASK if rht else 0)
+    return c.reshape(x.shape[0], x.shape[1], -1), s.reshape(x.shape[0], x.shape[1], -1)
+
+
+def dtype_of(name):
+    tt = torch()
+    return tt.bfloat16 if name == "bf16" else tt.float32
+
+
+def layouts(x, layout):
+    """The same [tokens, heads, dim] values in another place."""
+    tt = torch()
+    t, h, d = x.shape
+    if layout == "plain":
+        return x
+    if layout == "heads first":
+        return x.transpose(0, 1).contiguous().transpose(0, 1)
+    buf = tt.full((t, (h + 2) * d + 3), float("nan"), dtype=x.dtype, device="cuda")
+    view = buf[:, d + 1:d + 1 + h * d].unflatten(1, (h, d))
+    view.copy_(x)
+    return view
+
+
+WRITES = [
+    # tokens, heads, dim, page, type, rht, layout
+    (1, 1, 32, 16, "bf16", False, "plain"),
+    (1, 8, 64, 16, "bf16", True, "plain"),
+    (7, 3, 96, 32, "f32", False, "joint"),
+    (33, 2, 128, 16, "bf16", True, "heads first"),
+    (130, 5, 160, 64, "f32", True, "joint"),
+    (64, 1, 256, 128, "bf16", False, "joint"),
+    (300, 4, 192, 4096, "f32", True, "heads first"),
+    (257, 8, 128, 64, "bf16", True, "plain"),
+]
+
+
+def slots_for(tokens, pages, page, seed, gone=0.1):
+    rng = np.random.default_rng(seed)
+    slots = rng.permutation(pages * page)[:tokens].astype(np.int32)
+    if tokens > 3:
+        out = rng.random(tokens) < gone
+        slots[out] = rng.choice([-1, -2 ** 31, pages * page, 2 ** 31 - 1], size=int(out.sum()))
+    return slots
+
+
+@pytest.mark.parametrize("case", WRITES, ids=lambda c: "-".join(str(v) for v in c))
+def test_write_and_read(case):
+    tokens, heads, dim, page, kind, rht, layout = case
+    tt = torch()
+    pages = -(-tokens // page) + 2
+    cache = mx.kv_cache(pages, heads, page, dim, use_rht=rht, sign_mask=MASK)
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        t.fill_(0xA5)
+    _, k = values((tokens, heads, dim), dtype_of(kind), 1, 3.0)
+    _, v = values((tokens, heads, dim), dtype_of(kind), 2)
+    if tokens > 5:                                         # blocks of zeros, and such without a scale
+        k[2, 0], v[3, 0, 5], v[4, heads - 1, dim - 1] = 0.0, float("nan"), float("-inf")
+    slots = slots_for(tokens, pages, page, 3)
+    mx.cache_write(cache, layouts(k, layout), layouts(v, layout), dev(slots))
+    there = np.flatnonzero((slots >= 0) & (slots < pages * page))
+    p, o = slots[there] // page, slots[there] % page
+    got = [host(t) for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+    decoded = {}
+    for name, x, codes, scales in (("k", k, got[0], got[1]), ("v", v, got[2], got[3])):
+        c, s = quantized(x, rht)
+        want_c, want_s = np.full_like(codes, 0xA5), np.full_like(scales, 0xA5)
+        want_c[p, :, o] = c[there]
+        want_s[p, :, :, o] = s[there]
+        assert np.array_equal(codes, want_c) and np.array_equal(scales, want_s)        # nothing else written
+        y = np.zeros((tokens, heads, dim))
+        y[there] = ref.decode(c[there], s[there])
+        decoded[name] = ref.rht(y, MASK, inverse=True) if rht else y
+    for out_type in (tt.bfloat16, tt.float32):
+        back = mx.cache_read(cache, dev(slots), out_dtype=out_type)
+        for name, y in zip("kv", back):
+            want, have = decoded[name], y.double().cpu().numpy()
+            assert y.dtype == out_type and np.array_equal(np.isnan(have), np.isnan(want))
+            # decoded values are exact; the transform is five stages of fp32 and a product
+            norm = np.repeat(np.sqrt((want.reshape(tokens, heads, -1, 32) ** 2).sum(-1)), 32, -1)
+            tol = (8 * 2.0 ** -24 * norm if rht else 0.0) + (2.0 ** -8 if out_type == tt.bfloat16 else 2.0 ** -24) * np.abs(want)
+            assert (np.abs(have - want) <= tol)[~np.isnan(want)].all()
+    # into tensors of one's own, one of them in another order
+    k2 = layouts(tt.zeros((tokens, heads, dim), dtype=tt.float32, device="cuda"), "joint")
+    v2 = layouts(tt.zeros((tokens, heads, dim), dtype=tt.float32, device="cuda"), "heads first")
+    mx.cache_read(cache, dev(slots), k=k2, v=v2)
+    assert tt.equal(k2.nan_to_num(7.0), back[0].nan_to_num(7.0)) and tt.equal(v2.nan_to_num(7.0), back[1].nan_to_num(7.0))
+
+
+class Setup:
+    """A cache with every slot filled from the oracle, a table of shuffled
+    pages, and queries."""
+
+    def __init__(self, lengths, heads, group, dim, page, kind="bf16", rht=False, queries=None, seed=0, spare=3,
+                 extra_columns=1):
+        tt, rng = torch(), np.random.default_rng(seed)
+        self.lengths, self.page, self.rht = np.asarray(lengths, dtype=np.int32), page, rht
+        used = [-(-max(0, int(n)) // page) for n in lengths]
+        pages = sum(used) + spare
+        order = rng.permutation(pages).astype(np.int32)
+        self.table = np.full((len(lengths), max(used + [0]) + extra_columns), -7, dtype=np.int32)
+        at = 0
+        for s, n in enumerate(used):
+            self.table[s, :n] = order[at:at + n]
+            at += n
+        self.cache_host = []
+        for i in range(2):
+            x = rng.normal(size=(pages * heads * page, dim)).astype(np.float32) * np.exp(0.5 * rng.normal(size=dim)).astype(np.float32)
+            c, s = oracle.quantize_1d(x)
+            self.cache_host += [c.reshape(pages, heads, page, dim // 2),
+                                np.ascontiguousarray(s.reshape(pages, heads, page, dim // 32).swapaxes(2, 3))]
+        self.queries = [1] * len(lengths) if queries is None else queries
+        self.offsets = None if queries is None else np.concatenate([[0], np.cumsum(queries)]).astype(np.int32)
+        self.q64, self.q = values((sum(self.queries), heads * group, dim), dtype_of(kind), seed + 1)
+
+    def cache(self):
+        return mx.KVCache(*[dev(a) for a in self.cache_host], use_rht=self.rht, sign_mask=MASK if self.rht else 0)
+
+    def call(self, **kw):
+        args = dict(q_offsets=None if self.offsets is None else dev(self.offsets), need_lse=True)
+        args.update(kw)
+        q = args.pop("q", self.q)
+        table = args.pop("table", self.table)
+        return mx.cache_attention(self.cache(), q, dev(table), dev(self.lengths), **args)
+
+    def want(self, **kw):
+        args = dict(q_offsets=self.offsets, mask=MASK if self.rht else None)
+        args.update(kw)
+        table = args.pop("table", self.table)
+        return ref.attention(self.cache_host, self.q64, table, self.lengths, **args)
+
+    def bounds(self, want):
+        """Of out and lse."""
+        out, lse, size, reach = want
+        bf16 = self.q.dtype == torch().bfloat16
+        dim, a, n = self.q.shape[2], reach[..., None], max(1, int(self.lengths.max(initial=1)))
+        e = ((dim + 8) * 2.0 ** -24 + (2.0 ** -16 if self.rht or not bf16 else 0) + (2.0 ** -19 if self.rht else 0)) * a
+        e = e + 3 * 2.0 ** -23 * 2 * 1.4427 * np.maximum(a, 1) + 2.0 ** -22
+        tol = size * (2 * e + (2.0 ** -8 if bf16 else 2.0 ** -16) + (n + 64) * 2.0 ** -24)
+        tol = tol + 5 * 2.0 ** -24 * size + (2.0 ** -8 if bf16 else 2.0 ** -24) * (np.abs(out) + tol) + 1e-37
+        return tol, e[..., 0] + 2.0 ** -22 + (n + 64) * 2.0 ** -24 + 2.0 ** -23 * np.abs(lse)
+
+    def check(self, got, want):
+        out, lse = (t.double().cpu().numpy() for t in got)
+        for have, ref_, tol in ((out, want[0], self.bounds(want)[0]), (lse, want[1], self.bounds(want)[1])):
+            there = np.isfinite(ref_)
+            assert np.array_equal(np.isnan(have), np.isnan(ref_))
+            assert np.array_equal(np.isneginf(have), np.isneginf(ref_))
+            far = np.abs(have[there] - ref_[there]) / tol[there]
+            assert (far <= 1.0).all(), (float(far.max()), np.argwhere(there)[far.argmax()])
+
+
+DECODES = [
+    # lengths, heads, group, dim, page, type, rht
+    ([1], 1, 1, 32, 16, "bf16", False),
+    ([5], 8, 8, 64, 16, "bf16", False),
+    ([0, 3, 64], 2, 3, 96, 16, "bf16", True),
+    ([63, 64, 65, 1], 1, 1, 128, 32, "f32", False),
+    ([127, 128, 129, 0, 500], 2, 4, 128, 64, "bf16", True),
+    ([1000], 1, 16, 64, 256, "bf16", False),
+    ([777, 31], 2, 17, 64, 16, "bf16", True),
+    ([400, 17], 1, 40, 128, 64, "f32", True),
+    ([513], 3, 5, 160, 128, "bf16", False),
+    ([300, 2], 1, 8, 192, 16, "f32", True),
+    ([290, 0, 64], 2, 2, 256, 32, "bf16", True),
+    ([2, 900, 33] + [40] * 20, 2, 2, 64, 4096, "bf16", False),
+    ([5000], 1, 2, 128, 64, "bf16", False),
+    ([3], 2, 70, 32, 16, "bf16", False),
+]
+
+
+@pytest.mark.parametrize("case", DECODES, ids=lambda c: "-".join(str(v) for v in c)[:60])
+def test_one_query_each(case):
+    lengths, heads, group, dim, page, kind, rht = case
+    s = Setup(lengths, heads, group, dim, page, kind, rht, seed=11)
+    s.check(s.call(), s.want())
+
+
+CHUNKS = [
+    # lengths, queries, heads, group, dim, page, type, rht, window
+    ([5, 9], [2, 3], 2, 2, 64, 16, "bf16", False, 0),
+    ([200, 64, 3], [5, 1, 3], 2, 3, 96, 16, "f32", True, 0),
+    ([130], [130], 1, 4, 64, 32, "bf16", False, 0),
+    ([300, 70, 10], [33, 0, 10], 2, 5, 128, 64, "bf16", True, 0),
+    ([300, 70, 10], [33, 1, 10], 1, 3, 128, 64, "bf16", False, 20),
+    ([260, 500], [100, 7], 1, 1, 64, 16, "f32", False, 64),
+    ([600], [200], 1, 7, 32, 128, "bf16", False, 100),
+    ([70], [65], 1, 2, 256, 16, "bf16", True, 0),
+    ([40], [40], 2, 70, 64, 16, "bf16", False, 9),
+    ([90, 128], [90, 128], 1, 12, 96, 16, "bf16", False, 1),
+]
+
+
+@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "-".join(str(v) for v in c)[:60])
+@pytest.mark.parametrize("known", [True, False])
+def test_several_queries(case, known):
+    lengths, queries, heads, group, dim, page, kind, rht, window = case
+    s = Setup(lengths, heads, group, dim, page, kind, rht, queries=queries, seed=21)
+    s.check(s.call(window=window, max_queries=max(queries) if known else None), s.want(window=window))
+
+
+def test_more_queries_than_tokens():
+    """Queries that stand before the cache's first token see nothing."""
+    s = Setup([3, 0, 70], 2, 2, 64, 16, queries=[6, 4, 75], seed=31)
+    got, want = s.call(), s.want()
+    s.check(got, want)
+    assert (got[0][:3] == 0).all() and (got[0][6:10] == 0).all() and (got[1][:3] == -np.inf).all()
+
+
+@pytest.mark.parametrize("queries", [None, [4, 90, 2]])
+def test_not_causal(queries):
+    s = Setup([100, 65, 300], 2, 4, 64, 16, queries=queries, seed=41)
+    s.check(s.call(causal=False), s.want(causal=False))
+
+
+@pytest.mark.parametrize("queries", [None, [1, 3, 2]])
+@pytest.mark.parametrize("rht", [False, True])
+def test_sinks(queries, rht):
+    s = Setup([0, 65, 300], 2, 4, 64, 16, queries=queries, rht=rht, seed=51)
+    sinks = np.random.default_rng(5).normal(size=8).astype(np.float32) * 3
+    sinks[2], sinks[3], sinks[4] = -np.inf, 40.0, -60.0
+    got, want = s.call(sinks=dev(sinks)), s.want(sinks=sinks)
+    s.check(got, want)
+    assert (got[0][0] == 0).all()                          # nothing but the sink
+
+
+@pytest.mark.parametrize("window", [1, 7, 64, 128, 1000])
+def test_window(window):
+    s = Setup([1, 65, 300, 129, 900], 2, 4, 64, 16, seed=61)
+    s.check(s.call(window=window), s.want(window=window))
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.3, 4.0])
+def test_scale(scale):
+    s = Setup([200, 70], 1, 4, 64, 16, seed=71)
+    s.check(s.call(scale=scale), s.want(scale=scale))
+
+
+def test_rows_in_no_sequence_stay():
+    tt = torch()
+    s = Setup([50, 20], 1, 2, 64, 16, queries=[2, 3], seed=81)
+    _, q = values((9, 2, 64), tt.bfloat16, 82)
+    q[1:6] = s.q
+    out, lse = tt.full_like(q, 3.0), tt.full((9, 2), 5.0, device="cuda")
+    s.call(q=q, q_offsets=dev(s.offsets + 1), out=out, lse=lse)
+    s.check((out[1:6], lse[1:6]), s.want())
+    assert (out[0] == 3).all() and (out[6:] == 3).all() and (lse[0] == 5).all() and (lse[6:] == 5).all()
+
+
+@pytest.mark.parametrize("layout", ["heads first", "joint"])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_layouts(layout, kind):
+    tt = torch()
+    s = Setup([100, 70], 2, 3, 96, 16, kind, queries=[3, 2], rht=True, seed=91)
+    want = s.call()
+    out = layouts(tt.zeros_like(s.q), layout)
+    got = s.call(q=layouts(s.q, layout), out=out)
+    assert got[0] is out and tt.equal(out, want[0]) and tt.equal(got[1], want[1])
+    wide = np.full((2, s.table.shape[1] + 5), 2 ** 31 - 1, dtype=np.int32)
+    wide[:, :s.table.shape[1]] = s.table
+    view = dev(wide)[:, :s.table.shape[1]]
+    again = mx.cache_attention(s.cache(), s.q, view, dev(s.lengths), q_offsets=dev(s.offsets), need_lse=True)
+    assert tt.equal(again[0], want[0])
+
+
+@pytest.mark.parametrize("queries", [None, [3, 70, 2]])
+def test_nothing_unseen_is_read_into_a_row(queries):
+    """What the slots behind a sequence's length and the table behind its pages
+    hold has no effect."""
+    tt = torch()
+    s = Setup([70, 200, 5], 2, 2, 64, 16, queries=queries, seed=101)
+    want = s.call()
+    kept = set()
+    for row, n in zip(s.table, s.lengths):
+        kept |= set(ref.token_slots(row, int(n), 16, len(s.cache_host[0])).tolist())
+    gone = np.array([i for i in range(len(s.cache_host[0]) * 16) if i not in kept])
+    for c, sc in ((0, 1), (2, 3)):
+        s.cache_host[c][gone // 16, :, gone % 16] = 0x77
+        s.cache_host[sc][gone // 16, :, :, gone % 16] = 0xFF
+    s.table[s.table == -7] = 2 ** 31 - 1
+    got = s.call()
+    assert tt.equal(got[0], want[0]) and tt.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 10 ** 6, 2 ** 31 - 1])
+@pytest.mark.parametrize("queries", [None, [3, 70, 2]])
+def test_pages_that_do_not_exist(bad, queries):
+    s = Setup([70, 200, 16], 2, 2, 64, 16, queries=queries, seed=111)
+    s.table[0, 1] = s.table[1, 0] = s.table[1, 7] = s.table[2, 0] = bad
+    got, want = s.call(), s.want()
+    s.check(got, want)
+    assert (got[0][-1] == 0).all()
+
+
+@pytest.mark.parametrize("rht", [False, True])
+@pytest.mark.parametrize("window", [0, 40])
+def test_values_that_are_not_finite(rht, window):
+    """A NaN block of a value makes that block of the rows that see it NaN, one
+    of a key the whole row; rows that do not see it keep their results."""
+    s = Setup([150, 90], 2, 2, 64, 16, rht=rht, queries=[100, 3], seed=121)
+
+    def at(which, seq, key, head, block):
+        slot = int(ref.token_slots(s.table[seq], key + 1, 16, len(s.cache_host[0]))[-1])
+        s.cache_host[which + 1][slot // 16, head, block, slot % 16] = 255
+
+    at(2, 0, 120, 0, 1)
+    at(2, 0, 75, 1, 0)
+    at(0, 0, 140, 1, 1)
+    at(2, 1, 88, 0, 0)
+    want = s.want(window=window)
+    assert np.isnan(want[0]).any() and np.isfinite(want[0]).any()
+    s.check(s.call(window=window), want)
+
+
+def test_queries_that_are_not_finite():
+    s = Setup([100, 50], 1, 2, 64, 16, seed=131)
+    s.q[0, 1, 3] = float("nan")
+    s.q64[0, 1, 3] = np.nan
+    got = s.call()
+    s.check(got, s.want())
+
+
+def test_same_bits_every_time_and_alone():
+    """Twice the same; a sequence's rows do not depend on its neighbours but
+    for the order of their sums."""
+    tt = torch()
+    s = Setup([3000, 40, 700], 2, 4, 128, 64, rht=True, seed=141)
+    a, b = s.call(), s.call()
+    assert tt.equal(a[0], b[0]) and tt.equal(a[1], b[1])
+    one = mx.cache_attention(s.cache(), s.q[2:], dev(s.table[2:]), dev(s.lengths[2:]))[0]
+    want = s.want()
+    tol = 2 * s.bounds(want)[0][2]
+    assert (np.abs((one[0].double() - a[0][2].double()).cpu().numpy()) <= tol).all()
+
+
+def test_graphs_and_streams():
+    """Two captured calls with workspaces of their own, replayed on changing
+    inputs beside eager calls on another stream."""
+    tt = torch()
+    s = Setup([600, 40], 2, 4, 128, 64, seed=151)
+    cache, table, lengths = s.cache(), dev(s.table), dev(s.lengths)
+    q = [s.q.clone(), s.q.clone() * 0.5]
+    outs = [tt.empty_like(v) for v in q]
+    _, kv = values((2, 2, 128), tt.bfloat16, 152)
+    slot = dev(np.array([s.table[0, 599 // 64] * 64 + 599 % 64, -1], dtype=np.int32))
+    need = max(1, mx.lib().mx_cache_attention_workspace(cache._at, 2, 8, 1))
+    spaces = [tt.empty(need, dtype=tt.uint8, device="cuda") for _ in q]
+
+    def step():
+        mx.cache_write(cache, kv, kv, slot)
+        for a, o, w in zip(q, outs, spaces):
+            mx.cache_attention(cache, a, table, lengths, out=o, workspace=w)
+
+    stream = tt.cuda.Stream()
+    stream.wait_stream(tt.cuda.current_stream())
+    with tt.cuda.stream(stream):
+        step()
+    tt.cuda.current_stream().wait_stream(stream)
+    tt.cuda.synchronize()
+    graph = tt.cuda.CUDAGraph()
+    with tt.cuda.graph(graph):
+        step()
+    for i in range(4):
+        for a in q:
+            a.copy_(s.q * (1.0 + 0.25 * i))
+        kv.mul_(-1.5)
+        lengths[1] = 10 + i
+        with tt.cuda.stream(stream):
+            stream.wait_stream(tt.cuda.current_stream())
+            other = mx.cache_attention(cache, q[0] * 2, table, lengths)[0]
+        tt.cuda.current_stream().wait_stream(stream)
+        graph.replay()
+        tt.cuda.synchronize()
+        for a, o in zip(q, outs):
+            eager = mx.cache_attention(cache, a, table, lengths)[0]
+            assert tt.equal(o, eager) and tt.isfinite(other).all()
+
+
+def test_decoding_by_hand():
+    """Prompt and decoding steps through write and attention, against a plain
+    softmax over what the reads give back."""
+    tt = torch()
+    heads, group, dim, page = 2, 4, 64, 16
+    cache = mx.kv_cache(12, heads, page, dim, use_rht=True, sign_mask=MASK)
+    table = dev(np.array([[7, 2, 9, 4]], dtype=np.int32))
+    _, k = values((40, heads, dim), tt.bfloat16, 161)
+    _, v = values((40, heads, dim), tt.bfloat16, 162)
+    _, q = values((40, heads * group, dim), tt.bfloat16, 163)
+    at = tt.arange(40, device="cuda")
+    slots = (table[0].long()[at // page] * page + at % page).to(tt.int32)
+    mx.cache_write(cache, k[:30], v[:30], slots[:30])
+    length = lambda n: tt.tensor([n], dtype=tt.int32, device="cuda")  # noqa: E731
+    out = [mx.cache_attention(cache, q[:30], table, length(30), q_offsets=tt.tensor([0, 30], dtype=tt.int32, device="cuda"))[0]]
+    for i in range(30, 40):
+        mx.cache_write(cache, k[i:i + 1], v[i:i + 1], slots[i:i + 1])
+        out.append(mx.cache_attention(cache, q[i:i + 1], table, length(i + 1))[0])
+    out = tt.cat(out).double()
+    kd, vd = (t.double().repeat_interleave(group, 1) for t in mx.cache_read(cache, slots, out_dtype=tt.float32))
+    z = tt.einsum("ihd,jhd->hij", q.double(), kd) * dim ** -0.5
+    z = z.masked_fill(at[None, :] > at[:, None], -float("inf"))
+    want = tt.einsum("hij,jhd->ihd", tt.softmax(z, 2), vd)
+    # bf16 p and output: 2^-8 each of the row's sum of p |v|, the scores' 2^-16
+    size = tt.einsum("hij,jhd->ihd", tt.softmax(z, 2), vd.unflatten(2, (-1, 32)).norm(dim=3).repeat_interleave(32, 2))
+    assert ((out - want).abs() <= 2.1 * 2.0 ** -8 * size).all()
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 4 GiB of codes: slots and pages at its end."""
+    tt = torch()
+    heads, dim, page = 8, 256, 4096
+    pages = (2 ** 32 // (heads * page * dim // 2)) + 3
+    cache = mx.kv_cache(pages, heads, page, dim)
+    _, k = values((70, heads, dim), tt.bfloat16, 171)
+    _, v = values((70, heads, dim), tt.bfloat16, 172)
+    _, q = values((1, heads, dim), tt.bfloat16, 173)
+    slots = ((pages - 1) * page + tt.arange(70, device="cuda")).to(tt.int32)
+    mx.cache_write(cache, k, v, slots)
+    back = mx.cache_read(cache, slots)
+    c, s = quantized(k, False)
+    assert np.array_equal(back[0].double().cpu().numpy(), ref.decode(c, s))
+    out = mx.cache_attention(cache, q, dev(np.array([[pages - 1]], dtype=np.int32)), dev(np.array([70], dtype=np.int32)))[0]
+    small = mx.kv_cache(1, heads, page, dim)
+    mx.cache_write(small, k, v, tt.arange(70, device="cuda", dtype=tt.int32))
+    assert tt.equal(out, mx.cache_attention(small, q, dev(np.array([[0]], dtype=np.int32)), dev(np.array([70], dtype=np.int32)))[0])
+
+
+def test_no_tokens():
+    tt = torch()
+    cache = mx.kv_cache(2, 2, 16, 64)
+    none = tt.empty((0, 2, 64), dtype=tt.bfloat16, device="cuda")
+    ints = lambda *shape: tt.zeros(shape, dtype=tt.int32, device="cuda")  # noqa: E731
+    mx.cache_write(cache, none, none, ints(0))
+    assert mx.cache_read(cache, ints(0))[0].shape == (0, 2, 64)
+    assert mx.cache_attention(cache, none, ints(0, 1), ints(0))[0].shape == (0, 2, 64)
+    assert mx.cache_attention(cache, none, ints(3, 1), ints(3), q_offsets=ints(4))[0].shape == (0, 2, 64)
+    # sequences without table entries: no keys
+    q = tt.ones((2, 4, 64), dtype=tt.bfloat16, device="cuda")
+    assert (mx.cache_attention(cache, q, ints(2, 0), ints(2) + 9)[0] == 0).all()
+
+
+def test_refusals():
+    tt = torch()
+    cache = mx.kv_cache(4, 2, 16, 64)
+    x = tt.zeros((3, 2, 64), dtype=tt.bfloat16, device="cuda")
+    slots = tt.zeros(3, dtype=tt.int32, device="cuda")
+    q = tt.zeros((3, 4, 64), dtype=tt.bfloat16, device="cuda")
+    table, lengths = tt.zeros((3, 2), dtype=tt.int32, device="cuda"), tt.ones(3, dtype=tt.int32, device="cuda")
+    for bad in (lambda: mx.cache_write(cache, x[:, :1], x[:, :1], slots), lambda: mx.cache_write(cache, x, x.float(), slots),
+                lambda: mx.cache_write(cache, x, x, slots.long()), lambda: mx.cache_write(cache, x, x, slots[:2]),
+                lambda: mx.cache_write(cache, x.cpu(), x, slots), lambda: mx.cache_write(cache, x.half(), x.half(), slots),
+                lambda: mx.cache_write(cache, x[:1].expand(3, 2, 64), x, slots),
+                lambda: mx.cache_read(cache, slots.long()), lambda: mx.cache_read(cache, slots, out_dtype=tt.float16),
+                lambda: mx.cache_read(cache, slots, k=x[:2]),
+                lambda: mx.cache_attention(cache, q[..., :32], table, lengths),
+                lambda: mx.cache_attention(cache, q[:, :3], table, lengths),
+                lambda: mx.cache_attention(cache, q[:2], table, lengths),
+                lambda: mx.cache_attention(cache, q, table.long(), lengths),
+                lambda: mx.cache_attention(cache, q, table, lengths[:2]),
+                lambda: mx.cache_attention(cache, q, table, lengths, q_offsets=lengths),
+                lambda: mx.cache_attention(cache, q, table, lengths, window=3, causal=False),
+                lambda: mx.cache_attention(cache, q, table, lengths, scale=-1.0),
+                lambda: mx.cache_attention(cache, q, table, lengths, sinks=tt.zeros(3, device="cuda")),
+                lambda: mx.cache_attention(cache, q, table, lengths, out=q.float()),
+                lambda: mx.cache_attention(cache, q.half(), table, lengths),
+                lambda: mx.kv_cache(4, 2, 24, 64) and mx.cache_read(mx.kv_cache(4, 2, 24, 64), slots),
+                lambda: mx.cache_read(mx.kv_cache(4, 2, 16, 288), slots),
+                lambda: mx.KVCache(cache.k_codes, cache.k_scales, cache.v_codes[:2], cache.v_scales),
+                lambda: mx.KVCache(cache.k_codes, cache.k_codes, cache.v_codes, cache.v_scales)):
+        with pytest.raises((ValueError, TypeError, mx.MXError)):
+            bad()
