@@ -29,137 +29,803 @@ struct AttentionArgs {
     void* out;
     int64_t out_ld, out_head_ld;
     float* lse;
+    int group, tile_tokens, tile_log2, tile_heads, head_tiles, line_heads;
+    float* parts;
 };
 
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
+constexpr int UNIT = 64;              // keys that a wave takes at a time
+constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
+constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least
 
-// One wave: one query row of one head.  Lanes share the keys 64 at a time for
-// the scores, and the row's elements for the sum.
-template <bool BF16>
-__global__ __launch_bounds__(64) void attention_kernel(AttentionArgs a) {
-    __shared__ float q[256], p[64];
-    __shared__ int64_t page_of[64];
-    const int lane = threadIdx.x, dim = a.cache.dim, head = blockIdx.y;
-    const int64_t row = blockIdx.x;
-    const int kv = head / (a.q_heads / a.cache.heads);
-    int seq = (int)row;
-    int64_t first = row, rows = 1;
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4v __attribute__((ext_vector_type(4), aligned(2)));
+
+// ---------------------------------------------------------------------------
+// The work and its shares.
+//
+// A tile: up to 16 NT rows of one sequence and cache head: `tile_tokens`
+// consecutive queries (a power of two) times `tile_heads` of the group's query
+// heads.  A segment: a tile and the keys that its rows see, in units of 64.
+// All segments' units, in the order sequence, cache head (and part of its
+// group), tile, key, are one long line that the workgroups cut into equal
+// shares, whatever the lengths are: every workgroup finds its share from the
+// lengths themselves.  A segment that lies in one share is finished there; of
+// one that is cut every share leaves its part (sums, maxima) in the workspace,
+// two parts a workgroup at most, and a second launch joins them.
+// ---------------------------------------------------------------------------
+struct Seq {
+    int64_t row0;             // its first query row
+    int n, len;               // queries, keys
+};
+
+__device__ __forceinline__ Seq load_seq(const AttentionArgs& a, int s) {
+    Seq q;
+    int64_t b = s, e = s + 1;
     if (a.q_offsets) {
-        int lo = 0, hi = a.seqs;                           // the last sequence that starts at or before the row
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (mid < a.seqs ? a.q_offsets[mid] <= row : false) lo = mid;
-            else hi = mid - 1;
-        }
-        seq = lo;
-        first = a.q_offsets[seq];
-        rows = a.q_offsets[seq + 1] - first;
-        if (row < first || row >= first + rows) return;
+        b = min(max((int64_t)a.q_offsets[s], (int64_t)0), a.tokens);
+        e = min(max((int64_t)a.q_offsets[s + 1], b), a.tokens);
     }
-    const int64_t length = min(max((int64_t)a.lengths[seq], (int64_t)0), a.capacity);
-    const int64_t pos = length - rows + (row - first);
-    const int64_t end = a.causal ? pos + 1 : length, begin = a.window ? max(pos - a.window + 1, (int64_t)0) : 0;
+    q.row0 = b;
+    q.n = (int)(e - b);
+    q.len = (int)min(max((int64_t)a.lengths[s], (int64_t)0), a.capacity);
+    return q;
+}
 
-    const int64_t at = row * a.q_ld + head * a.q_head_ld + 8 * lane;
-    if (8 * lane < dim) {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)a.q)[at + i] << 16) : ((const float*)a.q)[at + i];
-        if (a.cache.rht) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = (a.cache.mask >> (8 * (lane & 3) + i)) & 1 ? -f[i] : f[i];
-            rht32_quad(f, lane & 3);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[8 * lane + i] = f[i];
+// Of a sequence's tile i: the first unit that its rows see, and the one after
+// the last (a tile whose rows see nothing still has one).
+__device__ __forceinline__ int first_unit(const AttentionArgs& a, const Seq& q, int i) {
+    return a.window ? max(q.len - q.n + i * a.tile_tokens - a.window + 1, 0) / UNIT : 0;
+}
+__device__ __forceinline__ int end_unit(const AttentionArgs& a, const Seq& q, int i) {
+    const int hi = a.causal ? q.len - q.n + min((i + 1) * a.tile_tokens, q.n) : q.len;
+    return max((hi + UNIT - 1) / UNIT, 1);
+}
+__device__ __forceinline__ int tiles_of(const AttentionArgs& a, const Seq& q) {
+    return (q.n + a.tile_tokens - 1) >> a.tile_log2;
+}
+
+// Units of a sequence's first x tiles, all of them full ones.  With t =
+// tile_tokens and Q = 64 / t, tile i's end is at ceil((b + i + 1) / Q) for a b
+// made of the sequence's lengths, its begin at floor((c + i) / Q): sums of
+// ceil(j / Q) and floor(j / Q) over a stretch of j.
+__device__ __forceinline__ int64_t sum_ceil(int64_t y, int q_log2) {       // over j = 1 .. y
+    const int64_t w = y >> q_log2, r = y - (w << q_log2);
+    return ((w * (w + 1) >> 1) << q_log2) + r * (w + 1);
+}
+__device__ __forceinline__ int64_t sum_floor(int64_t y, int q_log2) {      // over j = 0 .. y - 1
+    const int64_t w = y >> q_log2, r = y - (w << q_log2);
+    return ((w * (w - 1) >> 1) << q_log2) + r * w;
+}
+__device__ __forceinline__ int64_t units_before(const AttentionArgs& a, const Seq& q, int x) {
+    if (!a.causal) return (int64_t)x * end_unit(a, q, 0);
+    const int q_log2 = 6 - a.tile_log2;
+    const int64_t at = q.len - q.n;
+    const int64_t b = (at + a.tile_tokens - 1) >> a.tile_log2;
+    int64_t units = min((int64_t)x, max(-b, (int64_t)0));                  // tiles before the first key: one each
+    units += sum_ceil(max(b + x, (int64_t)0), q_log2) - sum_ceil(max(b, (int64_t)0), q_log2);
+    if (a.window) {
+        const int64_t c = (at - a.window + 1) >> a.tile_log2;
+        units -= sum_floor(max(c + x, (int64_t)0), q_log2) - sum_floor(max(c, (int64_t)0), q_log2);
     }
+    return units;
+}
+__device__ __forceinline__ int64_t units_of(const AttentionArgs& a, const Seq& q) {
+    const int tiles = tiles_of(a, q);
+    if (tiles == 0) return 0;
+    return units_before(a, q, tiles - 1) + end_unit(a, q, tiles - 1) - first_unit(a, q, tiles - 1);
+}
+
+// Where unit `at` of the line lies; the line's length.
+struct Line {
+    int64_t before[WAVES * 64 + 1];       // units before each thread's stretch of sequences
+    int64_t wave_units[WAVES];
+};
+
+struct Segment {
+    Seq seq;
+    int s, head, tile;        // sequence, cache head * head_tiles + part of its group, tile
+    int begin, end;           // its units (of keys)
+    int64_t start;            // its first unit's place in the line
+};
+
+__device__ __forceinline__ void measure_line(const AttentionArgs& a, Line& line) {
+    const int tid = threadIdx.x, per = (a.seqs + WAVES * 64 - 1) / (WAVES * 64);
+    int64_t mine = 0;
+    for (int s = tid * per; s < min((tid + 1) * per, a.seqs); ++s) mine += units_of(a, load_seq(a, s));
+    mine *= a.line_heads;
+    int64_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t other = __shfl_up(sum, d);
+        if ((tid & 63) >= d) sum += other;
+    }
+    if ((tid & 63) == 63) line.wave_units[tid >> 6] = sum;
     __syncthreads();
+    int64_t base = 0;
+    for (int w = 0; w < tid >> 6; ++w) base += line.wave_units[w];
+    line.before[tid] = base + sum - mine;
+    if (tid == WAVES * 64 - 1) line.before[WAVES * 64] = base + sum;
+    __syncthreads();
+}
 
-    float top = a.sinks ? a.sinks[head] * LOG2E : -__builtin_inff(), sum = a.sinks ? 1.0f : 0.0f;
-    float acc[4] = {};                                     // elements 2 lane, 2 lane + 1, and those 128 further
-    const int bytes = dim >> 1, shift = a.cache.page_log2;
-    for (int64_t base = begin; base < end; base += 64) {
-        const int64_t key = base + lane;
-        int64_t page = key < end ? a.table[seq * a.table_ld + (key >> shift)] : -1;
-        if (page >= a.cache.pages) page = -1;
-        const int offset = (int)(key & ((1 << shift) - 1));
-        float s = -__builtin_inff();
-        if (page >= 0) {
-            const uint8_t* codes = a.cache.codes[0] + a.cache.codes_at(page, kv, offset);
-            const uint8_t* scales = a.cache.scales[0] + a.cache.scales_at(page, kv, offset);
-            float dot = 0.0f;
-            for (int d = 0; d < dim; d += 8) {
-                const uint32_t byte = scales[(int64_t)(d >> 5) << shift];
-                float f[8];
-                decode8(*(const uint32_t*)(codes + (d >> 1)), scale_operand(byte), f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(q[d + i], byte == 0xFF ? __builtin_nanf("") : f[i], dot);
-            }
-            s = dot * a.scale;
+__device__ __forceinline__ void set_tile(const AttentionArgs& a, Segment& g) {
+    g.begin = first_unit(a, g.seq, g.tile);
+    g.end = end_unit(a, g.seq, g.tile);
+}
+
+// The segment that holds unit `at`, 0 <= at < the line's length.
+__device__ __forceinline__ Segment locate(const AttentionArgs& a, const Line& line, int64_t at) {
+    Segment g;
+    int lo = 0, hi = WAVES * 64 - 1;                       // the last stretch that starts at or before it
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (line.before[mid] <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    const int per = (a.seqs + WAVES * 64 - 1) / (WAVES * 64);
+    int64_t from = line.before[lo], units;
+    g.s = lo * per;
+    for (;; ++g.s) {
+        g.seq = load_seq(a, g.s);
+        units = units_of(a, g.seq);
+        if (at < from + units * a.line_heads) break;
+        from += units * a.line_heads;
+    }
+    g.head = (int)((at - from) / units);
+    from += g.head * units;
+    lo = 0;
+    hi = tiles_of(a, g.seq) - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (from + units_before(a, g.seq, mid) <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    g.tile = lo;
+    g.start = from + units_before(a, g.seq, lo);
+    set_tile(a, g);
+    return g;
+}
+
+__device__ __forceinline__ void next_segment(const AttentionArgs& a, Segment& g) {
+    g.start += g.end - g.begin;
+    if (++g.tile == tiles_of(a, g.seq)) {
+        g.tile = 0;
+        if (++g.head == a.line_heads) {
+            g.head = 0;
+            do g.seq = load_seq(a, ++g.s);
+            while (g.seq.n == 0);
         }
-        float m = s;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-        m = fmaxf(m, top);
-        const float safe = m == -__builtin_inff() ? 0.0f : m, keep = __builtin_amdgcn_exp2f(top - safe);
-        const float w = page < 0 ? 0.0f : __builtin_amdgcn_exp2f(s - safe);
-        float total = w;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
-        sum = sum * keep + total;
+    }
+    set_tile(a, g);
+}
+
+// A tile's row c: its query row and head; false where there is none.
+struct Row {
+    int64_t token;
+    int head, query;          // query: its number in the sequence
+};
+__device__ __forceinline__ bool row_of(const AttentionArgs& a, const Segment& g, int c, Row& r) {
+    const int t = c / a.tile_heads, part = g.head / a.head_tiles;
+    const int h = (g.head - part * a.head_tiles) * a.tile_heads + c - t * a.tile_heads;
+    r.query = (g.tile << a.tile_log2) + t;
+    r.token = g.seq.row0 + r.query;
+    r.head = part * a.group + h;
+    return t < a.tile_tokens && h < a.group && r.query < g.seq.n;
+}
+
+// ---------------------------------------------------------------------------
+// Eight elements of a row from the tile's sums: the sink, the division, the
+// transform back, the rounding.  top, sum: the row's maximum (times log2 e) and
+// sum; o relative to that maximum.  Four lanes hold a block of 32; all of them
+// call.
+// ---------------------------------------------------------------------------
+template <bool BF16>
+__device__ __forceinline__ void finish(const AttentionArgs& a, const Row& r, bool live, int d, float* o, float top,
+                                       float sum) {
+    if (a.sinks) {
+        const float sink = live ? a.sinks[r.head] * LOG2E : 0.0f, m = fmaxf(top, sink);
+        const float safe = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(top - safe);
+        sum = sum * f + __builtin_amdgcn_exp2f(sink - safe);
         top = m;
-        __syncthreads();
-        p[lane] = w;
-        page_of[lane] = page;
-        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] *= keep;
-        const int n = (int)min((int64_t)64, end - base);
-        for (int j = 0; j < n; ++j) {
-            if (page_of[j] < 0) continue;
-            const int o = (int)((base + j) & ((1 << shift) - 1));
-            const int64_t c = a.cache.codes_at(page_of[j], kv, o), sc = a.cache.scales_at(page_of[j], kv, o);
+        for (int i = 0; i < 8; ++i) o[i] *= f;
+    }
+    const float inv = 1.0f / sum;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int b = lane + 64 * h;
-                if (b >= bytes) continue;
-                const uint32_t byte = a.cache.scales[1][sc + ((int64_t)(b >> 4) << shift)];
-                const v2f v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(a.cache.codes[1][c + b], scale_operand(byte), 0);
-                acc[2 * h] = __builtin_fmaf(p[j], byte == 0xFF ? __builtin_nanf("") : v[0], acc[2 * h]);
-                acc[2 * h + 1] = __builtin_fmaf(p[j], byte == 0xFF ? __builtin_nanf("") : v[1], acc[2 * h + 1]);
+    for (int i = 0; i < 8; ++i) o[i] = sum == 0.0f ? 0.0f : o[i] * inv;
+    if (a.cache.rht) {
+        rht32_quad(o, (d >> 3) & 3);
+        const uint32_t m = a.cache.mask >> (d & 31);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(__float_as_uint(o[i]) ^ (m >> i << 31));
+    }
+    if (!live || d >= a.cache.dim) return;
+    const int64_t at = r.token * a.out_ld + r.head * a.out_head_ld + d;
+    if constexpr (BF16) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16_rne(o[2 * i]) | f32_to_bf16_rne(o[2 * i + 1]) << 16;
+        *(u32x4v*)((uint16_t*)a.out + at) = (u32x4v){u[0], u[1], u[2], u[3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *(u32x4v*)((float*)a.out + at + 4 * i) =
+                (u32x4v){__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                         __float_as_uint(o[4 * i + 3])};
+    }
+    if (a.lse && d == 0)
+        a.lse[r.token * a.q_heads + r.head] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2;
+}
+
+// A part in the workspace: sums [rows][32 NB], maxima [rows], sums of p [rows].
+template <int NB, int NT>
+struct Part {
+    static constexpr int ROWS = 16 * NT, FLOATS = ROWS * (32 * NB + 2);
+    float* p;
+    __device__ __forceinline__ Part(const AttentionArgs& a, int64_t i) : p(a.parts + i * FLOATS) {}
+    __device__ __forceinline__ float* row(int c) const { return p + c * 32 * NB; }
+    __device__ __forceinline__ float& top(int c) const { return p[ROWS * 32 * NB + c]; }
+    __device__ __forceinline__ float& sum(int c) const { return p[ROWS * 32 * NB + ROWS + c]; }
+};
+
+__device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ bf16x8 operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint4 v = {a, b, c, d};
+    return __builtin_bit_cast(bf16x8, v);
+}
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+// Two fp32 as bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    bf16x2 v;
+    v[0] = (__bf16)lo;
+    v[1] = (__bf16)hi;
+    return bits(v);
+}
+
+// Eight codes and their scale as bf16, exactly (E2M1 times a power of two).
+__device__ __forceinline__ void widen8(uint32_t w, float scale, uint32_t* u) {
+    u[0] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+    u[1] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+    u[2] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+    u[3] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+}
+__device__ __forceinline__ float scale_of(uint32_t word, int byte) {       // byte: 0..3
+    return scale_operand((word >> (8 * byte)) & 0xFFu);
+}
+
+// ---------------------------------------------------------------------------
+// The kernel.  A wave takes 64 keys and all rows of its tile:
+//   S^T = K Q^T   16x16x32 products, keys down, rows across: K's codes of a
+//                 lane are consecutive in memory (8 NB of them), Q comes from
+//                 LDS in the same order of elements;
+//   softmax       a lane has 4 keys of one row in each product, so maxima and
+//                 sums over the keys take two exchanges between lanes;
+//   O^T = V^T P^T the lane's own p are what the product wants of it when the
+//                 keys go in the order (group of 8, product, number): no p
+//                 changes lanes.  V's elements of a lane are 2 NB consecutive
+//                 ones of eight keys; converted key by key and paired by two
+//                 byte permutations.
+// Keys of a wave's 64: 32 j + 8 g + 4 t + i is row 4 g + i of score product
+// (j, t).  Lane l: column l & 15, group g = l >> 4.
+// NB: blocks of 32 that a row is padded to (2, 4, 8); NT: products of 16 rows.
+// QT: terms of q; PT: terms of p.
+// ---------------------------------------------------------------------------
+template <int NB, int NT, int QT>
+struct Shared {
+    static constexpr int PITCH = 32 * NB + 8;              // bf16: rows 4 banks apart
+    static constexpr int SIDE = NB == 8 ? 128 : 32 * NB, OUT_PITCH = SIDE + 4;
+    static constexpr int Q_BYTES = QT * 16 * NT * PITCH * 2, O_BYTES = WAVES * 16 * OUT_PITCH * 4;
+    alignas(16) unsigned char data[Q_BYTES > O_BYTES ? Q_BYTES : O_BYTES];
+    float top[WAVES][16 * NT], sum[WAVES][16 * NT];
+    Line line;
+};
+
+template <int NB, int NT, bool BF16, int QT, int PT>
+__global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attention_kernel(AttentionArgs a) {
+    using Sh = Shared<NB, NT, QT>;
+    constexpr int M = 2 * NB;                              // elements of V that a lane has, products of the sum
+    constexpr int VW = NB == 8 ? 2 : 1;                    // dwords they take
+    __shared__ Sh sh;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int shift = a.cache.page_log2, row_bytes = a.cache.dim >> 1, blocks = a.cache.dim >> 5;
+
+    measure_line(a, sh.line);
+    const int64_t total = sh.line.before[WAVES * 64];
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MIN_UNITS);
+    const int64_t begin = blockIdx.x * per, stop = min(begin + per, total);
+    if (begin >= total) return;
+    Segment seg = locate(a, sh.line, begin);
+
+    for (int64_t at = begin;;) {
+        // the rows' queries
+        const int head = seg.head / a.head_tiles;          // of the cache
+        const int rows = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2)) * a.tile_heads;
+        __syncthreads();
+        for (int i = tid; i < 16 * NT * 4 * NB; i += WAVES * 64) {
+            const int c = i / (4 * NB), d = i % (4 * NB) * 8;
+            Row r;
+            const bool live = row_of(a, seg, c, r) && d < a.cache.dim;
+            const int64_t from = r.token * a.q_ld + r.head * a.q_head_ld + d;
+            float f[8] = {};
+            if (live) {
+                if constexpr (BF16) {
+                    const u32x4v w = *(const u32x4v*)((const uint16_t*)a.q + from);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { f[2 * e] = bf16lo(u[e]); f[2 * e + 1] = bf16hi(u[e]); }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const u32x4v w = *(const u32x4v*)((const float*)a.q + from + 4 * e);
+                        f[4 * e] = __uint_as_float(w.x);
+                        f[4 * e + 1] = __uint_as_float(w.y);
+                        f[4 * e + 2] = __uint_as_float(w.z);
+                        f[4 * e + 3] = __uint_as_float(w.w);
+                    }
+                }
+            }
+            if (a.cache.rht) {
+                const uint32_t m = a.cache.mask >> (d & 31);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(__float_as_uint(f[e]) ^ (m >> e << 31));
+                rht32_quad(f, (d >> 3) & 3);
+            }
+            uint32_t u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = pack(f[2 * e], f[2 * e + 1]);
+            __bf16* q = (__bf16*)sh.data + c * Sh::PITCH + d;
+            *(uint4*)q = make_uint4(u[0], u[1], u[2], u[3]);
+            if constexpr (QT == 2) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // (an infinite element has no rest)
+                    const float lo = bf16lo(u[e]), hi = bf16hi(u[e]);
+                    w[e] = pack(__builtin_isinf(lo) ? 0.0f : f[2 * e] - lo, __builtin_isinf(hi) ? 0.0f : f[2 * e + 1] - hi);
+                }
+                *(uint4*)(q + 16 * NT * Sh::PITCH) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    __syncthreads();
+        __syncthreads();
+
+        // the keys that each of the lane's rows sees, and those that all see
+        int last[NT], low[NT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (lane + 64 * h >= bytes) continue;
-        q[2 * (lane + 64 * h)] = sum == 0.0f ? 0.0f : acc[2 * h] * inv;
-        q[2 * (lane + 64 * h) + 1] = sum == 0.0f ? 0.0f : acc[2 * h + 1] * inv;
-    }
-    __syncthreads();
-    if (8 * lane < dim) {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = q[8 * lane + i];
-        if (a.cache.rht) {
-            rht32_quad(f, lane & 3);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = (a.cache.mask >> (8 * (lane & 3) + i)) & 1 ? -f[i] : f[i];
+        for (int n = 0; n < NT; ++n) {
+            Row r;
+            const bool live = row_of(a, seg, 16 * n + col, r);
+            const int pos = seg.seq.len - seg.seq.n + r.query;
+            last[n] = !live ? -1 : a.causal ? pos : seg.seq.len - 1;
+            low[n] = a.window ? pos - a.window + 1 : 0;
         }
-        const int64_t to = row * a.out_ld + head * a.out_head_ld + 8 * lane;
+        const int pos0 = seg.seq.len - seg.seq.n + (seg.tile << a.tile_log2);
+        const int all_to = a.causal ? pos0 : seg.seq.len - 1;
+        const int all_from = a.window ? pos0 + rows / a.tile_heads - 1 - a.window + 1 : 0;
+
+        f32x4 acc[NT][M];
+        float top[NT], sum[NT];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (BF16) ((uint16_t*)a.out)[to + i] = (uint16_t)f32_to_bf16_rne(f[i]);
-            else ((float*)a.out)[to + i] = f[i];
+        for (int n = 0; n < NT; ++n) {
+            top[n] = -__builtin_inff();
+            sum[n] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) acc[n][m] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
         }
+
+        const int unit0 = seg.begin + (int)(at - seg.start);
+        const int unit1 = (int)min((int64_t)seg.end, seg.begin + (stop - seg.start));
+        // (a sequence without keys has no pages to look at)
+        const int units = seg.seq.len == 0 ? 0 : unit1;
+        const int32_t* table = a.table + seg.s * a.table_ld;
+        const int last_group = (seg.seq.len - 1) & ~7;
+
+        uint32_t kc[2][2][NB];        // codes of K: [j][t]
+        uint2 ks[2][NB == 8 ? 2 : 1]; // eight keys' scales of the lane's blocks
+        uint32_t vc[2][8][VW];        // codes of V: [j][key]
+        uint2 vs[2];
+        int page_k[2], page_v[2];     // of the unit after
+        const int kg = 8 * (col >> 2);                     // the lane's group of keys in a score product
+        const bool v_there = col * NB < row_bytes;
+
+        auto look_up = [&](int unit) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                page_k[j] = table[min(UNIT * unit + 32 * j + kg, last_group) >> shift];
+                page_v[j] = table[min(UNIT * unit + 32 * j + 8 * g, last_group) >> shift];
+            }
+        };
+        auto good = [&](int page) { return page >= 0 && page < (int)a.cache.pages; };
+        auto load_k = [&](int unit, int j, int page) {
+            const int o = (min(UNIT * unit + 32 * j + kg, last_group)) & ((1 << shift) - 1);
+            const int64_t p = (int64_t)(good(page) ? page : 0) * a.cache.heads + head;
+            const uint8_t* codes = a.cache.codes[0] + ((p << shift) + o + (col & 3)) * row_bytes;
+            const uint8_t* scales = a.cache.scales[0] + (p * blocks << shift) + o;
+            if constexpr (NB == 2) {
+                const bool there = 8 * g < row_bytes;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint2 w = *(const uint2*)(codes + (4 * t) * row_bytes + (there ? 8 * g : 0));
+                    kc[j][t][0] = there ? w.x : 0u;
+                    kc[j][t][1] = there ? w.y : 0u;
+                }
+                ks[j][0] = *(const uint2*)(scales + ((int64_t)(there ? g >> 1 : 0) << shift));
+                if (!there) ks[j][0] = make_uint2(0u, 0u);
+            } else {
+#pragma unroll
+                for (int h = 0; h < NB / 4; ++h) {
+                    const int block = g * (NB / 4) + h;
+                    const bool there = block < blocks;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint4 w = *(const uint4*)(codes + (4 * t) * row_bytes + (there ? 16 * block : 0));
+                        kc[j][t][4 * h] = there ? w.x : 0u;
+                        kc[j][t][4 * h + 1] = there ? w.y : 0u;
+                        kc[j][t][4 * h + 2] = there ? w.z : 0u;
+                        kc[j][t][4 * h + 3] = there ? w.w : 0u;
+                    }
+                    ks[j][h] = *(const uint2*)(scales + ((int64_t)(there ? block : 0) << shift));
+                    if (!there) ks[j][h] = make_uint2(0u, 0u);
+                }
+            }
+        };
+        auto load_v = [&](int unit, int j, int page) {
+            const int o = (min(UNIT * unit + 32 * j + 8 * g, last_group)) & ((1 << shift) - 1);
+            const int64_t p = (int64_t)(good(page) ? page : 0) * a.cache.heads + head;
+            const int c = v_there ? col : 0;
+            const uint8_t* codes = a.cache.codes[1] + ((p << shift) + o) * row_bytes + c * NB;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint8_t* from = codes + i * row_bytes;
+                if constexpr (NB == 2) vc[j][i][0] = *(const uint16_t*)from;
+                else if constexpr (NB == 4) vc[j][i][0] = *(const uint32_t*)from;
+                else {
+                    const uint2 w = *(const uint2*)from;
+                    vc[j][i][0] = w.x;
+                    vc[j][i][VW - 1] = w.y;
+                }
+            }
+            vs[j] = *(const uint2*)(a.cache.scales[1] + ((p * blocks + c * NB / 16) << shift) + o);
+        };
+
+        bool bad[2] = {false, false};                      // the lane's groups of keys in this unit do not exist
+        bf16x8 qf[QT][NB];
+        if constexpr (NT == 1) {
+#pragma unroll
+            for (int x = 0; x < QT; ++x)
+#pragma unroll
+                for (int s = 0; s < NB; ++s)
+                    qf[x][s] = *(const bf16x8*)((const __bf16*)sh.data + (x * 16 + col) * Sh::PITCH + 8 * NB * g + 8 * s);
+        }
+        int unit = unit0 + wave;
+        if (unit < units) {
+            look_up(unit);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                load_k(unit, j, page_k[j]);
+                load_v(unit, j, page_v[j]);
+                bad[j] = !good(page_v[j]);
+            }
+            look_up(min(unit + WAVES, units - 1));
+        }
+        for (; unit < units; unit += WAVES) {
+            const int key0 = UNIT * unit, ahead = min(unit + WAVES, units - 1);
+            const bool whole = key0 + UNIT - 1 <= all_to && key0 >= all_from && !__any(bad[0] || bad[1]);
+            const int next_k[2] = {page_k[0], page_k[1]}, next_v[2] = {page_v[0], page_v[1]};
+            look_up(min(unit + 2 * WAVES, units - 1));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // scores
+                f32x4 s[NT][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t kf[NB][4];
+#pragma unroll
+                    for (int x = 0; x < NB; ++x) {
+                        const uint2 w = ks[j][NB == 8 ? x >> 2 : 0];
+                        widen8(kc[j][t][x], scale_of(t ? w.y : w.x, col & 3), kf[x]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        s[n][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int y = 0; y < QT; ++y)
+#pragma unroll
+                            for (int x = 0; x < NB; ++x) {
+                                bf16x8 q;
+                                if constexpr (NT == 1) q = qf[y][x];
+                                else
+                                    q = *(const bf16x8*)((const __bf16*)sh.data +
+                                                         (y * 16 * NT + 16 * n + col) * Sh::PITCH + 8 * NB * g + 8 * x);
+                                s[n][t] = mfma(operand(kf[x][0], kf[x][1], kf[x][2], kf[x][3]), q, s[n][t]);
+                            }
+                    }
+                }
+                load_k(ahead, j, next_k[j]);
+
+                // softmax of these 32 keys
+                uint32_t p[NT][PT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = s[n][i >> 2][i & 3] * a.scale;
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int key = key0 + 32 * j + 8 * g + i;
+                            x[i] = key <= last[n] && key >= low[n] && !bad[j] ? x[i] : -__builtin_inff();
+                        }
+                    }
+                    float m = x[0];
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
+                    m = fmaxf(m, __shfl_xor(m, 16));
+                    m = fmaxf(m, __shfl_xor(m, 32));
+                    m = fmaxf(m, top[n]);
+                    const float safe = m == -__builtin_inff() ? 0.0f : m;
+                    if (__any(m > top[n])) {
+                        const float f = __builtin_amdgcn_exp2f(top[n] - safe);
+                        sum[n] *= f;
+#pragma unroll
+                        for (int k = 0; k < M; ++k) acc[n][k] *= f;
+                    }
+                    top[n] = m;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = __builtin_amdgcn_exp2f(x[i] - safe);
+                        sum[n] += x[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p[n][0][i] = pack(x[2 * i], x[2 * i + 1]);
+                        if constexpr (PT == 2)
+                            p[n][PT - 1][i] = pack(x[2 * i] - bf16lo(p[n][0][i]), x[2 * i + 1] - bf16hi(p[n][0][i]));
+                    }
+                }
+
+                // sums
+                uint2 scales = vs[j];
+                if (!whole) {
+                    // A value that is not finite reaches the rows that see it, and no others: its scale becomes 0
+                    // here, and a product of the marks "not finite" and "seen" says where there was one.
+                    bool odd = false;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) odd |= ((((i < 4 ? scales.x : scales.y) >> (8 * (i & 3))) & 0xFFu) == 0xFFu);
+                    if (__any(odd)) {
+                        uint32_t mark[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t& w = i < 4 ? scales.x : scales.y;
+                            const uint32_t byte = 0xFFu << (8 * (i & 3));
+                            if ((w & byte) == byte) {
+                                w &= ~byte;
+                                mark[i >> 1] |= 0x3F80u << (16 * (i & 1));
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t seen[4] = {0, 0, 0, 0};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int key = key0 + 32 * j + 8 * g + i;
+                                if (key <= last[n] && key >= low[n] && !bad[j]) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
+                            }
+                            const f32x4 hit = mfma(operand(mark[0], mark[1], mark[2], mark[3]),
+                                                   operand(seen[0], seen[1], seen[2], seen[3]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (hit[i] == 0.0f) continue;
+#pragma unroll
+                                for (int k = 0; k < M; ++k) acc[n][k][i] = __builtin_nanf("");
+                            }
+                        }
+                    }
+                }
+                uint32_t u[8][NB];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float sc = scale_of(i < 4 ? scales.x : scales.y, i & 3);
+                    if constexpr (NB == 2) {
+                        u[i][0] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vc[j][i][0], sc, 0));
+                        u[i][1] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vc[j][i][0], sc, 1));
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < VW; ++h) widen8(vc[j][i][h], sc, &u[i][4 * h]);
+                    }
+                }
+                load_v(ahead, j, next_v[j]);
+#pragma unroll
+                for (int k = 0; k < M; ++k) {
+                    const uint32_t sel = k & 1 ? 0x07060302u : 0x05040100u;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(u[2 * i + 1][k >> 1], u[2 * i][k >> 1], sel);
+                    const bf16x8 v = operand(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int y = 0; y < PT; ++y)
+                            acc[n][k] = mfma(v, operand(p[n][y][0], p[n][y][1], p[n][y][2], p[n][y][3]), acc[n][k]);
+                }
+                bad[j] = !good(next_v[j]);
+            }
+        }
+
+        // the waves' maxima and sums, then their rows
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            sum[n] += __shfl_xor(sum[n], 16);
+            sum[n] += __shfl_xor(sum[n], 32);
+            if (g == 0) {
+                sh.top[wave][16 * n + col] = top[n];
+                sh.sum[wave][16 * n + col] = sum[n];
+            }
+        }
+        __syncthreads();                                   // (also: nobody reads the queries any more)
+        const bool complete = at == seg.start && unit1 == seg.end;
+        const Part<NB, NT> part(a, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
+        constexpr int SIDES = 32 * NB / Sh::SIDE;
+        float* o = (float*)sh.data;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (16 * n >= rows) break;
+            float m = sh.top[0][16 * n + col];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) m = fmaxf(m, sh.top[w][16 * n + col]);
+            const float f = __builtin_amdgcn_exp2f(top[n] - (m == -__builtin_inff() ? 0.0f : m));
+#pragma unroll
+            for (int side = 0; side < SIDES; ++side) {
+                // the lane's elements of a row are consecutive, 8 NB of them: 32 blocks' worth a side
+                float* to = o + (wave * 16 + col) * Sh::OUT_PITCH + g * (Sh::SIDE / 4);
+                constexpr int PER = 4 / SIDES;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+#pragma unroll
+                    for (int k = 0; k < M; k += 4)
+                        *(f32x4*)(to + i * M + k) = (f32x4){acc[n][k][side * PER + i] * f, acc[n][k + 1][side * PER + i] * f,
+                                                            acc[n][k + 2][side * PER + i] * f, acc[n][k + 3][side * PER + i] * f};
+                __syncthreads();
+                for (int i = tid; i < 16 * Sh::SIDE / 8; i += WAVES * 64) {
+                    const int c = i / (Sh::SIDE / 8), e = i % (Sh::SIDE / 8) * 8;
+                    const int d = SIDES == 1 ? e : (e >> 5) * 64 + side * 32 + (e & 31);
+                    float most = sh.top[0][16 * n + c];
+#pragma unroll
+                    for (int w = 1; w < WAVES; ++w) most = fmaxf(most, sh.top[w][16 * n + c]);
+                    const float safe = most == -__builtin_inff() ? 0.0f : most;
+                    float all = 0.0f, v[8] = {};
+#pragma unroll
+                    for (int w = 0; w < WAVES; ++w) {
+                        all += sh.sum[w][16 * n + c] * __builtin_amdgcn_exp2f(sh.top[w][16 * n + c] - safe);
+                        const float* from = o + (w * 16 + c) * Sh::OUT_PITCH + e;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) v[y] += from[y];
+                    }
+                    Row r;
+                    const bool live = row_of(a, seg, 16 * n + c, r);
+                    if (complete) {
+                        finish<BF16>(a, r, live, d, v, most, all);
+                    } else if (live) {
+                        float* to_part = part.row(16 * n + c) + d;
+                        *(f32x4*)to_part = (f32x4){v[0], v[1], v[2], v[3]};
+                        *(f32x4*)(to_part + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+                        if (d == 0) {
+                            part.top(16 * n + c) = most;
+                            part.sum(16 * n + c) = all;
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        at = seg.start + (seg.end - seg.begin);
+        if (at >= stop) return;
+        next_segment(a, seg);
     }
-    if (a.lse && lane == 0)
-        a.lse[row * a.q_heads + head] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2;
+}
+
+// Joins the parts of the segments that were cut.  Workgroup x: the segment
+// that the x + 1st cut goes through, if that is the first cut in it; y: four
+// of its rows.  The parts are shared by `groups` sets of threads.
+template <int NB, int NT, bool BF16>
+__global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArgs a, int shares) {
+    constexpr int PIECES = 4 * NB, ITEMS = 4 * PIECES, GROUPS = WAVES * 64 / ITEMS;
+    __shared__ Line line;
+    __shared__ float o[GROUPS][ITEMS][8 + 1], sums[GROUPS][4], tops[GROUPS][4];
+    measure_line(a, line);
+    const int64_t total = line.before[WAVES * 64];
+    const int64_t per = max((total + shares - 1) / shares, (int64_t)MIN_UNITS);
+    const int64_t cut = (blockIdx.x + 1) * per;
+    if (cut >= total) return;
+    const Segment seg = locate(a, line, cut);
+    if (seg.start == cut || seg.start < cut - per) return;
+    const int rows = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2)) * a.tile_heads;
+    if (4 * (int)blockIdx.y >= rows) return;
+    const int64_t end = seg.start + seg.end - seg.begin;
+    const int first = blockIdx.x, count = (int)((end - 1) / per) - first + 1;
+    const int64_t slot0 = 2 * (int64_t)first + (seg.start == first * per ? 0 : 1);
+    const int item = threadIdx.x % ITEMS, group = threadIdx.x / ITEMS;
+    const int c = 4 * blockIdx.y + item / PIECES, d = item % PIECES * 8;
+    float top = -__builtin_inff(), sum = 0.0f, v[8] = {};
+    for (int i = group; i < count; i += GROUPS) {
+        const Part<NB, NT> part(a, i == 0 ? slot0 : 2 * (int64_t)(first + i));
+        const bool there = c < rows;
+        const float t = there ? part.top(c) : -__builtin_inff(), l = there ? part.sum(c) : 0.0f;
+        const f32x4 x = there ? *(const f32x4*)(part.row(c) + d) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        const f32x4 y = there ? *(const f32x4*)(part.row(c) + d + 4) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        const float m = fmaxf(top, t), safe = m == -__builtin_inff() ? 0.0f : m;
+        const float f = __builtin_amdgcn_exp2f(top - safe), e = __builtin_amdgcn_exp2f(t - safe);
+        sum = sum * f + l * e;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = v[k] * f + x[k] * e;
+            v[4 + k] = v[4 + k] * f + y[k] * e;
+        }
+        top = m;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[group][item][k] = v[k];
+    if (d == 0) {
+        tops[group][item / PIECES] = top;
+        sums[group][item / PIECES] = sum;
+    }
+    __syncthreads();
+    if (group != 0) return;
+    const int rr = item / PIECES;
+    float most = tops[0][rr];
+    for (int w = 1; w < GROUPS; ++w) most = fmaxf(most, tops[w][rr]);
+    const float safe = most == -__builtin_inff() ? 0.0f : most;
+    float all = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+    for (int w = 0; w < GROUPS; ++w) {
+        const float e = __builtin_amdgcn_exp2f(tops[w][rr] - safe);
+        all += sums[w][rr] * e;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += o[w][item][k] * e;
+    }
+    Row r;
+    const bool live = row_of(a, seg, c, r) && c < rows;
+    finish<BF16>(a, r, live, d, v, most, all);
+}
+
+// What the host chooses from the sizes it knows.
+struct Shape {
+    int nb, nt, tile_tokens, tile_heads, head_tiles;
+    int64_t shares, part_floats;
+};
+
+Shape shape_of(const CacheView& c, int64_t tokens, int q_heads, int max_queries) {
+    Shape s;
+    const int group = q_heads / c.heads;
+    const int64_t most = max_queries > 0 ? min((int64_t)max_queries, tokens) : tokens;
+    s.nb = c.dim <= 64 ? 2 : c.dim <= 128 ? 4 : 8;
+    const int64_t rows = most * group;
+    s.nt = rows <= 16 ? 1 : rows <= 32 || s.nb == 8 ? 2 : 4;
+    const int r = 16 * s.nt;
+    s.tile_heads = min(group, r);
+    s.head_tiles = (group + r - 1) / r;
+    s.tile_tokens = 1;
+    while (2 * s.tile_tokens * s.tile_heads <= r) s.tile_tokens *= 2;
+    s.shares = s.nt == 1 && s.nb < 8 ? 1024 : 512;
+    s.part_floats = (int64_t)r * (32 * s.nb + 2);
+    return s;
+}
+
+template <int NB, int NT>
+void launch(const AttentionArgs& a, bool bf16, int shares, hipStream_t s) {
+    const dim3 block(WAVES * 64), grid(shares), join(shares - 1, 4 * NT);
+    if (!bf16) hipLaunchKernelGGL((attention_kernel<NB, NT, false, 2, 2>), grid, block, 0, s, a);
+    else if (a.cache.rht) hipLaunchKernelGGL((attention_kernel<NB, NT, true, 2, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_kernel<NB, NT, true, 1, 1>), grid, block, 0, s, a);
+    if (shares == 1) return;
+    if (bf16) hipLaunchKernelGGL((attention_join_kernel<NB, NT, true>), join, block, 0, s, a, shares);
+    else hipLaunchKernelGGL((attention_join_kernel<NB, NT, false>), join, block, 0, s, a, shares);
 }
 
 mx_status check_pitches(int64_t ld, int64_t head_ld, int dim) {
@@ -171,7 +837,11 @@ mx_status check_pitches(int64_t ld, int64_t head_ld, int dim) {
 extern "C" {
 
 int64_t mx_cache_attention_workspace(const mx_cache* cache, int64_t tokens, int32_t q_heads, int32_t max_queries) {
-    return 0;
+    CacheView c;
+    if (view_cache(cache, c) != MX_OK || q_heads < 1 || q_heads % c.heads || max_queries < 0) return 0;
+    if (tokens < 1 || tokens > INT32_MAX / q_heads) return 0;
+    const Shape s = shape_of(c, tokens, q_heads, max_queries);
+    return 2 * s.shares * s.part_floats * (int64_t)sizeof(float);
 }
 
 mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, int64_t tokens, int32_t q_heads,
@@ -223,10 +893,33 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.out_head_ld = out_head_ld ? out_head_ld : c.dim;
     a.lse = lse;
     hipStream_t s = (hipStream_t)stream;
-    const dim3 grid((uint32_t)tokens, (uint32_t)q_heads);
+    const Shape shape = shape_of(c, tokens, q_heads, max_queries);
+    a.group = q_heads / c.heads;
+    a.tile_tokens = shape.tile_tokens;
+    a.tile_log2 = __builtin_ctz(shape.tile_tokens);
+    a.tile_heads = shape.tile_heads;
+    a.head_tiles = shape.head_tiles;
+    a.line_heads = c.heads * shape.head_tiles;
+    a.parts = (float*)workspace;
+    if (c.pages == 0) a.capacity = 0;
+    // no more workgroups than there can be work for
+    const int64_t tiles = (tokens / shape.tile_tokens + min(tokens, (int64_t)seqs)) * a.line_heads;
+    const int64_t units = tiles * max(ceil_div(a.capacity, UNIT), (int64_t)1);
+    const int shares = (int)min(shape.shares, ceil_div(units, MIN_UNITS));
+    const bool bf16 = qt == MX_BF16;
     (void)hipGetLastError();
-    if (qt == MX_BF16) hipLaunchKernelGGL(attention_kernel<true>, grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL(attention_kernel<false>, grid, dim3(64), 0, s, a);
+    if (shape.nb == 2) {
+        if (shape.nt == 1) launch<2, 1>(a, bf16, shares, s);
+        else if (shape.nt == 2) launch<2, 2>(a, bf16, shares, s);
+        else launch<2, 4>(a, bf16, shares, s);
+    } else if (shape.nb == 4) {
+        if (shape.nt == 1) launch<4, 1>(a, bf16, shares, s);
+        else if (shape.nt == 2) launch<4, 2>(a, bf16, shares, s);
+        else launch<4, 4>(a, bf16, shares, s);
+    } else {
+        if (shape.nt == 1) launch<8, 1>(a, bf16, shares, s);
+        else launch<8, 2>(a, bf16, shares, s);
+    }
     return launch_status();
 }
 
