@@ -12,6 +12,8 @@ namespace {
 
 using namespace mx;
 
+struct Cut;
+
 struct AttentionArgs {
     CacheView cache;
     const void* q;
@@ -31,6 +33,7 @@ struct AttentionArgs {
     float* lse;
     int group, tile_tokens, tile_log2, tile_heads, head_tiles, line_heads;
     float* parts;
+    Cut* cuts;                    // one a share
 };
 
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
@@ -56,6 +59,13 @@ typedef unsigned int u32x4v __attribute__((ext_vector_type(4), aligned(2)));
 // one that is cut every share leaves its part (sums, maxima) in the workspace,
 // two parts a workgroup at most, and a second launch joins them.
 // ---------------------------------------------------------------------------
+// A value that every lane has, for the scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
+}
+
 struct Seq {
     int64_t row0;             // its first query row
     int n, len;               // queries, keys
@@ -131,6 +141,15 @@ struct Segment {
     int64_t start;            // its first unit's place in the line
 };
 
+// What a share leaves about the segment that it began and did not finish:
+// count parts, the first one `slot`, then the even slots of the shares after.
+struct Cut {
+    Segment seg;
+    int count, pad;           // 0: there is none
+    int64_t slot;
+};
+static_assert(sizeof(Cut) % 16 == 0, "the parts follow the cuts, 16-byte aligned");
+
 __device__ __forceinline__ void measure_line(const AttentionArgs& a, Line& line) {
     const int tid = threadIdx.x, per = (a.seqs + WAVES * 64 - 1) / (WAVES * 64);
     int64_t mine = 0;
@@ -151,6 +170,14 @@ __device__ __forceinline__ void measure_line(const AttentionArgs& a, Line& line)
     __syncthreads();
 }
 
+__device__ __forceinline__ Seq load_uniform_seq(const AttentionArgs& a, int s) {
+    Seq q = load_seq(a, s);
+    q.row0 = uniform(q.row0);
+    q.n = uniform(q.n);
+    q.len = uniform(q.len);
+    return q;
+}
+
 __device__ __forceinline__ void set_tile(const AttentionArgs& a, Segment& g) {
     g.begin = first_unit(a, g.seq, g.tile);
     g.end = end_unit(a, g.seq, g.tile);
@@ -162,14 +189,14 @@ __device__ __forceinline__ Segment locate(const AttentionArgs& a, const Line& li
     int lo = 0, hi = WAVES * 64 - 1;                       // the last stretch that starts at or before it
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (line.before[mid] <= at) lo = mid;
+        if (uniform(line.before[mid]) <= at) lo = mid;
         else hi = mid - 1;
     }
     const int per = (a.seqs + WAVES * 64 - 1) / (WAVES * 64);
-    int64_t from = line.before[lo], units;
+    int64_t from = uniform(line.before[lo]), units;
     g.s = lo * per;
     for (;; ++g.s) {
-        g.seq = load_seq(a, g.s);
+        g.seq = load_uniform_seq(a, g.s);
         units = units_of(a, g.seq);
         if (at < from + units * a.line_heads) break;
         from += units * a.line_heads;
@@ -195,7 +222,7 @@ __device__ __forceinline__ void next_segment(const AttentionArgs& a, Segment& g)
         g.tile = 0;
         if (++g.head == a.line_heads) {
             g.head = 0;
-            do g.seq = load_seq(a, ++g.s);
+            do g.seq = load_uniform_seq(a, ++g.s);
             while (g.seq.n == 0);
         }
     }
@@ -287,12 +314,33 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return bits(v);
 }
 
+// The other value of a row of 16 lanes' neighbour (16 lanes on, then 32): of
+// the two results one is the lane's own, the other its partner's.
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+template <class Op>
+__device__ __forceinline__ float across(float v, Op op) {
+    u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r.x), __uint_as_float(r.y));
+    r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+struct MaxF { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+struct AddF { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
+
 // Eight codes and their scale as bf16, exactly (E2M1 times a power of two).
 __device__ __forceinline__ void widen8(uint32_t w, float scale, uint32_t* u) {
     u[0] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
     u[1] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
     u[2] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
     u[3] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+}
+__device__ __forceinline__ uint32_t widen2(uint32_t w, float scale, int byte) {
+    switch (byte) {           // (a constant)
+    case 0: return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+    case 1: return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+    case 2: return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+    default: return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+    }
 }
 __device__ __forceinline__ float scale_of(uint32_t word, int byte) {       // byte: 0..3
     return scale_operand((word >> (8 * byte)) & 0xFFu);
@@ -325,20 +373,22 @@ struct Shared {
     Line line;
 };
 
-template <int NB, int NT, bool BF16, int QT, int PT>
-__global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attention_kernel(AttentionArgs a) {
+template <int NB, int NT, bool EXACT, bool BF16, int QT, int PT>
+__global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attention_kernel(AttentionArgs a) {
     using Sh = Shared<NB, NT, QT>;
     constexpr int M = 2 * NB;                              // elements of V that a lane has, products of the sum
     constexpr int VW = NB == 8 ? 2 : 1;                    // dwords they take
     __shared__ Sh sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 15, g = lane >> 4;
-    const int shift = a.cache.page_log2, row_bytes = a.cache.dim >> 1, blocks = a.cache.dim >> 5;
+    const int col = lane & 15, g = lane >> 4, q_at = col * Sh::PITCH + 8 * NB * g;
+    const int shift = a.cache.page_log2;
+    const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1, blocks = EXACT ? NB : a.cache.dim >> 5;
 
     measure_line(a, sh.line);
-    const int64_t total = sh.line.before[WAVES * 64];
+    const int64_t total = uniform(sh.line.before[WAVES * 64]);
     const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MIN_UNITS);
     const int64_t begin = blockIdx.x * per, stop = min(begin + per, total);
+    if (tid == 0) a.cuts[blockIdx.x].count = 0;
     if (begin >= total) return;
     Segment seg = locate(a, sh.line, begin);
 
@@ -429,25 +479,21 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
         uint2 ks[2][NB == 8 ? 2 : 1]; // eight keys' scales of the lane's blocks
         uint32_t vc[2][8][VW];        // codes of V: [j][key]
         uint2 vs[2];
-        int page_k[2], page_v[2];     // of the unit after
         const int kg = 8 * (col >> 2);                     // the lane's group of keys in a score product
-        const bool v_there = col * NB < row_bytes;
+        const bool v_there = EXACT || col * NB < row_bytes;
 
-        auto look_up = [&](int unit) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                page_k[j] = table[min(UNIT * unit + 32 * j + kg, last_group) >> shift];
-                page_v[j] = table[min(UNIT * unit + 32 * j + 8 * g, last_group) >> shift];
-            }
-        };
-        auto good = [&](int page) { return page >= 0 && page < (int)a.cache.pages; };
+        // A lane looks up the page of one of a unit's eight groups of keys, -1 if it does not exist; others get it
+        // from there.
+        auto look_up = [&](int unit) { return table[min(UNIT * unit + 8 * (lane & 7), last_group) >> shift]; };
+        auto checked = [&](int page) { return page >= 0 && page < (int)a.cache.pages ? page : -1; };
+        auto page_of = [&](int pages, int group) { return __builtin_amdgcn_ds_bpermute(4 * group, pages); };
         auto load_k = [&](int unit, int j, int page) {
             const int o = (min(UNIT * unit + 32 * j + kg, last_group)) & ((1 << shift) - 1);
-            const int64_t p = (int64_t)(good(page) ? page : 0) * a.cache.heads + head;
+            const int64_t p = (int64_t)max(page, 0) * a.cache.heads + head;
             const uint8_t* codes = a.cache.codes[0] + ((p << shift) + o + (col & 3)) * row_bytes;
             const uint8_t* scales = a.cache.scales[0] + (p * blocks << shift) + o;
             if constexpr (NB == 2) {
-                const bool there = 8 * g < row_bytes;
+                const bool there = EXACT || 8 * g < row_bytes;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const uint2 w = *(const uint2*)(codes + (4 * t) * row_bytes + (there ? 8 * g : 0));
@@ -460,7 +506,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
 #pragma unroll
                 for (int h = 0; h < NB / 4; ++h) {
                     const int block = g * (NB / 4) + h;
-                    const bool there = block < blocks;
+                    const bool there = EXACT || block < blocks;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const uint4 w = *(const uint4*)(codes + (4 * t) * row_bytes + (there ? 16 * block : 0));
@@ -476,7 +522,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
         };
         auto load_v = [&](int unit, int j, int page) {
             const int o = (min(UNIT * unit + 32 * j + 8 * g, last_group)) & ((1 << shift) - 1);
-            const int64_t p = (int64_t)(good(page) ? page : 0) * a.cache.heads + head;
+            const int64_t p = (int64_t)max(page, 0) * a.cache.heads + head;
             const int c = v_there ? col : 0;
             const uint8_t* codes = a.cache.codes[1] + ((p << shift) + o) * row_bytes + c * NB;
 #pragma unroll
@@ -493,60 +539,50 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
             vs[j] = *(const uint2*)(a.cache.scales[1] + ((p * blocks + c * NB / 16) << shift) + o);
         };
 
-        bool bad[2] = {false, false};                      // the lane's groups of keys in this unit do not exist
-        bf16x8 qf[QT][NB];
-        if constexpr (NT == 1) {
-#pragma unroll
-            for (int x = 0; x < QT; ++x)
-#pragma unroll
-                for (int s = 0; s < NB; ++s)
-                    qf[x][s] = *(const bf16x8*)((const __bf16*)sh.data + (x * 16 + col) * Sh::PITCH + 8 * NB * g + 8 * s);
-        }
-        int unit = unit0 + wave;
+        int unit = unit0 + wave, pages = 0, next_pages = 0;
         if (unit < units) {
-            look_up(unit);
+            pages = checked(look_up(unit));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                load_k(unit, j, page_k[j]);
-                load_v(unit, j, page_v[j]);
-                bad[j] = !good(page_v[j]);
+                load_k(unit, j, page_of(pages, 4 * j + (col >> 2)));
+                load_v(unit, j, page_of(pages, 4 * j + g));
             }
-            look_up(min(unit + WAVES, units - 1));
+            next_pages = look_up(min(unit + WAVES, units - 1));
         }
         for (; unit < units; unit += WAVES) {
             const int key0 = UNIT * unit, ahead = min(unit + WAVES, units - 1);
-            const bool whole = key0 + UNIT - 1 <= all_to && key0 >= all_from && !__any(bad[0] || bad[1]);
-            const int next_k[2] = {page_k[0], page_k[1]}, next_v[2] = {page_v[0], page_v[1]};
-            look_up(min(unit + 2 * WAVES, units - 1));
+            const bool whole = key0 + UNIT - 1 <= all_to && key0 >= all_from && !__any(pages < 0);
+            next_pages = checked(next_pages);
+            const int after = look_up(min(unit + 2 * WAVES, units - 1));
+            int q_from = q_at;        // (the queries are read again for every unit: registers do not hold them)
+            asm volatile("" : "+v"(q_from));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // scores
                 f32x4 s[NT][2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    uint32_t kf[NB][4];
+                for (int x = 0; x < NB; ++x) {
+                    uint32_t kf[2][4];
 #pragma unroll
-                    for (int x = 0; x < NB; ++x) {
+                    for (int t = 0; t < 2; ++t) {
                         const uint2 w = ks[j][NB == 8 ? x >> 2 : 0];
-                        widen8(kc[j][t][x], scale_of(t ? w.y : w.x, col & 3), kf[x]);
+                        widen8(kc[j][t][x], scale_of(t ? w.y : w.x, col & 3), kf[t]);
                     }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        s[n][t] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int y = 0; y < QT; ++y)
+                        for (int y = 0; y < QT; ++y) {
+                            const bf16x8 q = *(const bf16x8*)((const __bf16*)sh.data + q_from +
+                                                              (y * 16 * NT + 16 * n) * Sh::PITCH + 8 * x);
 #pragma unroll
-                            for (int x = 0; x < NB; ++x) {
-                                bf16x8 q;
-                                if constexpr (NT == 1) q = qf[y][x];
-                                else
-                                    q = *(const bf16x8*)((const __bf16*)sh.data +
-                                                         (y * 16 * NT + 16 * n + col) * Sh::PITCH + 8 * NB * g + 8 * x);
-                                s[n][t] = mfma(operand(kf[x][0], kf[x][1], kf[x][2], kf[x][3]), q, s[n][t]);
-                            }
-                    }
+                            for (int t = 0; t < 2; ++t)
+                                s[n][t] = mfma(operand(kf[t][0], kf[t][1], kf[t][2], kf[t][3]), q,
+                                               x == 0 && y == 0 ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : s[n][t]);
+                        }
                 }
-                load_k(ahead, j, next_k[j]);
+                const bool bad = !whole && page_of(pages, 4 * j + g) < 0;
+                __builtin_amdgcn_sched_barrier(0);
+                load_k(ahead, j, page_of(next_pages, 4 * j + (col >> 2)));
 
                 // softmax of these 32 keys
                 uint32_t p[NT][PT][4];
@@ -559,14 +595,13 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int key = key0 + 32 * j + 8 * g + i;
-                            x[i] = key <= last[n] && key >= low[n] && !bad[j] ? x[i] : -__builtin_inff();
+                            x[i] = key <= last[n] && key >= low[n] && !bad ? x[i] : -__builtin_inff();
                         }
                     }
                     float m = x[0];
 #pragma unroll
                     for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
-                    m = fmaxf(m, __shfl_xor(m, 16));
-                    m = fmaxf(m, __shfl_xor(m, 32));
+                    m = across(m, MaxF());
                     m = fmaxf(m, top[n]);
                     const float safe = m == -__builtin_inff() ? 0.0f : m;
                     if (__any(m > top[n])) {
@@ -589,6 +624,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
                     }
                 }
 
+                __builtin_amdgcn_sched_barrier(0);
                 // sums
                 uint2 scales = vs[j];
                 if (!whole) {
@@ -614,7 +650,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int key = key0 + 32 * j + 8 * g + i;
-                                if (key <= last[n] && key >= low[n] && !bad[j]) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
+                                if (key <= last[n] && key >= low[n] && !bad) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
                             }
                             const f32x4 hit = mfma(operand(mark[0], mark[1], mark[2], mark[3]),
                                                    operand(seen[0], seen[1], seen[2], seen[3]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
@@ -627,41 +663,38 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
                         }
                     }
                 }
-                uint32_t u[8][NB];
+                float sc[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float sc = scale_of(i < 4 ? scales.x : scales.y, i & 3);
-                    if constexpr (NB == 2) {
-                        u[i][0] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vc[j][i][0], sc, 0));
-                        u[i][1] = bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(vc[j][i][0], sc, 1));
-                    } else {
+                for (int i = 0; i < 8; ++i) sc[i] = scale_of(i < 4 ? scales.x : scales.y, i & 3);
 #pragma unroll
-                        for (int h = 0; h < VW; ++h) widen8(vc[j][i][h], sc, &u[i][4 * h]);
+                for (int k = 0; k < M; k += 2) {
+                    uint32_t u[8];                         // elements k and k + 1 of the eight keys
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = widen2(vc[j][i][k >> 3], sc[i], (k >> 1) & 3);
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd) {
+                        const uint32_t sel = odd ? 0x07060302u : 0x05040100u;
+                        const bf16x8 v = operand(__builtin_amdgcn_perm(u[1], u[0], sel), __builtin_amdgcn_perm(u[3], u[2], sel),
+                                                 __builtin_amdgcn_perm(u[5], u[4], sel), __builtin_amdgcn_perm(u[7], u[6], sel));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int y = 0; y < PT; ++y)
+                                acc[n][k + odd] = mfma(v, operand(p[n][y][0], p[n][y][1], p[n][y][2], p[n][y][3]),
+                                                       acc[n][k + odd]);
                     }
                 }
-                load_v(ahead, j, next_v[j]);
-#pragma unroll
-                for (int k = 0; k < M; ++k) {
-                    const uint32_t sel = k & 1 ? 0x07060302u : 0x05040100u;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(u[2 * i + 1][k >> 1], u[2 * i][k >> 1], sel);
-                    const bf16x8 v = operand(w[0], w[1], w[2], w[3]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int y = 0; y < PT; ++y)
-                            acc[n][k] = mfma(v, operand(p[n][y][0], p[n][y][1], p[n][y][2], p[n][y][3]), acc[n][k]);
-                }
-                bad[j] = !good(next_v[j]);
+                __builtin_amdgcn_sched_barrier(0);
+                load_v(ahead, j, page_of(next_pages, 4 * j + g));
             }
+            pages = next_pages;
+            next_pages = after;
         }
 
         // the waves' maxima and sums, then their rows
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            sum[n] += __shfl_xor(sum[n], 16);
-            sum[n] += __shfl_xor(sum[n], 32);
+            sum[n] = across(sum[n], AddF());
             if (g == 0) {
                 sh.top[wave][16 * n + col] = top[n];
                 sh.sum[wave][16 * n + col] = sum[n];
@@ -723,48 +756,66 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 4 : 2) void attenti
                 __syncthreads();
             }
         }
-        at = seg.start + (seg.end - seg.begin);
+        const int64_t next = seg.start + (seg.end - seg.begin);
+        if (next > stop && seg.start >= begin && tid == 0) {
+            Cut& cut = a.cuts[blockIdx.x];
+            cut.seg = seg;
+            cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
+            cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
+        }
+        at = next;
         if (at >= stop) return;
         next_segment(a, seg);
     }
 }
 
 // Joins the parts of the segments that were cut.  Workgroup x: the segment
-// that the x + 1st cut goes through, if that is the first cut in it; y: four
-// of its rows.  The parts are shared by `groups` sets of threads.
+// that share x began and did not finish, if there is one; y: two of its rows.
+// Sets of threads (groups) share the parts, AHEAD of them under way at once.
 template <int NB, int NT, bool BF16>
-__global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArgs a, int shares) {
-    constexpr int PIECES = 4 * NB, ITEMS = 4 * PIECES, GROUPS = WAVES * 64 / ITEMS;
-    __shared__ Line line;
-    __shared__ float o[GROUPS][ITEMS][8 + 1], sums[GROUPS][4], tops[GROUPS][4];
-    measure_line(a, line);
-    const int64_t total = line.before[WAVES * 64];
-    const int64_t per = max((total + shares - 1) / shares, (int64_t)MIN_UNITS);
-    const int64_t cut = (blockIdx.x + 1) * per;
-    if (cut >= total) return;
-    const Segment seg = locate(a, line, cut);
-    if (seg.start == cut || seg.start < cut - per) return;
+__global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArgs a) {
+    constexpr int PIECES = 4 * NB, ITEMS = 2 * PIECES, GROUPS = WAVES * 64 / ITEMS, AHEAD = 4;
+    __shared__ float o[GROUPS][ITEMS][8 + 1], sums[GROUPS][2], tops[GROUPS][2];
+    const Cut cut = a.cuts[blockIdx.x];
+    if (cut.count == 0) return;
+    const Segment& seg = cut.seg;
     const int rows = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2)) * a.tile_heads;
-    if (4 * (int)blockIdx.y >= rows) return;
-    const int64_t end = seg.start + seg.end - seg.begin;
-    const int first = blockIdx.x, count = (int)((end - 1) / per) - first + 1;
-    const int64_t slot0 = 2 * (int64_t)first + (seg.start == first * per ? 0 : 1);
+    if (2 * (int)blockIdx.y >= rows) return;
     const int item = threadIdx.x % ITEMS, group = threadIdx.x / ITEMS;
-    const int c = 4 * blockIdx.y + item / PIECES, d = item % PIECES * 8;
+    const int c = 2 * blockIdx.y + item / PIECES, d = item % PIECES * 8;
     float top = -__builtin_inff(), sum = 0.0f, v[8] = {};
-    for (int i = group; i < count; i += GROUPS) {
-        const Part<NB, NT> part(a, i == 0 ? slot0 : 2 * (int64_t)(first + i));
-        const bool there = c < rows;
-        const float t = there ? part.top(c) : -__builtin_inff(), l = there ? part.sum(c) : 0.0f;
-        const f32x4 x = there ? *(const f32x4*)(part.row(c) + d) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        const f32x4 y = there ? *(const f32x4*)(part.row(c) + d + 4) : (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        const float m = fmaxf(top, t), safe = m == -__builtin_inff() ? 0.0f : m;
-        const float f = __builtin_amdgcn_exp2f(top - safe), e = __builtin_amdgcn_exp2f(t - safe);
-        sum = sum * f + l * e;
+    for (int i0 = group; i0 < cut.count; i0 += AHEAD * GROUPS) {
+        float t[AHEAD], l[AHEAD];
+        f32x4 x[AHEAD], y[AHEAD];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = v[k] * f + x[k] * e;
-            v[4 + k] = v[4 + k] * f + y[k] * e;
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = min(i0 + k * GROUPS, cut.count - 1);
+            const Part<NB, NT> part(a, i == 0 ? cut.slot : 2 * (int64_t)(blockIdx.x + i));
+            t[k] = part.top(c);                            // (rows that do not exist hold anything and go nowhere)
+            l[k] = part.sum(c);
+            x[k] = *(const f32x4*)(part.row(c) + d);
+            y[k] = *(const f32x4*)(part.row(c) + d + 4);
+        }
+        float m = top;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (i0 + k * GROUPS >= cut.count) t[k] = -__builtin_inff();
+            m = fmaxf(m, t[k]);
+        }
+        const float safe = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(top - safe);
+        sum *= f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= f;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (i0 + k * GROUPS >= cut.count) continue;
+            const float e = __builtin_amdgcn_exp2f(t[k] - safe);
+            sum += l[k] * e;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                v[z] += x[k][z] * e;
+                v[4 + z] += y[k][z] * e;
+            }
         }
         top = m;
     }
@@ -776,16 +827,18 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
     }
     __syncthreads();
     if (group != 0) return;
-    const int rr = item / PIECES;
-    float most = tops[0][rr];
-    for (int w = 1; w < GROUPS; ++w) most = fmaxf(most, tops[w][rr]);
+    const int r2 = item / PIECES;
+    float most = tops[0][r2];
+#pragma unroll
+    for (int w = 1; w < GROUPS; ++w) most = fmaxf(most, tops[w][r2]);
     const float safe = most == -__builtin_inff() ? 0.0f : most;
     float all = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+#pragma unroll
     for (int w = 0; w < GROUPS; ++w) {
-        const float e = __builtin_amdgcn_exp2f(tops[w][rr] - safe);
-        all += sums[w][rr] * e;
+        const float e = __builtin_amdgcn_exp2f(tops[w][r2] - safe);
+        all += sums[w][r2] * e;
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += o[w][item][k] * e;
     }
@@ -812,20 +865,27 @@ Shape shape_of(const CacheView& c, int64_t tokens, int q_heads, int max_queries)
     s.head_tiles = (group + r - 1) / r;
     s.tile_tokens = 1;
     while (2 * s.tile_tokens * s.tile_heads <= r) s.tile_tokens *= 2;
-    s.shares = s.nt == 1 && s.nb < 8 ? 1024 : 512;
+    s.shares = s.nt == 1 && s.nb < 8 ? 768 : 512;
     s.part_floats = (int64_t)r * (32 * s.nb + 2);
     return s;
 }
 
+template <int NB, int NT, bool EXACT>
+void launch_main(const AttentionArgs& a, bool bf16, dim3 grid, hipStream_t s) {
+    const dim3 block(WAVES * 64);
+    if (!bf16) hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, false, 2, 2>), grid, block, 0, s, a);
+    else if (a.cache.rht) hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, true, 2, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, true, 1, 1>), grid, block, 0, s, a);
+}
+
 template <int NB, int NT>
 void launch(const AttentionArgs& a, bool bf16, int shares, hipStream_t s) {
-    const dim3 block(WAVES * 64), grid(shares), join(shares - 1, 4 * NT);
-    if (!bf16) hipLaunchKernelGGL((attention_kernel<NB, NT, false, 2, 2>), grid, block, 0, s, a);
-    else if (a.cache.rht) hipLaunchKernelGGL((attention_kernel<NB, NT, true, 2, 1>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((attention_kernel<NB, NT, true, 1, 1>), grid, block, 0, s, a);
+    const dim3 block(WAVES * 64), grid(shares), join(shares, 8 * NT);
+    if (a.cache.dim == 32 * NB) launch_main<NB, NT, true>(a, bf16, grid, s);
+    else launch_main<NB, NT, false>(a, bf16, grid, s);
     if (shares == 1) return;
-    if (bf16) hipLaunchKernelGGL((attention_join_kernel<NB, NT, true>), join, block, 0, s, a, shares);
-    else hipLaunchKernelGGL((attention_join_kernel<NB, NT, false>), join, block, 0, s, a, shares);
+    if (bf16) hipLaunchKernelGGL((attention_join_kernel<NB, NT, true>), join, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_join_kernel<NB, NT, false>), join, block, 0, s, a);
 }
 
 mx_status check_pitches(int64_t ld, int64_t head_ld, int dim) {
@@ -841,7 +901,7 @@ int64_t mx_cache_attention_workspace(const mx_cache* cache, int64_t tokens, int3
     if (view_cache(cache, c) != MX_OK || q_heads < 1 || q_heads % c.heads || max_queries < 0) return 0;
     if (tokens < 1 || tokens > INT32_MAX / q_heads) return 0;
     const Shape s = shape_of(c, tokens, q_heads, max_queries);
-    return 2 * s.shares * s.part_floats * (int64_t)sizeof(float);
+    return s.shares * (2 * s.part_floats * (int64_t)sizeof(float) + (int64_t)sizeof(Cut));
 }
 
 mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, int64_t tokens, int32_t q_heads,
@@ -900,7 +960,8 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.tile_heads = shape.tile_heads;
     a.head_tiles = shape.head_tiles;
     a.line_heads = c.heads * shape.head_tiles;
-    a.parts = (float*)workspace;
+    a.cuts = (Cut*)workspace;
+    a.parts = (float*)(a.cuts + shape.shares);
     if (c.pages == 0) a.capacity = 0;
     // no more workgroups than there can be work for
     const int64_t tiles = (tokens / shape.tile_tokens + min(tokens, (int64_t)seqs)) * a.line_heads;

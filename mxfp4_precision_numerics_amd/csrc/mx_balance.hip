@@ -53,7 +53,7 @@ __device__ __forceinline__ void row_scores(float* v, bool softmax, float* rest) 
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float e = soft_exp(-fabsf(v[i])), r = 1.0f / (1.0f + e);     // (NaN stays NaN)
+            const float e = soft_exp(-fabsf(v[i])), r = __builtin_amdgcn_rcpf(1.0f + e);     // (NaN stays NaN)
             const bool up = v[i] >= 0.0f;
             if constexpr (SLOPES) rest[i] = up ? e * r : r;
             v[i] = up ? r : e * r;
@@ -118,27 +118,49 @@ __global__ __launch_bounds__(THREADS) void balance_kernel(BalanceArgs a) {
         a.counts[(int64_t)blockIdx.x * (a.experts + 1) + e] = count[e];
 }
 
-// The workgroups' sums and counts, then the slopes and the loss.
+// The workgroups' sums and counts, then the slopes and the loss.  Threads side
+// by side take neighbouring experts, 2^lanes_log2 of them, and the others
+// further workgroups' rows, eight at a time.
 __global__ __launch_bounds__(THREADS) void balance_loss_kernel(const float* sums, const int32_t* counts, int blocks,
-                                                               int experts, int32_t* out_counts, float* slope,
-                                                               float* loss) {
-    __shared__ double total[THREADS / 64];
-    __shared__ long long made[THREADS / 64];
-    __shared__ long long used_by;
-    const int e = threadIdx.x;
+                                                               int experts, int lanes_log2, int32_t* out_counts,
+                                                               float* slope, float* loss) {
+    __shared__ double part[THREADS], total[THREADS / 64];
+    __shared__ long long made_part[THREADS], made[THREADS / 64];
+    constexpr int AHEAD = 8;
+    const int e = threadIdx.x & ((1 << lanes_log2) - 1), first = threadIdx.x >> lanes_log2, step = THREADS >> lanes_log2;
     double s = 0.0;
-    long long c = 0;
-    if (e < experts) {
-        for (int b = 0; b < blocks; ++b) s += (double)sums[(int64_t)b * experts + e];
-        for (int b = 0; b < blocks; ++b) c += counts[(int64_t)b * (experts + 1) + e];
-        out_counts[e] = (int32_t)c;
+    int c = 0;
+    for (int b0 = first; b0 < blocks; b0 += AHEAD * step) {
+        float x[AHEAD];
+        int y[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int b = min(b0 + i * step, blocks - 1), at = min(e, experts - 1);
+            x[i] = sums[(int64_t)b * experts + at];
+            y[i] = counts[(int64_t)b * (experts + 1) + at];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool in = b0 + i * step < blocks && e < experts;
+            s += in ? (double)x[i] : 0.0;
+            c += in ? y[i] : 0;
+        }
     }
-    if (e == 0) {
-        long long u = 0;
-        for (int b = 0; b < blocks; ++b) u += counts[(int64_t)b * (experts + 1) + experts];
-        used_by = u;
+    int used = 0;
+    for (int b = threadIdx.x; b < blocks; b += THREADS) used += counts[(int64_t)b * (experts + 1) + experts];
+    part[threadIdx.x] = s;
+    made_part[threadIdx.x] = (long long)c << 32 | (uint32_t)used;      // (their sums stay below 2^31 each)
+    __syncthreads();
+    s = 0.0;
+    long long n = made_part[threadIdx.x];
+    c = 0;
+    if (threadIdx.x < 1 << lanes_log2) {
+        for (int i = threadIdx.x; i < THREADS; i += 1 << lanes_log2) {
+            s += part[i];
+            c += (int)(made_part[i] >> 32);
+        }
+        if (e < experts) out_counts[e] = c;
     }
-    long long n = c;
 #pragma unroll
     for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
     if ((threadIdx.x & 63) == 0) made[threadIdx.x >> 6] = n;
@@ -146,10 +168,11 @@ __global__ __launch_bounds__(THREADS) void balance_loss_kernel(const float* sums
     n = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w) n += made[w];
-    const double all = (double)n * (double)used_by;
-    const double k = e < experts && all > 0.0 ? (double)experts * (double)c / all : 0.0;
-    if (e < experts) slope[e] = (float)k;
-    double l = e < experts && all > 0.0 ? k * s : 0.0;
+    const double all = (double)(n >> 32) * (double)(uint32_t)n;
+    const bool mine = threadIdx.x < 1 << lanes_log2 && e < experts;
+    const double k = mine && all > 0.0 ? (double)experts * (double)c / all : 0.0;
+    if (mine) slope[e] = (float)k;
+    double l = mine && all > 0.0 ? k * s : 0.0;
 #pragma unroll
     for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
     if ((threadIdx.x & 63) == 0) total[threadIdx.x >> 6] = l;
@@ -233,10 +256,17 @@ template <bool B, int L, int C>
 void launch(const BalanceBwdArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((balance_bwd_kernel<B, L, C>), dim3((uint32_t)ceil_div(a.tokens, 256 / L)), dim3(256), 0, s, a);
 }
+// The lanes that share a row and the chunks of four experts each holds.  With
+// many tokens half as many lanes take a row, as in the router.
+constexpr int64_t MANY_TOKENS = 8192;
 template <bool B, class A>
 void dispatch(const A& a, hipStream_t s) {
     const int e = a.experts;
+    const bool many = a.tokens >= MANY_TOKENS;
     if (e <= 32) launch<B, 8, 1>(a, s);
+    else if (e <= 64 && many) launch<B, 8, 2>(a, s);
+    else if (e <= 128 && many) launch<B, 8, 4>(a, s);
+    else if (e <= 256 && many) launch<B, 8, 8>(a, s);
     else if (e <= 64) launch<B, 16, 1>(a, s);
     else if (e <= 128) launch<B, 16, 2>(a, s);
     else if (e <= 256) launch<B, 16, 4>(a, s);
@@ -282,8 +312,10 @@ mx_status mx_balance(const void* logits, mx_dtype lt, int64_t tokens, int32_t ex
         if (lt == MX_BF16) dispatch<true>(a, s);
         else dispatch<false>(a, s);
     }
-    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(THREADS), 0, s, a.sums, a.counts, blocks, experts, counts, slope,
-                       loss);
+    int lanes_log2 = 0;
+    while (1 << lanes_log2 < experts) ++lanes_log2;
+    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(THREADS), 0, s, a.sums, a.counts, blocks, experts, lanes_log2,
+                       counts, slope, loss);
     return launch_status();
 }
 
