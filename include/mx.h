@@ -651,7 +651,8 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
  * tokens > 0.
  * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
  * MX_ERR_LAUNCH.  tokens == 0 launches nothing. */
-int64_t mx_cache_attention_workspace(const mx_cache* cache, int64_t tokens, int32_t q_heads, int32_t max_queries);
+int64_t mx_cache_attention_workspace(const mx_cache* cache, mx_dtype qt, int64_t tokens, int32_t q_heads,
+                                     int32_t max_queries);
 mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, int64_t tokens, int32_t q_heads,
                              int64_t q_ld, int64_t q_head_ld, const int32_t* q_offsets, int32_t max_queries,
                              int32_t seqs, const int32_t* page_table, int64_t table_ld, int32_t table_pages,

@@ -97,10 +97,11 @@ __device__ __forceinline__ int tiles_of(const AttentionArgs& a, const Seq& q) {
     return (q.n + a.tile_tokens - 1) >> a.tile_log2;
 }
 
-// Units of a sequence's first x tiles, all of them full ones.  With t =
-// tile_tokens and Q = 64 / t, tile i's end is at ceil((b + i + 1) / Q) for a b
-// made of the sequence's lengths, its begin at floor((c + i) / Q): sums of
-// ceil(j / Q) and floor(j / Q) over a stretch of j.
+// Units of a sequence's first x tiles, all of them full ones: sums over the
+// tiles of their ends less their begins.  With t tokens a tile, t <= 64 and Q =
+// 64 / t, tile i ends at ceil((b + i + 1) / Q) and begins at floor((c + i) / Q)
+// for b and c made of the sequence's lengths; with t = 64 C at A + (i + 1) C and
+// B + i C.  Ends are 1 at least, begins 0.
 __device__ __forceinline__ int64_t sum_ceil(int64_t y, int q_log2) {       // over j = 1 .. y
     const int64_t w = y >> q_log2, r = y - (w << q_log2);
     return ((w * (w + 1) >> 1) << q_log2) + r * (w + 1);
@@ -111,14 +112,27 @@ __device__ __forceinline__ int64_t sum_floor(int64_t y, int q_log2) {      // ov
 }
 __device__ __forceinline__ int64_t units_before(const AttentionArgs& a, const Seq& q, int x) {
     if (!a.causal) return (int64_t)x * end_unit(a, q, 0);
-    const int q_log2 = 6 - a.tile_log2;
-    const int64_t at = q.len - q.n;
-    const int64_t b = (at + a.tile_tokens - 1) >> a.tile_log2;
-    int64_t units = min((int64_t)x, max(-b, (int64_t)0));                  // tiles before the first key: one each
-    units += sum_ceil(max(b + x, (int64_t)0), q_log2) - sum_ceil(max(b, (int64_t)0), q_log2);
-    if (a.window) {
-        const int64_t c = (at - a.window + 1) >> a.tile_log2;
-        units -= sum_floor(max(c + x, (int64_t)0), q_log2) - sum_floor(max(c, (int64_t)0), q_log2);
+    const int64_t at = q.len - q.n, low = at - a.window + 1;
+    int64_t units;
+    if (a.tile_log2 <= 6) {
+        const int q_log2 = 6 - a.tile_log2;
+        const int64_t b = (at + a.tile_tokens - 1) >> a.tile_log2;
+        units = min((int64_t)x, max(-b, (int64_t)0));                      // tiles before the first key: one each
+        units += sum_ceil(max(b + x, (int64_t)0), q_log2) - sum_ceil(max(b, (int64_t)0), q_log2);
+        if (a.window) {
+            const int64_t c = low >> a.tile_log2;
+            units -= sum_floor(max(c + x, (int64_t)0), q_log2) - sum_floor(max(c, (int64_t)0), q_log2);
+        }
+    } else {
+        const int c_log2 = a.tile_log2 - 6;
+        const int64_t n = x, end0 = (at + UNIT - 1) >> 6;
+        const int64_t ones = min(n, max((1 - end0) >> c_log2, (int64_t)0));
+        units = ones + (n - ones) * end0 + (((n * (n + 1) - ones * (ones + 1)) >> 1) << c_log2);
+        if (a.window) {
+            const int64_t begin0 = low >> 6;
+            const int64_t none = min(n, max((-begin0 + (1 << c_log2) - 1) >> c_log2, (int64_t)0));
+            units -= (n - none) * begin0 + (((n * (n - 1) - none * (none - 1)) >> 1) << c_log2);
+        }
     }
     return units;
 }
@@ -314,6 +328,62 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return bits(v);
 }
 
+// The same for the 8 NB consecutive elements of a row that a lane has in
+// registers, from d on (a multiple of 8 NB).  Heads of up to 64 elements share a
+// block between lanes 16 apart.
+template <int NB, bool BF16>
+__device__ __forceinline__ void finish_row(const AttentionArgs& a, const Row& r, bool live, int d, float* o, float top,
+                                           float sum) {
+    constexpr int N = 8 * NB;
+    float f = 1.0f;
+    if (a.sinks) {
+        const float sink = live ? a.sinks[r.head] * LOG2E : 0.0f, m = fmaxf(top, sink);
+        const float safe = m == -__builtin_inff() ? 0.0f : m;
+        f = __builtin_amdgcn_exp2f(top - safe);
+        sum = sum * f + __builtin_amdgcn_exp2f(sink - safe);
+        top = m;
+    }
+    const float inv = f / sum;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = sum == 0.0f ? 0.0f : o[i] * inv;
+    if (a.cache.rht) {
+        constexpr int IN = N < 32 ? N : 32;
+#pragma unroll
+        for (int b = 0; b < N; b += IN) {
+            fwht_inlane<IN>(o + b);
+            if constexpr (IN < 32) {
+                const float s = threadIdx.x & 16 ? -1.0f : 1.0f;
+#pragma unroll
+                for (int i = 0; i < IN; ++i) o[b + i] = __builtin_fmaf(o[b + i], s, __shfl_xor(o[b + i], 16));
+            }
+            const float c = __uint_as_float(0x3E3504F3u);  // fp32(2^-2.5)
+            const uint32_t m = a.cache.mask >> ((d + b) & 31);
+#pragma unroll
+            for (int i = 0; i < IN; ++i) o[b + i] = __uint_as_float(__float_as_uint(o[b + i] * c) ^ (m >> i << 31));
+        }
+    }
+    if (!live) return;
+    const int64_t at = r.token * a.out_ld + r.head * a.out_head_ld + d;
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        if (d + i >= a.cache.dim) continue;
+        if constexpr (BF16) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = pack(o[i + 2 * k], o[i + 2 * k + 1]);
+            *(u32x4v*)((uint16_t*)a.out + at + i) = (u32x4v){u[0], u[1], u[2], u[3]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; k += 4)
+                *(u32x4v*)((float*)a.out + at + i + k) =
+                    (u32x4v){__float_as_uint(o[i + k]), __float_as_uint(o[i + k + 1]), __float_as_uint(o[i + k + 2]),
+                             __float_as_uint(o[i + k + 3])};
+        }
+    }
+    if (a.lse && d == 0)
+        a.lse[r.token * a.q_heads + r.head] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2;
+}
+
 // The other value of a row of 16 lanes' neighbour (16 lanes on, then 32): of
 // the two results one is the lane's own, the other its partner's.
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -373,6 +443,56 @@ struct Shared {
     Line line;
 };
 
+// A tile's queries into LDS, QT terms of bf16, transformed where the cache is;
+// 0 where there is none.  The whole workgroup calls.
+template <int NB, int ROWS, bool BF16, int QT>
+__device__ __forceinline__ void load_queries(const AttentionArgs& a, const Segment& seg, __bf16* to, int pitch) {
+    for (int i = threadIdx.x; i < ROWS * 4 * NB; i += WAVES * 64) {
+        const int c = i / (4 * NB), d = i % (4 * NB) * 8;
+        Row r;
+        const bool live = row_of(a, seg, c, r) && d < a.cache.dim;
+        const int64_t from = r.token * a.q_ld + r.head * a.q_head_ld + d;
+        float f[8] = {};
+        if (live) {
+            if constexpr (BF16) {
+                const u32x4v w = *(const u32x4v*)((const uint16_t*)a.q + from);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { f[2 * e] = bf16lo(u[e]); f[2 * e + 1] = bf16hi(u[e]); }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const u32x4v w = *(const u32x4v*)((const float*)a.q + from + 4 * e);
+                    f[4 * e] = __uint_as_float(w.x);
+                    f[4 * e + 1] = __uint_as_float(w.y);
+                    f[4 * e + 2] = __uint_as_float(w.z);
+                    f[4 * e + 3] = __uint_as_float(w.w);
+                }
+            }
+        }
+        if (a.cache.rht) {
+            const uint32_t m = a.cache.mask >> (d & 31);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(__float_as_uint(f[e]) ^ (m >> e << 31));
+            rht32_quad(f, (d >> 3) & 3);
+        }
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = pack(f[2 * e], f[2 * e + 1]);
+        *(uint4*)(to + c * pitch + d) = make_uint4(u[0], u[1], u[2], u[3]);
+        if constexpr (QT == 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // (an infinite element has no rest)
+                const float lo = bf16lo(u[e]), hi = bf16hi(u[e]);
+                w[e] = pack(__builtin_isinf(lo) ? 0.0f : f[2 * e] - lo, __builtin_isinf(hi) ? 0.0f : f[2 * e + 1] - hi);
+            }
+            *(uint4*)(to + (ROWS + c) * pitch + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
 template <int NB, int NT, bool EXACT, bool BF16, int QT, int PT>
 __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attention_kernel(AttentionArgs a) {
     using Sh = Shared<NB, NT, QT>;
@@ -393,55 +513,10 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
     Segment seg = locate(a, sh.line, begin);
 
     for (int64_t at = begin;;) {
-        // the rows' queries
         const int head = seg.head / a.head_tiles;          // of the cache
         const int rows = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2)) * a.tile_heads;
         __syncthreads();
-        for (int i = tid; i < 16 * NT * 4 * NB; i += WAVES * 64) {
-            const int c = i / (4 * NB), d = i % (4 * NB) * 8;
-            Row r;
-            const bool live = row_of(a, seg, c, r) && d < a.cache.dim;
-            const int64_t from = r.token * a.q_ld + r.head * a.q_head_ld + d;
-            float f[8] = {};
-            if (live) {
-                if constexpr (BF16) {
-                    const u32x4v w = *(const u32x4v*)((const uint16_t*)a.q + from);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) { f[2 * e] = bf16lo(u[e]); f[2 * e + 1] = bf16hi(u[e]); }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const u32x4v w = *(const u32x4v*)((const float*)a.q + from + 4 * e);
-                        f[4 * e] = __uint_as_float(w.x);
-                        f[4 * e + 1] = __uint_as_float(w.y);
-                        f[4 * e + 2] = __uint_as_float(w.z);
-                        f[4 * e + 3] = __uint_as_float(w.w);
-                    }
-                }
-            }
-            if (a.cache.rht) {
-                const uint32_t m = a.cache.mask >> (d & 31);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(__float_as_uint(f[e]) ^ (m >> e << 31));
-                rht32_quad(f, (d >> 3) & 3);
-            }
-            uint32_t u[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = pack(f[2 * e], f[2 * e + 1]);
-            __bf16* q = (__bf16*)sh.data + c * Sh::PITCH + d;
-            *(uint4*)q = make_uint4(u[0], u[1], u[2], u[3]);
-            if constexpr (QT == 2) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // (an infinite element has no rest)
-                    const float lo = bf16lo(u[e]), hi = bf16hi(u[e]);
-                    w[e] = pack(__builtin_isinf(lo) ? 0.0f : f[2 * e] - lo, __builtin_isinf(hi) ? 0.0f : f[2 * e + 1] - hi);
-                }
-                *(uint4*)(q + 16 * NT * Sh::PITCH) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
+        load_queries<NB, 16 * NT, BF16, QT>(a, seg, (__bf16*)sh.data, Sh::PITCH);
         __syncthreads();
 
         // the keys that each of the lane's rows sees, and those that all see
@@ -769,6 +844,347 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows of a sequence: prompts, drafts of many heads.
+//
+// A tile has 128 rows; a wave takes 32 of them and every key.  The workgroup
+// brings in 64 keys at a time, each wave a quarter: it widens K and V to bf16
+// operands, once for all waves, and puts them into LDS lane by lane as the
+// products read them (no bank conflicts).  Two buffers; the next unit's is
+// filled while this one's is read.  Products as in attention_kernel.
+//
+// (K's codes could enter a block-scaled product as they are, with q as a sum of
+// e4m3 terms.  Within 16 elements that product aligns its terms to the largest
+// and drops what is below 2^-13 of it, so the scores would not be sums in fp32.)
+// ---------------------------------------------------------------------------
+constexpr int ROWS_TILE = 128, ROWS_WAVE = 32;
+
+template <int NB, int QT>
+struct RowsShared {
+    static constexpr int M = 2 * NB;
+    static constexpr int PITCH = 32 * NB + 8;                  // of q, in bf16
+    static constexpr int K_BYTES = 4 * NB * 1024, V_BYTES = 2 * M * 1024;
+    union {
+        alignas(16) __bf16 q[QT][ROWS_TILE][PITCH];
+        struct {
+            alignas(16) unsigned char k[2][K_BYTES], v[2][V_BYTES];
+            alignas(16) unsigned char marks[2][2][1024];
+            int odd[2][2];
+        } work;
+    };
+    Line line;
+};
+
+template <int NB, bool EXACT, bool BF16, int QT, int PT>
+__global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_kernel(AttentionArgs a) {
+    using Sh = RowsShared<NB, QT>;
+    constexpr int M = Sh::M, NT = ROWS_WAVE / 16, KV = NB / 2;     // KV: bytes of V that a lane loads of a key
+    __shared__ Sh sh;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, g = lane >> 4;
+    const int shift = a.cache.page_log2;
+    const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1, blocks = EXACT ? NB : a.cache.dim >> 5;
+
+    measure_line(a, sh.line);
+    const int64_t total = uniform(sh.line.before[WAVES * 64]);
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MIN_UNITS);
+    const int64_t begin = blockIdx.x * per, stop = min(begin + per, total);
+    if (tid == 0) a.cuts[blockIdx.x].count = 0;
+    if (begin >= total) return;
+    Segment seg = locate(a, sh.line, begin);
+
+    for (int64_t at = begin;;) {
+        const int head = seg.head / a.head_tiles;
+        const int tokens = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2));
+        const int rows = tokens * a.tile_heads;
+        __syncthreads();
+        load_queries<NB, ROWS_TILE, BF16, QT>(a, seg, &sh.q[0][0][0], Sh::PITCH);
+        __syncthreads();
+        bf16x8 qf[QT][NT][NB];
+#pragma unroll
+        for (int y = 0; y < QT; ++y)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < NB; ++x)
+                    qf[y][n][x] = *(const bf16x8*)&sh.q[y][wave * ROWS_WAVE + 16 * n + col][8 * NB * g + 8 * x];
+
+        // the keys that each of the lane's rows sees; those that all of the wave's see, and that any does
+        int last[NT], low[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            Row r;
+            const bool live = row_of(a, seg, wave * ROWS_WAVE + 16 * n + col, r);
+            const int pos = seg.seq.len - seg.seq.n + r.query;
+            last[n] = !live ? -1 : a.causal ? pos : seg.seq.len - 1;
+            low[n] = a.window ? pos - a.window + 1 : 0;
+        }
+        const int pos0 = seg.seq.len - seg.seq.n + (seg.tile << a.tile_log2);
+        const int first_token = wave * ROWS_WAVE / a.tile_heads;
+        const int last_token = min((wave * ROWS_WAVE + ROWS_WAVE - 1) / a.tile_heads, tokens - 1);
+        const bool idle = first_token >= tokens;
+        const int all_to = a.causal ? pos0 + first_token : seg.seq.len - 1;
+        const int any_to = idle ? -1 : a.causal ? pos0 + last_token : seg.seq.len - 1;
+        const int all_from = a.window ? pos0 + last_token - a.window + 1 : 0;
+        const int any_from = a.window ? pos0 + first_token - a.window + 1 : 0;
+
+        f32x4 acc[NT][M];
+        float top[NT], sum[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            top[n] = -__builtin_inff();
+            sum[n] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) acc[n][m] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+
+        const int unit0 = seg.begin + (int)(at - seg.start);
+        const int unit1 = (int)min((int64_t)seg.end, seg.begin + (stop - seg.start));
+        const int units = seg.seq.len == 0 ? unit0 : unit1;
+        const int32_t* table = a.table + seg.s * a.table_ld;
+        const int last_group = (seg.seq.len - 1) & ~7;
+        auto look_up = [&](int unit) { return table[min(UNIT * unit + 8 * (lane & 7), last_group) >> shift]; };
+        auto checked = [&](int page) { return page >= 0 && page < (int)a.cache.pages ? page : -1; };
+        auto page_of = [&](int pages, int group) { return __builtin_amdgcn_ds_bpermute(4 * group, pages); };
+
+        // what this wave brings in: K of the scores' product `wave` of the unit's four, and of V the keys of products
+        // 2 j and 2 j + 1, half of each lane's elements
+        const int j_in = wave >> 1, t_in = wave & 1;
+        uint32_t kc[NB], vc[8];
+        int kb[NB == 8 ? 2 : 1];
+        uint2 vs;
+        auto load = [&](int unit, int pages) {
+            const int key_k = min(UNIT * unit + 32 * j_in + 8 * (col >> 2), last_group);
+            const int o = (key_k & ((1 << shift) - 1)) + 4 * t_in + (col & 3);
+            const int64_t pk = (int64_t)max(page_of(pages, 4 * j_in + (col >> 2)), 0) * a.cache.heads + head;
+            const uint8_t* codes = a.cache.codes[0] + ((pk << shift) + o) * row_bytes;
+            const uint8_t* scales = a.cache.scales[0] + (pk * blocks << shift) + o;
+            if constexpr (NB == 2) {
+                const bool there = EXACT || 8 * g < row_bytes;
+                const uint2 w = *(const uint2*)(codes + (there ? 8 * g : 0));
+                kc[0] = there ? w.x : 0u;
+                kc[1] = there ? w.y : 0u;
+                kb[0] = scales[(int64_t)(there ? g >> 1 : 0) << shift];
+                if (!there) kb[0] = 0;
+            } else {
+#pragma unroll
+                for (int h = 0; h < NB / 4; ++h) {
+                    const int block = g * (NB / 4) + h;
+                    const bool there = EXACT || block < blocks;
+                    const uint4 w = *(const uint4*)(codes + (there ? 16 * block : 0));
+                    kc[4 * h] = there ? w.x : 0u;
+                    kc[4 * h + 1] = there ? w.y : 0u;
+                    kc[4 * h + 2] = there ? w.z : 0u;
+                    kc[4 * h + 3] = there ? w.w : 0u;
+                    kb[h] = scales[(int64_t)(there ? block : 0) << shift];
+                    if (!there) kb[h] = 0;
+                }
+            }
+            const int key_v = min(UNIT * unit + 32 * j_in + 8 * g, last_group), ov = key_v & ((1 << shift) - 1);
+            const int64_t pv = (int64_t)max(page_of(pages, 4 * j_in + g), 0) * a.cache.heads + head;
+            const int c = EXACT || col * NB < row_bytes ? col : 0;
+            const uint8_t* from = a.cache.codes[1] + ((pv << shift) + ov) * row_bytes + c * NB + t_in * KV;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (KV == 1) vc[i] = from[i * row_bytes];
+                else if constexpr (KV == 2) vc[i] = *(const uint16_t*)(from + i * row_bytes);
+                else vc[i] = *(const uint32_t*)(from + i * row_bytes);
+            }
+            vs = *(const uint2*)(a.cache.scales[1] + ((pv * blocks + c * NB / 16) << shift) + ov);
+        };
+        auto store = [&](int buf) {
+#pragma unroll
+            for (int x = 0; x < NB; ++x) {
+                uint32_t u[4];
+                widen8(kc[x], scale_operand((uint32_t)kb[x >> 2]), u);
+                *(uint4*)&sh.work.k[buf][((wave * NB + x) * 64 + lane) * 16] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            // a value that is not finite: its scale becomes 0, and a mark says where it was
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) odd |= (((i < 4 ? vs.x : vs.y) >> (8 * (i & 3))) & 0xFFu) == 0xFFu;
+            const bool any = __any(odd);
+            if (any) {
+                uint32_t mark[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t& w = i < 4 ? vs.x : vs.y;
+                    const uint32_t byte = 0xFFu << (8 * (i & 3));
+                    if ((w & byte) == byte) {
+                        w &= ~byte;
+                        mark[i >> 1] |= 0x3F80u << (16 * (i & 1));
+                    }
+                }
+                if (t_in == 0) *(uint4*)&sh.work.marks[buf][j_in][lane * 16] = make_uint4(mark[0], mark[1], mark[2], mark[3]);
+            }
+            if (t_in == 0 && lane == 0) sh.work.odd[buf][j_in] = any;
+            float sc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = scale_of(i < 4 ? vs.x : vs.y, i & 3);
+#pragma unroll
+            for (int b = 0; b < KV; ++b) {
+                uint32_t u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = widen2(vc[i], sc[i], b);
+#pragma unroll
+                for (int second = 0; second < 2; ++second) {
+                    const uint32_t sel = second ? 0x07060302u : 0x05040100u;
+                    const int k = 2 * (t_in * KV + b) + second;
+                    *(uint4*)&sh.work.v[buf][((j_in * M + k) * 64 + lane) * 16] =
+                        make_uint4(__builtin_amdgcn_perm(u[1], u[0], sel), __builtin_amdgcn_perm(u[3], u[2], sel),
+                                   __builtin_amdgcn_perm(u[5], u[4], sel), __builtin_amdgcn_perm(u[7], u[6], sel));
+                }
+            }
+        };
+
+        __syncthreads();                                   // the queries are in registers: their place is free
+        int pages = 0, pages1 = 0, pages2 = 0;             // of this unit, the next, the one after
+        if (unit0 < units) {
+            pages = checked(look_up(unit0));
+            load(unit0, pages);
+            pages1 = checked(look_up(min(unit0 + 1, units - 1)));
+            store(unit0 & 1);
+            load(min(unit0 + 1, units - 1), pages1);
+            pages2 = look_up(min(unit0 + 2, units - 1));
+        }
+        for (int unit = unit0; unit < units; ++unit) {
+            const int buf = unit & 1, key0 = UNIT * unit;
+            __syncthreads();                               // this unit's operands are there, the last one's are read
+            pages2 = checked(pages2);
+            const int pages3 = look_up(min(unit + 3, units - 1));
+            if (unit + 1 < units) store(buf ^ 1);
+            load(min(unit + 2, units - 1), pages2);
+            __builtin_amdgcn_sched_barrier(0);
+            if (key0 <= any_to && key0 + UNIT - 1 >= any_from) {
+                const bool whole = key0 + UNIT - 1 <= all_to && key0 >= all_from && !__any(pages < 0);
+                f32x4 s[NT][4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                    for (int x = 0; x < NB; ++x) {
+                        const bf16x8 k = *(const bf16x8*)&sh.work.k[buf][((t * NB + x) * 64 + lane) * 16];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int y = 0; y < QT; ++y)
+                                s[n][t] = mfma(k, qf[y][n][x], x == 0 && y == 0 ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : s[n][t]);
+                    }
+                }
+                uint32_t p[NT][2][PT][4];
+                bool bad[2] = {false, false};
+                if (!whole) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) bad[j] = page_of(pages, 4 * j + g) < 0;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = s[n][i >> 2][i & 3] * a.scale;
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int key = key0 + 32 * (i >> 3) + 8 * g + (i & 7);
+                            x[i] = key <= last[n] && key >= low[n] && !bad[i >> 3] ? x[i] : -__builtin_inff();
+                        }
+                    }
+                    float m = x[0];
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) m = fmaxf(m, x[i]);
+                    m = fmaxf(across(m, MaxF()), top[n]);
+                    const float safe = m == -__builtin_inff() ? 0.0f : m;
+                    if (__any(m > top[n])) {
+                        const float f = __builtin_amdgcn_exp2f(top[n] - safe);
+                        sum[n] *= f;
+#pragma unroll
+                        for (int k = 0; k < M; ++k) acc[n][k] *= f;
+                    }
+                    top[n] = m;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float e0 = __builtin_amdgcn_exp2f(x[2 * i] - safe), e1 = __builtin_amdgcn_exp2f(x[2 * i + 1] - safe);
+                        sum[n] += e0 + e1;
+                        const uint32_t w = pack(e0, e1);
+                        p[n][i >> 2][0][i & 3] = w;
+                        if constexpr (PT == 2) p[n][i >> 2][PT - 1][i & 3] = pack(e0 - bf16lo(w), e1 - bf16hi(w));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (__builtin_amdgcn_readfirstlane(sh.work.odd[buf][j])) {
+                        const uint4 mark = *(const uint4*)&sh.work.marks[buf][j][lane * 16];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t seen[4] = {0, 0, 0, 0};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int key = key0 + 32 * j + 8 * g + i;
+                                if (key <= last[n] && key >= low[n] && !bad[j]) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
+                            }
+                            const f32x4 hit = mfma(operand(mark.x, mark.y, mark.z, mark.w),
+                                                   operand(seen[0], seen[1], seen[2], seen[3]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int k = 0; k < M; ++k) acc[n][k][i] = hit[i] == 0.0f ? acc[n][k][i] : __builtin_nanf("");
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < M; ++k) {
+                        const bf16x8 v = *(const bf16x8*)&sh.work.v[buf][((j * M + k) * 64 + lane) * 16];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int y = 0; y < PT; ++y)
+                                acc[n][k] = mfma(v, operand(p[n][j][y][0], p[n][j][y][1], p[n][j][y][2], p[n][j][y][3]),
+                                                 acc[n][k]);
+                    }
+                }
+            }
+            pages = pages1;
+            pages1 = pages2;
+            pages2 = pages3;
+        }
+
+        const bool complete = at == seg.start && unit1 == seg.end;
+        float* part = a.parts + (2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1)) * (ROWS_TILE * (32 * NB + 2));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int c = wave * ROWS_WAVE + 16 * n + col;
+            Row r;
+            const bool live = row_of(a, seg, c, r) && c < rows;
+            sum[n] = across(sum[n], AddF());
+            // the lane's elements of the row, 8 NB consecutive ones from 8 NB g on
+            float o[8 * NB];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < M; ++k) o[M * i + k] = acc[n][k][i];
+            if (complete) {
+                finish_row<NB, BF16>(a, r, live, 8 * NB * g, o, top[n], sum[n]);
+            } else if (live) {
+                float* to = part + c * 32 * NB + 8 * NB * g;
+#pragma unroll
+                for (int i = 0; i < 8 * NB; i += 4) *(f32x4*)(to + i) = (f32x4){o[i], o[i + 1], o[i + 2], o[i + 3]};
+                if (g == 0) {
+                    part[ROWS_TILE * 32 * NB + c] = top[n];
+                    part[ROWS_TILE * 32 * NB + ROWS_TILE + c] = sum[n];
+                }
+            }
+        }
+        const int64_t next = seg.start + (seg.end - seg.begin);
+        if (next > stop && seg.start >= begin && tid == 0) {
+            Cut& cut = a.cuts[blockIdx.x];
+            cut.seg = seg;
+            cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
+            cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
+        }
+        at = next;
+        if (at >= stop) return;
+        next_segment(a, seg);
+    }
+}
+
 // Joins the parts of the segments that were cut.  Workgroup x: the segment
 // that share x began and did not finish, if there is one; y: two of its rows.
 // Sets of threads (groups) share the parts, AHEAD of them under way at once.
@@ -849,18 +1265,18 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
 
 // What the host chooses from the sizes it knows.
 struct Shape {
-    int nb, nt, tile_tokens, tile_heads, head_tiles;
+    int nb, nt, tile_tokens, tile_heads, head_tiles;     // nt 0: attention_rows_kernel
     int64_t shares, part_floats;
 };
 
-Shape shape_of(const CacheView& c, int64_t tokens, int q_heads, int max_queries) {
+Shape shape_of(const CacheView& c, bool bf16, int64_t tokens, int q_heads, int max_queries) {
     Shape s;
     const int group = q_heads / c.heads;
     const int64_t most = max_queries > 0 ? min((int64_t)max_queries, tokens) : tokens;
     s.nb = c.dim <= 64 ? 2 : c.dim <= 128 ? 4 : 8;
     const int64_t rows = most * group;
-    s.nt = rows <= 16 ? 1 : rows <= 32 || s.nb == 8 ? 2 : 4;
-    const int r = 16 * s.nt;
+    s.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+    const int r = s.nt ? 16 * s.nt : ROWS_TILE;
     s.tile_heads = min(group, r);
     s.head_tiles = (group + r - 1) / r;
     s.tile_tokens = 1;
@@ -878,14 +1294,36 @@ void launch_main(const AttentionArgs& a, bool bf16, dim3 grid, hipStream_t s) {
     else hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, true, 1, 1>), grid, block, 0, s, a);
 }
 
-template <int NB, int NT>
+template <int NB, bool EXACT>
+void launch_rows(const AttentionArgs& a, bool bf16, dim3 grid, hipStream_t s) {
+    const dim3 block(WAVES * 64);
+    if (!bf16) hipLaunchKernelGGL((attention_rows_kernel<NB, EXACT, false, 2, 2>), grid, block, 0, s, a);
+    else if (a.cache.rht) hipLaunchKernelGGL((attention_rows_kernel<NB, EXACT, true, 2, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_rows_kernel<NB, EXACT, true, 1, 1>), grid, block, 0, s, a);
+}
+
+template <int NB, int NT>     // NT 0: attention_rows_kernel
 void launch(const AttentionArgs& a, bool bf16, int shares, hipStream_t s) {
-    const dim3 block(WAVES * 64), grid(shares), join(shares, 8 * NT);
-    if (a.cache.dim == 32 * NB) launch_main<NB, NT, true>(a, bf16, grid, s);
-    else launch_main<NB, NT, false>(a, bf16, grid, s);
+    constexpr int ROWS = NT ? 16 * NT : ROWS_TILE;
+    const dim3 block(WAVES * 64), grid(shares), join(shares, ROWS / 2);
+    const bool exact = a.cache.dim == 32 * NB;
+    if constexpr (NT == 0) {
+        if (exact) launch_rows<NB, true>(a, bf16, grid, s);
+        else launch_rows<NB, false>(a, bf16, grid, s);
+    } else {
+        if (exact) launch_main<NB, NT, true>(a, bf16, grid, s);
+        else launch_main<NB, NT, false>(a, bf16, grid, s);
+    }
     if (shares == 1) return;
-    if (bf16) hipLaunchKernelGGL((attention_join_kernel<NB, NT, true>), join, block, 0, s, a);
-    else hipLaunchKernelGGL((attention_join_kernel<NB, NT, false>), join, block, 0, s, a);
+    if (bf16) hipLaunchKernelGGL((attention_join_kernel<NB, ROWS / 16, true>), join, block, 0, s, a);
+    else hipLaunchKernelGGL((attention_join_kernel<NB, ROWS / 16, false>), join, block, 0, s, a);
+}
+
+template <int NB>
+void launch(const AttentionArgs& a, int nt, bool bf16, int shares, hipStream_t s) {
+    if (nt == 0) launch<NB, 0>(a, bf16, shares, s);
+    else if (nt == 1) launch<NB, 1>(a, bf16, shares, s);
+    else launch<NB, 2>(a, bf16, shares, s);
 }
 
 mx_status check_pitches(int64_t ld, int64_t head_ld, int dim) {
@@ -896,11 +1334,12 @@ mx_status check_pitches(int64_t ld, int64_t head_ld, int dim) {
 
 extern "C" {
 
-int64_t mx_cache_attention_workspace(const mx_cache* cache, int64_t tokens, int32_t q_heads, int32_t max_queries) {
+int64_t mx_cache_attention_workspace(const mx_cache* cache, mx_dtype qt, int64_t tokens, int32_t q_heads,
+                                     int32_t max_queries) {
     CacheView c;
     if (view_cache(cache, c) != MX_OK || q_heads < 1 || q_heads % c.heads || max_queries < 0) return 0;
-    if (tokens < 1 || tokens > INT32_MAX / q_heads) return 0;
-    const Shape s = shape_of(c, tokens, q_heads, max_queries);
+    if (tokens < 1 || tokens > INT32_MAX / q_heads || (qt != MX_F32 && qt != MX_BF16)) return 0;
+    const Shape s = shape_of(c, qt == MX_BF16, tokens, q_heads, max_queries);
     return s.shares * (2 * s.part_floats * (int64_t)sizeof(float) + (int64_t)sizeof(Cut));
 }
 
@@ -925,7 +1364,7 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
         return MX_ERR_SHAPE;
     if (tokens == 0) return MX_OK;
     if (!q || !out || !lengths || (table_pages > 0 && !page_table)) return MX_ERR_NULL;
-    if (mx_cache_attention_workspace(cache, tokens, q_heads, max_queries) > 0 && !workspace) return MX_ERR_NULL;
+    if (!workspace) return MX_ERR_NULL;
     if (!aligned_to(q, type_bytes(qt)) || !aligned_to(out, type_bytes(qt)) || !aligned_to(q_offsets, 4) ||
         !aligned_to(page_table, 4) || !aligned_to(lengths, 4) || !aligned_to(sinks, 4) || !aligned_to(lse, 4) ||
         !aligned_to(workspace, 16))
@@ -953,7 +1392,8 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.out_head_ld = out_head_ld ? out_head_ld : c.dim;
     a.lse = lse;
     hipStream_t s = (hipStream_t)stream;
-    const Shape shape = shape_of(c, tokens, q_heads, max_queries);
+    const bool bf16 = qt == MX_BF16;
+    const Shape shape = shape_of(c, bf16, tokens, q_heads, max_queries);
     a.group = q_heads / c.heads;
     a.tile_tokens = shape.tile_tokens;
     a.tile_log2 = __builtin_ctz(shape.tile_tokens);
@@ -967,20 +1407,10 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     const int64_t tiles = (tokens / shape.tile_tokens + min(tokens, (int64_t)seqs)) * a.line_heads;
     const int64_t units = tiles * max(ceil_div(a.capacity, UNIT), (int64_t)1);
     const int shares = (int)min(shape.shares, ceil_div(units, MIN_UNITS));
-    const bool bf16 = qt == MX_BF16;
     (void)hipGetLastError();
-    if (shape.nb == 2) {
-        if (shape.nt == 1) launch<2, 1>(a, bf16, shares, s);
-        else if (shape.nt == 2) launch<2, 2>(a, bf16, shares, s);
-        else launch<2, 4>(a, bf16, shares, s);
-    } else if (shape.nb == 4) {
-        if (shape.nt == 1) launch<4, 1>(a, bf16, shares, s);
-        else if (shape.nt == 2) launch<4, 2>(a, bf16, shares, s);
-        else launch<4, 4>(a, bf16, shares, s);
-    } else {
-        if (shape.nt == 1) launch<8, 1>(a, bf16, shares, s);
-        else launch<8, 2>(a, bf16, shares, s);
-    }
+    if (shape.nb == 2) launch<2>(a, shape.nt, bf16, shares, s);
+    else if (shape.nb == 4) launch<4>(a, shape.nt, bf16, shares, s);
+    else launch<8>(a, shape.nt, bf16, shares, s);
     return launch_status();
 }
 

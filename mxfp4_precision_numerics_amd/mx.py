@@ -85,7 +85,7 @@ def lib():
         L.mx_balance_bwd.argtypes = [P, c_int, i64, i32, i64, c_int, P, P, f32, P, i64, P, i64, P]
         L.mx_cache_write.argtypes = [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]
         L.mx_cache_read.argtypes = [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]
-        L.mx_cache_attention_workspace.argtypes = [P, i64, i32, i32]
+        L.mx_cache_attention_workspace.argtypes = [P, c_int, i64, i32, i32]
         L.mx_cache_attention_workspace.restype = i64
         L.mx_cache_attention.argtypes = [P, P, c_int, i64, i32, i64, i64, P, i32, i32, P, i64, i32, P, f32, c_int,
                                          i32, P, P, i64, i64, P, P, P]
@@ -1006,8 +1006,8 @@ def cache_attention(cache, q, page_table, lengths, scale=None, q_offsets=None, m
         _same(lse, (tokens, q_heads), torch.float32, "lse")
     elif need_lse:
         lse = _new(q.device, torch.float32, tokens, q_heads)
-    workspace = _workspace(workspace, lib().mx_cache_attention_workspace(cache._at, tokens, q_heads, max_queries),
-                           q.device)
+    need = lib().mx_cache_attention_workspace(cache._at, _dtype_code(q), tokens, q_heads, max_queries)
+    workspace = _workspace(workspace, need, q.device)
     _here(cache.device_index, q=q, page_table=page_table, lengths=lengths, q_offsets=q_offsets, sinks=sinks, out=out,
           lse=lse, workspace=workspace)
     _check("mx_cache_attention", lib().mx_cache_attention(

@@ -115,7 +115,7 @@ def test_attention_validation(L):
         assert call(**{name: None}) == NULL, name
     for name in ("q", "out", "len", "table", "sinks", "lse", "off"):
         assert call(**{name: FAKE + 1}) == ALIGN, name
-    assert call(ws=FAKE + 8) == ALIGN
+    assert call(ws=FAKE + 8) == ALIGN and call(ws=None) == NULL
     assert call(n=0, seqs=0, q=None, out=None, len=None, table=None, ws=None) == 0
     assert call(n=0, seqs=5, off=FAKE) == 0
 
@@ -123,12 +123,12 @@ def test_attention_validation(L):
 def test_attention_workspace_validation(L):
     ws, c = L.mx_cache_attention_workspace, cache()
     at = ctypes.addressof(c)
-    assert ws(None, 3, 4, 1) == 0 and ws(at, 0, 4, 1) == 0 and ws(at, -3, 4, 1) == 0 and ws(at, 3, 3, 1) == 0
-    assert ws(at, 3, 0, 1) == 0 and ws(at, 2 ** 31, 4, 0) == 0
-    assert ws(at, 3, 4, 1) >= 0
+    assert ws(None, 1, 3, 4, 1) == 0 and ws(at, 1, 0, 4, 1) == 0 and ws(at, 1, -3, 4, 1) == 0
+    assert ws(at, 1, 3, 3, 1) == 0 and ws(at, 1, 3, 0, 1) == 0 and ws(at, 0, 2 ** 31, 4, 0) == 0
+    assert ws(at, 2, 3, 4, 1) == 0 and ws(at, 0, 3, 4, -1) == 0 and ws(at, 0, 3, 4, 1) > 0 and ws(at, 1, 300, 4, 0) > 0
     for bad, _ in BAD_CACHES[:13]:
         b = cache(**bad)
-        assert ws(ctypes.addressof(b), 3, 4, 1) == 0
+        assert ws(ctypes.addressof(b), 1, 3, 4, 1) == 0
 
 
 def test_balance_validation(L):

@@ -383,7 +383,7 @@ def test_graphs_and_streams():
     outs = [tt.empty_like(v) for v in q]
     _, kv = values((2, 2, 128), tt.bfloat16, 152)
     slot = dev(np.array([s.table[0, 599 // 64] * 64 + 599 % 64, -1], dtype=np.int32))
-    need = max(1, mx.lib().mx_cache_attention_workspace(cache._at, 2, 8, 1))
+    need = max(1, mx.lib().mx_cache_attention_workspace(cache._at, mx.MX_BF16, 2, 8, 1))
     spaces = [tt.empty(need, dtype=tt.uint8, device="cuda") for _ in q]
 
     def step():
