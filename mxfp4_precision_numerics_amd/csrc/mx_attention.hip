@@ -32,6 +32,7 @@ struct AttentionArgs {
     int64_t out_ld, out_head_ld;
     float* lse;
     int group, tile_tokens, tile_log2, tile_heads, head_tiles, line_heads;
+    uint32_t code_page, scale_page;   // bytes of a page's codes, scales
     float* parts;
     Cut* cuts;                    // one a share
 };
@@ -243,6 +244,23 @@ __device__ __forceinline__ void next_segment(const AttentionArgs& a, Segment& g)
     set_tile(a, g);
 }
 
+// The kernel's arguments, read again from where they were passed.  What only
+// the begin and the end of a segment need would otherwise hold scalar registers
+// through the loop over the keys, which then spills (150 of them, a vector
+// instruction each on the way back).
+__device__ __forceinline__ AttentionArgs arguments() {
+    typedef const __attribute__((address_space(4))) uint32_t Word;
+    Word* p = (Word*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    union {
+        uint32_t w[sizeof(AttentionArgs) / 4];
+        AttentionArgs a;
+    } u;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(AttentionArgs) / 4); ++i) u.w[i] = p[i];
+    return u.a;
+}
+
 // A tile's row c: its query row and head; false where there is none.
 struct Row {
     int64_t token;
@@ -443,6 +461,47 @@ struct Shared {
     Line line;
 };
 
+// Where a lane finds its part of a page's first group of eight keys, in page 0:
+// K's codes (8 NB of them) and scales of key col & 3, V's codes (2 NB) and
+// scales of the first key.
+template <int NB, bool EXACT>
+struct Lane {
+    const uint8_t *k, *ks, *v, *vs;
+    bool k_there[NB == 8 ? 2 : 1];        // the row reaches that far (its halves, NB = 8)
+
+    __device__ __forceinline__ Lane(const AttentionArgs& a, int head, int col, int g) {
+        const int shift = a.cache.page_log2, row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1;
+        const int blocks = EXACT ? NB : a.cache.dim >> 5;
+        const int c = EXACT || col * NB < row_bytes ? col : 0;
+        int piece = 4 * NB * g;                            // bytes into a row
+        if constexpr (NB == 2) {
+            k_there[0] = EXACT || piece < row_bytes;
+        } else {
+#pragma unroll
+            for (int h = 0; h < NB / 4; ++h) k_there[h] = EXACT || piece + 16 * h < row_bytes;
+        }
+        if (!k_there[0]) piece = 0;
+        const int64_t codes = ((int64_t)head << shift) * row_bytes, scales = (int64_t)head * blocks << shift;
+        k = a.cache.codes[0] + codes + (col & 3) * row_bytes + piece;
+        ks = a.cache.scales[0] + scales + ((int64_t)(piece >> 4) << shift);
+        v = a.cache.codes[1] + codes + c * NB;
+        vs = a.cache.scales[1] + scales + ((int64_t)(c * NB >> 4) << shift);
+    }
+};
+
+__device__ __forceinline__ const uint8_t* in_page(const uint8_t* p, int page, uint32_t bytes) {
+    return p + (uint64_t)(uint32_t)page * bytes;
+}
+
+// Whether one of eight scale bytes is 0xFF.
+__device__ __forceinline__ bool any_odd(uint2 w) {
+    const uint32_t x = ((w.x & 0x7F7F7F7Fu) + 0x01010101u) & w.x, y = ((w.y & 0x7F7F7F7Fu) + 0x01010101u) & w.y;
+    return ((x | y) & 0x80808080u) != 0;
+}
+
+// Whether a row that sees the keys low .. last sees key from + i.
+__device__ __forceinline__ bool sees(int last, int low, int from, int i) { return i <= last - from && i >= low - from; }
+
 // A tile's queries into LDS, QT terms of bf16, transformed where the cache is;
 // 0 where there is none.  The whole workgroup calls.
 template <int NB, int ROWS, bool BF16, int QT>
@@ -502,7 +561,8 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4, q_at = col * Sh::PITCH + 8 * NB * g;
     const int shift = a.cache.page_log2;
-    const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1, blocks = EXACT ? NB : a.cache.dim >> 5;
+    const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1;
+    const float scale = a.scale;
 
     measure_line(a, sh.line);
     const int64_t total = uniform(sh.line.before[WAVES * 64]);
@@ -516,7 +576,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         const int head = seg.head / a.head_tiles;          // of the cache
         const int rows = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2)) * a.tile_heads;
         __syncthreads();
-        load_queries<NB, 16 * NT, BF16, QT>(a, seg, (__bf16*)sh.data, Sh::PITCH);
+        load_queries<NB, 16 * NT, BF16, QT>(arguments(), seg, (__bf16*)sh.data, Sh::PITCH);
         __syncthreads();
 
         // the keys that each of the lane's rows sees, and those that all see
@@ -555,51 +615,47 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         uint32_t vc[2][8][VW];        // codes of V: [j][key]
         uint2 vs[2];
         const int kg = 8 * (col >> 2);                     // the lane's group of keys in a score product
-        const bool v_there = EXACT || col * NB < row_bytes;
 
         // A lane looks up the page of one of a unit's eight groups of keys, -1 if it does not exist; others get it
         // from there.
         auto look_up = [&](int unit) { return table[min(UNIT * unit + 8 * (lane & 7), last_group) >> shift]; };
         auto checked = [&](int page) { return page >= 0 && page < (int)a.cache.pages ? page : -1; };
         auto page_of = [&](int pages, int group) { return __builtin_amdgcn_ds_bpermute(4 * group, pages); };
+        const Lane<NB, EXACT> my(a, head, col, g);
         auto load_k = [&](int unit, int j, int page) {
-            const int o = (min(UNIT * unit + 32 * j + kg, last_group)) & ((1 << shift) - 1);
-            const int64_t p = (int64_t)max(page, 0) * a.cache.heads + head;
-            const uint8_t* codes = a.cache.codes[0] + ((p << shift) + o + (col & 3)) * row_bytes;
-            const uint8_t* scales = a.cache.scales[0] + (p * blocks << shift) + o;
+            const int o = min(UNIT * unit + 32 * j + kg, last_group) & ((1 << shift) - 1);
+            const uint8_t* codes = in_page(my.k, max(page, 0), a.code_page) + o * row_bytes;
+            const uint8_t* scales = in_page(my.ks, max(page, 0), a.scale_page) + o;
             if constexpr (NB == 2) {
-                const bool there = EXACT || 8 * g < row_bytes;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const uint2 w = *(const uint2*)(codes + (4 * t) * row_bytes + (there ? 8 * g : 0));
-                    kc[j][t][0] = there ? w.x : 0u;
-                    kc[j][t][1] = there ? w.y : 0u;
+                    const uint2 w = *(const uint2*)(codes + 4 * t * row_bytes);
+                    kc[j][t][0] = my.k_there[0] ? w.x : 0u;
+                    kc[j][t][1] = my.k_there[0] ? w.y : 0u;
                 }
-                ks[j][0] = *(const uint2*)(scales + ((int64_t)(there ? g >> 1 : 0) << shift));
-                if (!there) ks[j][0] = make_uint2(0u, 0u);
+                ks[j][0] = *(const uint2*)scales;
+                if (!my.k_there[0]) ks[j][0] = make_uint2(0u, 0u);
             } else {
 #pragma unroll
                 for (int h = 0; h < NB / 4; ++h) {
-                    const int block = g * (NB / 4) + h;
-                    const bool there = EXACT || block < blocks;
+                    const bool there = my.k_there[h];
+                    const int more = !EXACT && !there ? 0 : h;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const uint4 w = *(const uint4*)(codes + (4 * t) * row_bytes + (there ? 16 * block : 0));
+                        const uint4 w = *(const uint4*)(codes + 4 * t * row_bytes + 16 * more);
                         kc[j][t][4 * h] = there ? w.x : 0u;
                         kc[j][t][4 * h + 1] = there ? w.y : 0u;
                         kc[j][t][4 * h + 2] = there ? w.z : 0u;
                         kc[j][t][4 * h + 3] = there ? w.w : 0u;
                     }
-                    ks[j][h] = *(const uint2*)(scales + ((int64_t)(there ? block : 0) << shift));
+                    ks[j][h] = *(const uint2*)(scales + (more << shift));
                     if (!there) ks[j][h] = make_uint2(0u, 0u);
                 }
             }
         };
         auto load_v = [&](int unit, int j, int page) {
-            const int o = (min(UNIT * unit + 32 * j + 8 * g, last_group)) & ((1 << shift) - 1);
-            const int64_t p = (int64_t)max(page, 0) * a.cache.heads + head;
-            const int c = v_there ? col : 0;
-            const uint8_t* codes = a.cache.codes[1] + ((p << shift) + o) * row_bytes + c * NB;
+            const int o = min(UNIT * unit + 32 * j + 8 * g, last_group) & ((1 << shift) - 1);
+            const uint8_t* codes = in_page(my.v, max(page, 0), a.code_page) + o * row_bytes;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint8_t* from = codes + i * row_bytes;
@@ -611,7 +667,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                     vc[j][i][VW - 1] = w.y;
                 }
             }
-            vs[j] = *(const uint2*)(a.cache.scales[1] + ((p * blocks + c * NB / 16) << shift) + o);
+            vs[j] = *(const uint2*)(in_page(my.vs, max(page, 0), a.scale_page) + o);
         };
 
         int unit = unit0 + wave, pages = 0, next_pages = 0;
@@ -665,19 +721,16 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                 for (int n = 0; n < NT; ++n) {
                     float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = s[n][i >> 2][i & 3] * a.scale;
+                    for (int i = 0; i < 8; ++i) x[i] = s[n][i >> 2][i & 3];
                     if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int key = key0 + 32 * j + 8 * g + i;
-                            x[i] = key <= last[n] && key >= low[n] && !bad ? x[i] : -__builtin_inff();
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            x[i] = sees(last[n], low[n], key0 + 32 * j + 8 * g, i) && !bad ? x[i] : -__builtin_inff();
                     }
                     float m = x[0];
 #pragma unroll
                     for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
-                    m = across(m, MaxF());
-                    m = fmaxf(m, top[n]);
+                    m = fmaxf(across(m, MaxF()) * scale, top[n]);
                     const float safe = m == -__builtin_inff() ? 0.0f : m;
                     if (__any(m > top[n])) {
                         const float f = __builtin_amdgcn_exp2f(top[n] - safe);
@@ -688,7 +741,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                     top[n] = m;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        x[i] = __builtin_amdgcn_exp2f(x[i] - safe);
+                        x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, -safe));
                         sum[n] += x[i];
                     }
 #pragma unroll
@@ -705,10 +758,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                 if (!whole) {
                     // A value that is not finite reaches the rows that see it, and no others: its scale becomes 0
                     // here, and a product of the marks "not finite" and "seen" says where there was one.
-                    bool odd = false;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) odd |= ((((i < 4 ? scales.x : scales.y) >> (8 * (i & 3))) & 0xFFu) == 0xFFu);
-                    if (__any(odd)) {
+                    if (__any(any_odd(scales))) {
                         uint32_t mark[4] = {0, 0, 0, 0};
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -722,11 +772,11 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             uint32_t seen[4] = {0, 0, 0, 0};
+                            int from = key0 + 32 * j + 8 * g;
+                            asm volatile("" : "+v"(from));     // (the comparisons made above are not kept for this)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int key = key0 + 32 * j + 8 * g + i;
-                                if (key <= last[n] && key >= low[n] && !bad) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                if (sees(last[n], low[n], from, i) && !bad) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
                             const f32x4 hit = mfma(operand(mark[0], mark[1], mark[2], mark[3]),
                                                    operand(seen[0], seen[1], seen[2], seen[3]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
@@ -776,8 +826,9 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
             }
         }
         __syncthreads();                                   // (also: nobody reads the queries any more)
+        const AttentionArgs b = arguments();
         const bool complete = at == seg.start && unit1 == seg.end;
-        const Part<NB, NT> part(a, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
+        const Part<NB, NT> part(b, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
         constexpr int SIDES = 32 * NB / Sh::SIDE;
         float* o = (float*)sh.data;
 #pragma unroll
@@ -815,9 +866,9 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                         for (int y = 0; y < 8; ++y) v[y] += from[y];
                     }
                     Row r;
-                    const bool live = row_of(a, seg, 16 * n + c, r);
+                    const bool live = row_of(b, seg, 16 * n + c, r);
                     if (complete) {
-                        finish<BF16>(a, r, live, d, v, most, all);
+                        finish<BF16>(b, r, live, d, v, most, all);
                     } else if (live) {
                         float* to_part = part.row(16 * n + c) + d;
                         *(f32x4*)to_part = (f32x4){v[0], v[1], v[2], v[3]};
@@ -833,14 +884,14 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         }
         const int64_t next = seg.start + (seg.end - seg.begin);
         if (next > stop && seg.start >= begin && tid == 0) {
-            Cut& cut = a.cuts[blockIdx.x];
+            Cut& cut = b.cuts[blockIdx.x];
             cut.seg = seg;
             cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
             cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
         }
         at = next;
         if (at >= stop) return;
-        next_segment(a, seg);
+        next_segment(b, seg);
     }
 }
 
@@ -883,7 +934,8 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int shift = a.cache.page_log2;
-    const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1, blocks = EXACT ? NB : a.cache.dim >> 5;
+    const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1;
+    const float scale = a.scale;
 
     measure_line(a, sh.line);
     const int64_t total = uniform(sh.line.before[WAVES * 64]);
@@ -898,7 +950,7 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
         const int tokens = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2));
         const int rows = tokens * a.tile_heads;
         __syncthreads();
-        load_queries<NB, ROWS_TILE, BF16, QT>(a, seg, &sh.q[0][0][0], Sh::PITCH);
+        load_queries<NB, ROWS_TILE, BF16, QT>(arguments(), seg, &sh.q[0][0][0], Sh::PITCH);
         __syncthreads();
         bf16x8 qf[QT][NT][NB];
 #pragma unroll
@@ -953,44 +1005,42 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
         uint32_t kc[NB], vc[8];
         int kb[NB == 8 ? 2 : 1];
         uint2 vs;
+        const Lane<NB, EXACT> my(a, head, col, g);
         auto load = [&](int unit, int pages) {
-            const int key_k = min(UNIT * unit + 32 * j_in + 8 * (col >> 2), last_group);
-            const int o = (key_k & ((1 << shift) - 1)) + 4 * t_in + (col & 3);
-            const int64_t pk = (int64_t)max(page_of(pages, 4 * j_in + (col >> 2)), 0) * a.cache.heads + head;
-            const uint8_t* codes = a.cache.codes[0] + ((pk << shift) + o) * row_bytes;
-            const uint8_t* scales = a.cache.scales[0] + (pk * blocks << shift) + o;
+            const int ok = min(UNIT * unit + 32 * j_in + 8 * (col >> 2), last_group) & ((1 << shift) - 1);
+            const int page_k = max(page_of(pages, 4 * j_in + (col >> 2)), 0);
+            const uint8_t* codes = in_page(my.k, page_k, a.code_page) + (ok + 4 * t_in) * row_bytes;
+            const uint8_t* scales = in_page(my.ks, page_k, a.scale_page) + ok + 4 * t_in + (col & 3);
             if constexpr (NB == 2) {
-                const bool there = EXACT || 8 * g < row_bytes;
-                const uint2 w = *(const uint2*)(codes + (there ? 8 * g : 0));
-                kc[0] = there ? w.x : 0u;
-                kc[1] = there ? w.y : 0u;
-                kb[0] = scales[(int64_t)(there ? g >> 1 : 0) << shift];
-                if (!there) kb[0] = 0;
+                const uint2 w = *(const uint2*)codes;
+                kc[0] = my.k_there[0] ? w.x : 0u;
+                kc[1] = my.k_there[0] ? w.y : 0u;
+                kb[0] = *scales;
+                if (!my.k_there[0]) kb[0] = 0;
             } else {
 #pragma unroll
                 for (int h = 0; h < NB / 4; ++h) {
-                    const int block = g * (NB / 4) + h;
-                    const bool there = EXACT || block < blocks;
-                    const uint4 w = *(const uint4*)(codes + (there ? 16 * block : 0));
+                    const bool there = my.k_there[h];
+                    const int more = !EXACT && !there ? 0 : h;
+                    const uint4 w = *(const uint4*)(codes + 16 * more);
                     kc[4 * h] = there ? w.x : 0u;
                     kc[4 * h + 1] = there ? w.y : 0u;
                     kc[4 * h + 2] = there ? w.z : 0u;
                     kc[4 * h + 3] = there ? w.w : 0u;
-                    kb[h] = scales[(int64_t)(there ? block : 0) << shift];
+                    kb[h] = scales[more << shift];
                     if (!there) kb[h] = 0;
                 }
             }
-            const int key_v = min(UNIT * unit + 32 * j_in + 8 * g, last_group), ov = key_v & ((1 << shift) - 1);
-            const int64_t pv = (int64_t)max(page_of(pages, 4 * j_in + g), 0) * a.cache.heads + head;
-            const int c = EXACT || col * NB < row_bytes ? col : 0;
-            const uint8_t* from = a.cache.codes[1] + ((pv << shift) + ov) * row_bytes + c * NB + t_in * KV;
+            const int ov = min(UNIT * unit + 32 * j_in + 8 * g, last_group) & ((1 << shift) - 1);
+            const int page_v = max(page_of(pages, 4 * j_in + g), 0);
+            const uint8_t* from = in_page(my.v, page_v, a.code_page) + ov * row_bytes + t_in * KV;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if constexpr (KV == 1) vc[i] = from[i * row_bytes];
                 else if constexpr (KV == 2) vc[i] = *(const uint16_t*)(from + i * row_bytes);
                 else vc[i] = *(const uint32_t*)(from + i * row_bytes);
             }
-            vs = *(const uint2*)(a.cache.scales[1] + ((pv * blocks + c * NB / 16) << shift) + ov);
+            vs = *(const uint2*)(in_page(my.vs, page_v, a.scale_page) + ov);
         };
         auto store = [&](int buf) {
 #pragma unroll
@@ -1000,10 +1050,7 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
                 *(uint4*)&sh.work.k[buf][((wave * NB + x) * 64 + lane) * 16] = make_uint4(u[0], u[1], u[2], u[3]);
             }
             // a value that is not finite: its scale becomes 0, and a mark says where it was
-            bool odd = false;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) odd |= (((i < 4 ? vs.x : vs.y) >> (8 * (i & 3))) & 0xFFu) == 0xFFu;
-            const bool any = __any(odd);
+            const bool any = __any(any_odd(vs));
             if (any) {
                 uint32_t mark[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -1080,18 +1127,17 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
                 for (int n = 0; n < NT; ++n) {
                     float x[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = s[n][i >> 2][i & 3] * a.scale;
+                    for (int i = 0; i < 16; ++i) x[i] = s[n][i >> 2][i & 3];
                     if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int key = key0 + 32 * (i >> 3) + 8 * g + (i & 7);
-                            x[i] = key <= last[n] && key >= low[n] && !bad[i >> 3] ? x[i] : -__builtin_inff();
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = sees(last[n], low[n], key0 + 8 * g, 32 * (i >> 3) + (i & 7)) && !bad[i >> 3]
+                                       ? x[i] : -__builtin_inff();
                     }
                     float m = x[0];
 #pragma unroll
                     for (int i = 1; i < 16; ++i) m = fmaxf(m, x[i]);
-                    m = fmaxf(across(m, MaxF()), top[n]);
+                    m = fmaxf(across(m, MaxF()) * scale, top[n]);
                     const float safe = m == -__builtin_inff() ? 0.0f : m;
                     if (__any(m > top[n])) {
                         const float f = __builtin_amdgcn_exp2f(top[n] - safe);
@@ -1102,7 +1148,8 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
                     top[n] = m;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float e0 = __builtin_amdgcn_exp2f(x[2 * i] - safe), e1 = __builtin_amdgcn_exp2f(x[2 * i + 1] - safe);
+                        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], scale, -safe));
+                        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i + 1], scale, -safe));
                         sum[n] += e0 + e1;
                         const uint32_t w = pack(e0, e1);
                         p[n][i >> 2][0][i & 3] = w;
@@ -1116,11 +1163,11 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             uint32_t seen[4] = {0, 0, 0, 0};
+                            int from = key0 + 32 * j + 8 * g;
+                            asm volatile("" : "+v"(from));     // (the comparisons made above are not kept for this)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int key = key0 + 32 * j + 8 * g + i;
-                                if (key <= last[n] && key >= low[n] && !bad[j]) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                if (sees(last[n], low[n], from, i) && !bad[j]) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
                             const f32x4 hit = mfma(operand(mark.x, mark.y, mark.z, mark.w),
                                                    operand(seen[0], seen[1], seen[2], seen[3]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
@@ -1146,13 +1193,14 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
             pages2 = pages3;
         }
 
+        const AttentionArgs b = arguments();
         const bool complete = at == seg.start && unit1 == seg.end;
-        float* part = a.parts + (2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1)) * (ROWS_TILE * (32 * NB + 2));
+        float* part = b.parts + (2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1)) * (ROWS_TILE * (32 * NB + 2));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int c = wave * ROWS_WAVE + 16 * n + col;
             Row r;
-            const bool live = row_of(a, seg, c, r) && c < rows;
+            const bool live = row_of(b, seg, c, r) && c < rows;
             sum[n] = across(sum[n], AddF());
             // the lane's elements of the row, 8 NB consecutive ones from 8 NB g on
             float o[8 * NB];
@@ -1161,7 +1209,7 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
 #pragma unroll
                 for (int k = 0; k < M; ++k) o[M * i + k] = acc[n][k][i];
             if (complete) {
-                finish_row<NB, BF16>(a, r, live, 8 * NB * g, o, top[n], sum[n]);
+                finish_row<NB, BF16>(b, r, live, 8 * NB * g, o, top[n], sum[n]);
             } else if (live) {
                 float* to = part + c * 32 * NB + 8 * NB * g;
 #pragma unroll
@@ -1174,14 +1222,14 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
         }
         const int64_t next = seg.start + (seg.end - seg.begin);
         if (next > stop && seg.start >= begin && tid == 0) {
-            Cut& cut = a.cuts[blockIdx.x];
+            Cut& cut = b.cuts[blockIdx.x];
             cut.seg = seg;
             cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
             cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
         }
         at = next;
         if (at >= stop) return;
-        next_segment(a, seg);
+        next_segment(b, seg);
     }
 }
 
@@ -1400,6 +1448,8 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.tile_heads = shape.tile_heads;
     a.head_tiles = shape.head_tiles;
     a.line_heads = c.heads * shape.head_tiles;
+    a.code_page = (uint32_t)(c.heads * cache->page_size * (c.dim / 2));
+    a.scale_page = (uint32_t)(c.heads * cache->page_size * (c.dim / 32));
     a.cuts = (Cut*)workspace;
     a.parts = (float*)(a.cuts + shape.shares);
     if (c.pages == 0) a.capacity = 0;
