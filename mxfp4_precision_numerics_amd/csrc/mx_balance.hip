@@ -83,10 +83,16 @@ __global__ __launch_bounds__(THREADS) void balance_kernel(BalanceArgs a) {
     const bool softmax = a.score == MX_SOFTMAX;
     float acc[N] = {};
     int used = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < a.tokens; row0 += (int64_t)a.blocks * ROWS) {
-        const bool live = row0 + r < a.tokens;
-        float v[N];
-        load_row<BF16, L, C>(a.logits, (live ? row0 + r : a.tokens - 1) * a.ld, a.experts, a.vec, lane, v);
+    // the next rows are under way while these are worked on
+    const int64_t step = (int64_t)a.blocks * ROWS;
+    float v[N], next[N];
+    int64_t row = (int64_t)blockIdx.x * ROWS + r;
+    load_row<BF16, L, C>(a.logits, min(row, a.tokens - 1) * a.ld, a.experts, a.vec, lane, next);
+    for (; row - r < a.tokens; row += step) {
+        const bool live = row < a.tokens;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = next[i];
+        load_row<BF16, L, C>(a.logits, min(row + step, a.tokens - 1) * a.ld, a.experts, a.vec, lane, next);
         float any = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) any = v[i] == -__builtin_inff() ? any : 1.0f;
@@ -260,9 +266,8 @@ void launch(const BalanceBwdArgs& a, hipStream_t s) {
 // many tokens half as many lanes take a row, as in the router.
 constexpr int64_t MANY_TOKENS = 8192;
 template <bool B, class A>
-void dispatch(const A& a, hipStream_t s) {
+void dispatch(const A& a, bool many, hipStream_t s) {
     const int e = a.experts;
-    const bool many = a.tokens >= MANY_TOKENS;
     if (e <= 32) launch<B, 8, 1>(a, s);
     else if (e <= 64 && many) launch<B, 8, 2>(a, s);
     else if (e <= 128 && many) launch<B, 8, 4>(a, s);
@@ -309,8 +314,8 @@ mx_status mx_balance(const void* logits, mx_dtype lt, int64_t tokens, int32_t ex
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
     if (blocks > 0) {
-        if (lt == MX_BF16) dispatch<true>(a, s);
-        else dispatch<false>(a, s);
+        if (lt == MX_BF16) dispatch<true>(a, false, s);
+        else dispatch<false>(a, false, s);
     }
     int lanes_log2 = 0;
     while (1 << lanes_log2 < experts) ++lanes_log2;
@@ -339,8 +344,9 @@ mx_status mx_balance_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_
     a.vec_add = experts % 4 == 0 && a.add_ld % 4 == 0 && aligned_to(add, four);
     a.vec_out = experts % 4 == 0 && a.dld % 4 == 0 && aligned_to(dlogits, four);
     (void)hipGetLastError();
-    if (lt == MX_BF16) dispatch<true>(a, (hipStream_t)stream);
-    else dispatch<false>(a, (hipStream_t)stream);
+    const bool many = tokens >= MANY_TOKENS;
+    if (lt == MX_BF16) dispatch<true>(a, many, (hipStream_t)stream);
+    else dispatch<false>(a, many, (hipStream_t)stream);
     return launch_status();
 }
 

@@ -25,19 +25,32 @@ struct CacheArgs {
     CacheView cache;
     Rows rows;
     const int32_t* slots;
-    int64_t pieces;           // of eight elements: tokens * heads * dim / 8
+    int64_t tokens;
+    int lanes;                // of a row: dim / 8
+    int per;                  // tokens of a workgroup's pass: 256 / lanes
 };
 
-// Where piece i lies: its token, head and first element.
-struct Place {
-    int64_t token;
-    int head, at;
-    __device__ __forceinline__ Place(const CacheArgs& a, int64_t i) {
-        const int per = a.cache.dim >> 3;
-        const int64_t row = i / per;
-        at = (int)(i - row * per) * 8;
-        token = row / a.cache.heads;
-        head = (int)(row - token * a.cache.heads);
+// What a thread of a pass handles: eight elements of one token's row of one
+// head; four lanes hold a block of 32, the lanes after them the token's next
+// blocks, then the head's next token, so that a wave writes consecutive tokens
+// of a page: whole lines of codes, neighbouring scale bytes.
+struct Piece {
+    int64_t token, slot;      // slot -1: outside the cache, or no such token
+    int at;                   // first element
+    bool live;                // there is such a token
+
+    __device__ __forceinline__ Piece(const CacheArgs& a, int64_t first) {
+        const int t = (int)threadIdx.x / a.lanes;
+        at = ((int)threadIdx.x - t * a.lanes) * 8;
+        token = first + t;
+        live = t < a.per && token < a.tokens;
+        slot = live ? a.slots[token] : -1;
+        if (slot >= a.cache.pages << a.cache.page_log2) slot = -1;
+    }
+    __device__ __forceinline__ int64_t page(const CacheArgs& a) const { return slot >> a.cache.page_log2; }
+    __device__ __forceinline__ int offset(const CacheArgs& a) const { return (int)slot & ((1 << a.cache.page_log2) - 1); }
+    __device__ __forceinline__ int64_t row(const CacheArgs& a, int which, int head) const {
+        return token * a.rows.ld[which] + head * a.rows.head_ld[which] + at;
     }
 };
 
@@ -60,19 +73,20 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float* f) {
     }
 }
 
+// Past the caches: what is read back is far more than they would keep of it.
 template <bool BF16>
 __device__ __forceinline__ void store8(void* p, int64_t at, const float* f) {
     if constexpr (BF16) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16_rne(f[2 * i]) | f32_to_bf16_rne(f[2 * i + 1]) << 16;
-        *(u32x4v*)((uint16_t*)p + at) = (u32x4v){u[0], u[1], u[2], u[3]};
+        __builtin_nontemporal_store((u32x4v){u[0], u[1], u[2], u[3]}, (u32x4v*)((uint16_t*)p + at));
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            *(u32x4v*)((float*)p + at + 4 * i) =
-                (u32x4v){__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                         __float_as_uint(f[4 * i + 3])};
+            __builtin_nontemporal_store((u32x4v){__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                                 __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])},
+                                        (u32x4v*)((float*)p + at + 4 * i));
     }
 }
 
@@ -82,62 +96,88 @@ __device__ __forceinline__ void flip_signs(float* f, uint32_t mask, int q) {
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(__float_as_uint(f[i]) ^ (m >> i << 31));
 }
 
-// A thread: eight elements of a token's keys (blockIdx.y = 0) or values (1); a
-// block of 32 is a quad of lanes.
-template <bool BF16>
+// PASSES passes of a workgroup, keys and values: all of their loads are under
+// way before the first is used.
+template <bool BF16, int PASSES>
 __global__ __launch_bounds__(256) void cache_write_kernel(CacheArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= a.pieces) return;                             // (whole quads: pieces % 4 == 0)
-    const Place p(a, i);
-    const int64_t slot = a.slots[p.token];
-    if (slot < 0 || slot >= (a.cache.pages << a.cache.page_log2)) return;
-    const int which = blockIdx.y, q = threadIdx.x & 3;
-    float f[8];
-    load8<BF16>(a.rows.p[which], p.token * a.rows.ld[which] + p.head * a.rows.head_ld[which] + p.at, f);
-    if (a.cache.rht) {
-        flip_signs(f, a.cache.mask, q);
-        rht32_quad(f, q);
-    }
-    uint32_t most = 0;
+    const int head = blockIdx.y, q = threadIdx.x & 3;
+    float f[PASSES][2][8];
+    int64_t slot[PASSES];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-    const uint32_t byte = scale_byte_from_amax_bits(quad_max_u(most));
-    uint32_t codes = cvt8_rne(f, scale_operand(byte));
-    if (byte == 0xFFu) codes = 0;                          // non-finite block: codes are 0
-    const int64_t page = slot >> a.cache.page_log2;
-    const int offset = (int)(slot & ((1 << a.cache.page_log2) - 1));
-    *(uint32_t*)(a.cache.codes[which] + a.cache.codes_at(page, p.head, offset) + (p.at >> 1)) = codes;
-    if (q == 0)
-        a.cache.scales[which][a.cache.scales_at(page, p.head, offset) + ((int64_t)(p.at >> 5) << a.cache.page_log2)] =
-            (uint8_t)byte;
+    for (int u = 0; u < PASSES; ++u) {
+        const Piece p(a, ((int64_t)blockIdx.x * PASSES + u) * a.per);
+        slot[u] = p.slot;
+        if (p.slot < 0) continue;                          // (the four lanes of a block together)
+#pragma unroll
+        for (int which = 0; which < 2; ++which) load8<BF16>(a.rows.p[which], p.row(a, which, head), f[u][which]);
+    }
+#pragma unroll
+    for (int u = 0; u < PASSES; ++u) {
+        if (slot[u] < 0) continue;
+        const int at = ((int)threadIdx.x - (int)threadIdx.x / a.lanes * a.lanes) * 8;
+        const int64_t page = slot[u] >> a.cache.page_log2;
+        const int offset = (int)slot[u] & ((1 << a.cache.page_log2) - 1);
+        const int64_t codes_at = a.cache.codes_at(page, head, offset) + (at >> 1);
+        const int64_t scale_at = a.cache.scales_at(page, head, offset) + ((int64_t)(at >> 5) << a.cache.page_log2);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float* v = f[u][which];
+            if (a.cache.rht) {
+                flip_signs(v, a.cache.mask, q);
+                rht32_quad(v, q);
+            }
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+            const uint32_t byte = scale_byte_from_amax_bits(quad_max_u(most));
+            uint32_t codes = cvt8_rne(v, scale_operand(byte));
+            if (byte == 0xFFu) codes = 0;                  // non-finite block: codes are 0
+            *(uint32_t*)(a.cache.codes[which] + codes_at) = codes;
+            if (q == 0) a.cache.scales[which][scale_at] = (uint8_t)byte;
+        }
+    }
 }
 
-template <bool BF16>
+// The same way back.
+template <bool BF16, int PASSES>
 __global__ __launch_bounds__(256) void cache_read_kernel(CacheArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int which = a.rows.p[0] ? blockIdx.y : 1;
-    if (i >= a.pieces) return;
-    const Place p(a, i);
-    const int64_t slot = a.slots[p.token];
-    float f[8] = {};
-    if (slot >= 0 && slot < (a.cache.pages << a.cache.page_log2)) {
-        const int64_t page = slot >> a.cache.page_log2;
-        const int offset = (int)(slot & ((1 << a.cache.page_log2) - 1)), q = threadIdx.x & 3;
-        const uint32_t codes =
-            *(const uint32_t*)(a.cache.codes[which] + a.cache.codes_at(page, p.head, offset) + (p.at >> 1));
-        const uint32_t byte = a.cache.scales[which][a.cache.scales_at(page, p.head, offset) +
-                                                    ((int64_t)(p.at >> 5) << a.cache.page_log2)];
-        decode8(codes, scale_operand(byte), f);
-        if (byte == 0xFFu) {
+    const int head = blockIdx.y, q = threadIdx.x & 3;
+    uint32_t codes[PASSES][2], byte[PASSES][2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(0x7FC00000u);
-        }
-        if (a.cache.rht) {
-            rht32_quad(f, q);
-            flip_signs(f, a.cache.mask, q);
+    for (int u = 0; u < PASSES; ++u) {
+        const Piece p(a, ((int64_t)blockIdx.x * PASSES + u) * a.per);
+        if (p.slot < 0) continue;
+        const int64_t codes_at = a.cache.codes_at(p.page(a), head, p.offset(a)) + (p.at >> 1);
+        const int64_t scale_at =
+            a.cache.scales_at(p.page(a), head, p.offset(a)) + ((int64_t)(p.at >> 5) << a.cache.page_log2);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            codes[u][which] = *(const uint32_t*)(a.cache.codes[which] + codes_at);
+            byte[u][which] = a.cache.scales[which][scale_at];
         }
     }
-    store8<BF16>(a.rows.p[which], p.token * a.rows.ld[which] + p.head * a.rows.head_ld[which] + p.at, f);
+#pragma unroll
+    for (int u = 0; u < PASSES; ++u) {
+        const Piece p(a, ((int64_t)blockIdx.x * PASSES + u) * a.per);
+        if (!p.live) continue;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            if (!a.rows.p[which]) continue;
+            float f[8] = {};
+            if (p.slot >= 0) {
+                decode8(codes[u][which], scale_operand(byte[u][which]), f);
+                if (byte[u][which] == 0xFFu) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(0x7FC00000u);
+                }
+                if (a.cache.rht) {
+                    rht32_quad(f, q);
+                    flip_signs(f, a.cache.mask, q);
+                }
+            }
+            store8<BF16>(a.rows.p[which], p.row(a, which, head), f);
+        }
+    }
 }
 
 mx_status check_rows(const CacheView& c, mx_dtype t, int64_t tokens, int64_t ld, int64_t head_ld) {
@@ -152,8 +192,11 @@ CacheArgs cache_args(const CacheView& c, void* k, int64_t k_ld, int64_t k_head_l
     const int64_t row = (int64_t)c.heads * c.dim;
     return CacheArgs{c,
                      {{k, v}, {k_ld ? k_ld : row, v_ld ? v_ld : row}, {k_head_ld ? k_head_ld : c.dim, v_head_ld ? v_head_ld : c.dim}},
-                     slots, tokens * row / 8};
+                     slots, tokens, c.dim / 8, 256 / (c.dim / 8)};
 }
+
+// Passes of a workgroup: two where that leaves the GPU full.
+int passes(const CacheArgs& a) { return ceil_div(a.tokens, a.per) * a.cache.heads > 4096 ? 2 : 1; }
 
 }  // namespace
 
@@ -172,10 +215,17 @@ mx_status mx_cache_write(const mx_cache* cache, const void* k, int64_t k_ld, int
     if (!aligned_to(k, type_bytes(t)) || !aligned_to(v, type_bytes(t)) || !aligned_to(slots, 4)) return MX_ERR_ALIGN;
     const CacheArgs a = cache_args(c, const_cast<void*>(k), k_ld, k_head_ld, const_cast<void*>(v), v_ld, v_head_ld,
                                    tokens, slots);
-    const dim3 grid((uint32_t)ceil_div(a.pieces, 256), 2);
+    const int n = passes(a);
+    const dim3 grid((uint32_t)ceil_div(tokens, (int64_t)n * a.per), c.heads);
+    hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (t == MX_BF16) hipLaunchKernelGGL(cache_write_kernel<true>, grid, dim3(256), 0, (hipStream_t)stream, a);
-    else hipLaunchKernelGGL(cache_write_kernel<false>, grid, dim3(256), 0, (hipStream_t)stream, a);
+    if (t == MX_BF16) {
+        if (n == 2) hipLaunchKernelGGL((cache_write_kernel<true, 2>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((cache_write_kernel<true, 1>), grid, dim3(256), 0, s, a);
+    } else {
+        if (n == 2) hipLaunchKernelGGL((cache_write_kernel<false, 2>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((cache_write_kernel<false, 1>), grid, dim3(256), 0, s, a);
+    }
     return launch_status();
 }
 
@@ -190,10 +240,17 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
     if (!slots) return MX_ERR_NULL;
     if (!aligned_to(k, type_bytes(t)) || !aligned_to(v, type_bytes(t)) || !aligned_to(slots, 4)) return MX_ERR_ALIGN;
     const CacheArgs a = cache_args(c, k, k_ld, k_head_ld, v, v_ld, v_head_ld, tokens, slots);
-    const dim3 grid((uint32_t)ceil_div(a.pieces, 256), k && v ? 2 : 1);
+    const int n = passes(a);
+    const dim3 grid((uint32_t)ceil_div(tokens, (int64_t)n * a.per), c.heads);
+    hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (t == MX_BF16) hipLaunchKernelGGL(cache_read_kernel<true>, grid, dim3(256), 0, (hipStream_t)stream, a);
-    else hipLaunchKernelGGL(cache_read_kernel<false>, grid, dim3(256), 0, (hipStream_t)stream, a);
+    if (t == MX_BF16) {
+        if (n == 2) hipLaunchKernelGGL((cache_read_kernel<true, 2>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((cache_read_kernel<true, 1>), grid, dim3(256), 0, s, a);
+    } else {
+        if (n == 2) hipLaunchKernelGGL((cache_read_kernel<false, 2>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((cache_read_kernel<false, 1>), grid, dim3(256), 0, s, a);
+    }
     return launch_status();
 }
 
