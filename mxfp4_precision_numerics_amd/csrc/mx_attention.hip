@@ -47,6 +47,17 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4v __attribute__((ext_vector_type(4), aligned(2)));
 
+// Accesses through pointers that the compiler cannot tell to be ones to global
+// memory.  (A flat access makes it wait for every load under way.)
+template <class T>
+__device__ __forceinline__ T load_global(const void* p) {
+    return *(const __attribute__((address_space(1))) T*)p;
+}
+template <class T>
+__device__ __forceinline__ void store_global(void* p, T v) {
+    *(__attribute__((address_space(1))) T*)p = v;
+}
+
 // ---------------------------------------------------------------------------
 // The work and its shares.
 //
@@ -76,12 +87,12 @@ __device__ __forceinline__ Seq load_seq(const AttentionArgs& a, int s) {
     Seq q;
     int64_t b = s, e = s + 1;
     if (a.q_offsets) {
-        b = min(max((int64_t)a.q_offsets[s], (int64_t)0), a.tokens);
-        e = min(max((int64_t)a.q_offsets[s + 1], b), a.tokens);
+        b = min(max((int64_t)load_global<int32_t>(a.q_offsets + s), (int64_t)0), a.tokens);
+        e = min(max((int64_t)load_global<int32_t>(a.q_offsets + s + 1), b), a.tokens);
     }
     q.row0 = b;
     q.n = (int)(e - b);
-    q.len = (int)min(max((int64_t)a.lengths[s], (int64_t)0), a.capacity);
+    q.len = (int)min(max((int64_t)load_global<int32_t>(a.lengths + s), (int64_t)0), a.capacity);
     return q;
 }
 
@@ -162,6 +173,13 @@ struct Cut {
     Segment seg;
     int count, pad;           // 0: there is none
     int64_t slot;
+
+    __device__ __forceinline__ void write(Cut* to) const {
+        uint32_t w[sizeof(Cut) / 4];
+        __builtin_memcpy(w, this, sizeof(Cut));
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Cut) / 4); ++i) store_global((uint32_t*)to + i, w[i]);
+    }
 };
 static_assert(sizeof(Cut) % 16 == 0, "the parts follow the cuts, 16-byte aligned");
 
@@ -285,7 +303,7 @@ template <bool BF16>
 __device__ __forceinline__ void finish(const AttentionArgs& a, const Row& r, bool live, int d, float* o, float top,
                                        float sum) {
     if (a.sinks) {
-        const float sink = live ? a.sinks[r.head] * LOG2E : 0.0f, m = fmaxf(top, sink);
+        const float sink = live ? load_global<float>(a.sinks + r.head) * LOG2E : 0.0f, m = fmaxf(top, sink);
         const float safe = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(top - safe);
         sum = sum * f + __builtin_amdgcn_exp2f(sink - safe);
         top = m;
@@ -307,27 +325,27 @@ __device__ __forceinline__ void finish(const AttentionArgs& a, const Row& r, boo
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16_rne(o[2 * i]) | f32_to_bf16_rne(o[2 * i + 1]) << 16;
-        *(u32x4v*)((uint16_t*)a.out + at) = (u32x4v){u[0], u[1], u[2], u[3]};
+        store_global((uint16_t*)a.out + at, (u32x4v){u[0], u[1], u[2], u[3]});
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            *(u32x4v*)((float*)a.out + at + 4 * i) =
-                (u32x4v){__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                         __float_as_uint(o[4 * i + 3])};
+            store_global((float*)a.out + at + 4 * i,
+                         (u32x4v){__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                                  __float_as_uint(o[4 * i + 3])});
     }
     if (a.lse && d == 0)
-        a.lse[r.token * a.q_heads + r.head] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2;
+        store_global(a.lse + r.token * a.q_heads + r.head, sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2);
 }
 
 // A part in the workspace: sums [rows][32 NB], maxima [rows], sums of p [rows].
-template <int NB, int NT>
+template <int NB, int ROWS>
 struct Part {
-    static constexpr int ROWS = 16 * NT, FLOATS = ROWS * (32 * NB + 2);
+    static constexpr int FLOATS = ROWS * (32 * NB + 2);
     float* p;
     __device__ __forceinline__ Part(const AttentionArgs& a, int64_t i) : p(a.parts + i * FLOATS) {}
     __device__ __forceinline__ float* row(int c) const { return p + c * 32 * NB; }
-    __device__ __forceinline__ float& top(int c) const { return p[ROWS * 32 * NB + c]; }
-    __device__ __forceinline__ float& sum(int c) const { return p[ROWS * 32 * NB + ROWS + c]; }
+    __device__ __forceinline__ float* top(int c) const { return p + ROWS * 32 * NB + c; }
+    __device__ __forceinline__ float* sum(int c) const { return p + ROWS * 32 * NB + ROWS + c; }
 };
 
 __device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
@@ -355,7 +373,7 @@ __device__ __forceinline__ void finish_row(const AttentionArgs& a, const Row& r,
     constexpr int N = 8 * NB;
     float f = 1.0f;
     if (a.sinks) {
-        const float sink = live ? a.sinks[r.head] * LOG2E : 0.0f, m = fmaxf(top, sink);
+        const float sink = live ? load_global<float>(a.sinks + r.head) * LOG2E : 0.0f, m = fmaxf(top, sink);
         const float safe = m == -__builtin_inff() ? 0.0f : m;
         f = __builtin_amdgcn_exp2f(top - safe);
         sum = sum * f + __builtin_amdgcn_exp2f(sink - safe);
@@ -389,17 +407,17 @@ __device__ __forceinline__ void finish_row(const AttentionArgs& a, const Row& r,
             uint32_t u[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) u[k] = pack(o[i + 2 * k], o[i + 2 * k + 1]);
-            *(u32x4v*)((uint16_t*)a.out + at + i) = (u32x4v){u[0], u[1], u[2], u[3]};
+            store_global((uint16_t*)a.out + at + i, (u32x4v){u[0], u[1], u[2], u[3]});
         } else {
 #pragma unroll
             for (int k = 0; k < 8; k += 4)
-                *(u32x4v*)((float*)a.out + at + i + k) =
-                    (u32x4v){__float_as_uint(o[i + k]), __float_as_uint(o[i + k + 1]), __float_as_uint(o[i + k + 2]),
-                             __float_as_uint(o[i + k + 3])};
+                store_global((float*)a.out + at + i + k,
+                             (u32x4v){__float_as_uint(o[i + k]), __float_as_uint(o[i + k + 1]), __float_as_uint(o[i + k + 2]),
+                                      __float_as_uint(o[i + k + 3])});
         }
     }
     if (a.lse && d == 0)
-        a.lse[r.token * a.q_heads + r.head] = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2;
+        store_global(a.lse + r.token * a.q_heads + r.head, sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2);
 }
 
 // The other value of a row of 16 lanes' neighbour (16 lanes on, then 32): of
@@ -467,20 +485,18 @@ struct Shared {
 template <int NB, bool EXACT>
 struct Lane {
     const uint8_t *k, *ks, *v, *vs;
-    bool k_there[NB == 8 ? 2 : 1];        // the row reaches that far (its halves, NB = 8)
+    bool second;                          // NB = 8: the row reaches the lane's second half
 
+    // What a lane would read past the row's end it reads from its begin instead.
+    // Of K that meets elements of q that are 0, and is not finite only where the
+    // key's score is not anyway; of V it makes elements that nobody writes.
+    __device__ __forceinline__ int half(int h) const { return EXACT || second ? h : 0; }
     __device__ __forceinline__ Lane(const AttentionArgs& a, int head, int col, int g) {
         const int shift = a.cache.page_log2, row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1;
         const int blocks = EXACT ? NB : a.cache.dim >> 5;
         const int c = EXACT || col * NB < row_bytes ? col : 0;
-        int piece = 4 * NB * g;                            // bytes into a row
-        if constexpr (NB == 2) {
-            k_there[0] = EXACT || piece < row_bytes;
-        } else {
-#pragma unroll
-            for (int h = 0; h < NB / 4; ++h) k_there[h] = EXACT || piece + 16 * h < row_bytes;
-        }
-        if (!k_there[0]) piece = 0;
+        const int piece = EXACT || 4 * NB * g < row_bytes ? 4 * NB * g : 0;        // bytes into a row
+        second = piece + 16 < row_bytes;
         const int64_t codes = ((int64_t)head << shift) * row_bytes, scales = (int64_t)head * blocks << shift;
         k = a.cache.codes[0] + codes + (col & 3) * row_bytes + piece;
         ks = a.cache.scales[0] + scales + ((int64_t)(piece >> 4) << shift);
@@ -514,14 +530,14 @@ __device__ __forceinline__ void load_queries(const AttentionArgs& a, const Segme
         float f[8] = {};
         if (live) {
             if constexpr (BF16) {
-                const u32x4v w = *(const u32x4v*)((const uint16_t*)a.q + from);
+                const u32x4v w = load_global<u32x4v>((const uint16_t*)a.q + from);
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) { f[2 * e] = bf16lo(u[e]); f[2 * e + 1] = bf16hi(u[e]); }
             } else {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const u32x4v w = *(const u32x4v*)((const float*)a.q + from + 4 * e);
+                    const u32x4v w = load_global<u32x4v>((const float*)a.q + from + 4 * e);
                     f[4 * e] = __uint_as_float(w.x);
                     f[4 * e + 1] = __uint_as_float(w.y);
                     f[4 * e + 2] = __uint_as_float(w.z);
@@ -630,26 +646,23 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const uint2 w = *(const uint2*)(codes + 4 * t * row_bytes);
-                    kc[j][t][0] = my.k_there[0] ? w.x : 0u;
-                    kc[j][t][1] = my.k_there[0] ? w.y : 0u;
+                    kc[j][t][0] = w.x;
+                    kc[j][t][1] = w.y;
                 }
                 ks[j][0] = *(const uint2*)scales;
-                if (!my.k_there[0]) ks[j][0] = make_uint2(0u, 0u);
             } else {
 #pragma unroll
                 for (int h = 0; h < NB / 4; ++h) {
-                    const bool there = my.k_there[h];
-                    const int more = !EXACT && !there ? 0 : h;
+                    const int more = my.half(h);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const uint4 w = *(const uint4*)(codes + 4 * t * row_bytes + 16 * more);
-                        kc[j][t][4 * h] = there ? w.x : 0u;
-                        kc[j][t][4 * h + 1] = there ? w.y : 0u;
-                        kc[j][t][4 * h + 2] = there ? w.z : 0u;
-                        kc[j][t][4 * h + 3] = there ? w.w : 0u;
+                        kc[j][t][4 * h] = w.x;
+                        kc[j][t][4 * h + 1] = w.y;
+                        kc[j][t][4 * h + 2] = w.z;
+                        kc[j][t][4 * h + 3] = w.w;
                     }
                     ks[j][h] = *(const uint2*)(scales + (more << shift));
-                    if (!there) ks[j][h] = make_uint2(0u, 0u);
                 }
             }
         };
@@ -672,13 +685,18 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 
         int unit = unit0 + wave, pages = 0, next_pages = 0;
         if (unit < units) {
-            pages = checked(look_up(unit));
+            // (all in the loop's own order, so that it waits for the oldest loads alone)
+            pages = look_up(unit);
+            next_pages = look_up(min(unit + WAVES, units - 1));
+            __builtin_amdgcn_sched_barrier(0);
+            pages = checked(pages);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 load_k(unit, j, page_of(pages, 4 * j + (col >> 2)));
+                __builtin_amdgcn_sched_barrier(0);
                 load_v(unit, j, page_of(pages, 4 * j + g));
+                __builtin_amdgcn_sched_barrier(0);
             }
-            next_pages = look_up(min(unit + WAVES, units - 1));
         }
         for (; unit < units; unit += WAVES) {
             const int key0 = UNIT * unit, ahead = min(unit + WAVES, units - 1);
@@ -828,7 +846,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         __syncthreads();                                   // (also: nobody reads the queries any more)
         const AttentionArgs b = arguments();
         const bool complete = at == seg.start && unit1 == seg.end;
-        const Part<NB, NT> part(b, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
+        const Part<NB, 16 * NT> part(b, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
         constexpr int SIDES = 32 * NB / Sh::SIDE;
         float* o = (float*)sh.data;
 #pragma unroll
@@ -871,11 +889,11 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                         finish<BF16>(b, r, live, d, v, most, all);
                     } else if (live) {
                         float* to_part = part.row(16 * n + c) + d;
-                        *(f32x4*)to_part = (f32x4){v[0], v[1], v[2], v[3]};
-                        *(f32x4*)(to_part + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+                        store_global(to_part, (f32x4){v[0], v[1], v[2], v[3]});
+                        store_global(to_part + 4, (f32x4){v[4], v[5], v[6], v[7]});
                         if (d == 0) {
-                            part.top(16 * n + c) = most;
-                            part.sum(16 * n + c) = all;
+                            store_global(part.top(16 * n + c), most);
+                            store_global(part.sum(16 * n + c), all);
                         }
                     }
                 }
@@ -884,10 +902,12 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         }
         const int64_t next = seg.start + (seg.end - seg.begin);
         if (next > stop && seg.start >= begin && tid == 0) {
-            Cut& cut = b.cuts[blockIdx.x];
+            Cut cut;
             cut.seg = seg;
             cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
             cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
+            cut.pad = 0;
+            cut.write(b.cuts + blockIdx.x);
         }
         at = next;
         if (at >= stop) return;
@@ -1013,22 +1033,19 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
             const uint8_t* scales = in_page(my.ks, page_k, a.scale_page) + ok + 4 * t_in + (col & 3);
             if constexpr (NB == 2) {
                 const uint2 w = *(const uint2*)codes;
-                kc[0] = my.k_there[0] ? w.x : 0u;
-                kc[1] = my.k_there[0] ? w.y : 0u;
+                kc[0] = w.x;
+                kc[1] = w.y;
                 kb[0] = *scales;
-                if (!my.k_there[0]) kb[0] = 0;
             } else {
 #pragma unroll
                 for (int h = 0; h < NB / 4; ++h) {
-                    const bool there = my.k_there[h];
-                    const int more = !EXACT && !there ? 0 : h;
+                    const int more = my.half(h);
                     const uint4 w = *(const uint4*)(codes + 16 * more);
-                    kc[4 * h] = there ? w.x : 0u;
-                    kc[4 * h + 1] = there ? w.y : 0u;
-                    kc[4 * h + 2] = there ? w.z : 0u;
-                    kc[4 * h + 3] = there ? w.w : 0u;
+                    kc[4 * h] = w.x;
+                    kc[4 * h + 1] = w.y;
+                    kc[4 * h + 2] = w.z;
+                    kc[4 * h + 3] = w.w;
                     kb[h] = scales[more << shift];
-                    if (!there) kb[h] = 0;
                 }
             }
             const int ov = min(UNIT * unit + 32 * j_in + 8 * g, last_group) & ((1 << shift) - 1);
@@ -1087,12 +1104,14 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
         __syncthreads();                                   // the queries are in registers: their place is free
         int pages = 0, pages1 = 0, pages2 = 0;             // of this unit, the next, the one after
         if (unit0 < units) {
-            pages = checked(look_up(unit0));
+            pages = look_up(unit0);
+            pages1 = look_up(min(unit0 + 1, units - 1));
+            pages2 = look_up(min(unit0 + 2, units - 1));
+            pages = checked(pages);
+            pages1 = checked(pages1);
             load(unit0, pages);
-            pages1 = checked(look_up(min(unit0 + 1, units - 1)));
             store(unit0 & 1);
             load(min(unit0 + 1, units - 1), pages1);
-            pages2 = look_up(min(unit0 + 2, units - 1));
         }
         for (int unit = unit0; unit < units; ++unit) {
             const int buf = unit & 1, key0 = UNIT * unit;
@@ -1195,7 +1214,7 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
 
         const AttentionArgs b = arguments();
         const bool complete = at == seg.start && unit1 == seg.end;
-        float* part = b.parts + (2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1)) * (ROWS_TILE * (32 * NB + 2));
+        const Part<NB, ROWS_TILE> part(b, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int c = wave * ROWS_WAVE + 16 * n + col;
@@ -1211,21 +1230,23 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
             if (complete) {
                 finish_row<NB, BF16>(b, r, live, 8 * NB * g, o, top[n], sum[n]);
             } else if (live) {
-                float* to = part + c * 32 * NB + 8 * NB * g;
+                float* to = part.row(c) + 8 * NB * g;
 #pragma unroll
-                for (int i = 0; i < 8 * NB; i += 4) *(f32x4*)(to + i) = (f32x4){o[i], o[i + 1], o[i + 2], o[i + 3]};
+                for (int i = 0; i < 8 * NB; i += 4) store_global(to + i, (f32x4){o[i], o[i + 1], o[i + 2], o[i + 3]});
                 if (g == 0) {
-                    part[ROWS_TILE * 32 * NB + c] = top[n];
-                    part[ROWS_TILE * 32 * NB + ROWS_TILE + c] = sum[n];
+                    store_global(part.top(c), top[n]);
+                    store_global(part.sum(c), sum[n]);
                 }
             }
         }
         const int64_t next = seg.start + (seg.end - seg.begin);
         if (next > stop && seg.start >= begin && tid == 0) {
-            Cut& cut = b.cuts[blockIdx.x];
+            Cut cut;
             cut.seg = seg;
             cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
             cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
+            cut.pad = 0;
+            cut.write(b.cuts + blockIdx.x);
         }
         at = next;
         if (at >= stop) return;
@@ -1254,9 +1275,9 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int i = min(i0 + k * GROUPS, cut.count - 1);
-            const Part<NB, NT> part(a, i == 0 ? cut.slot : 2 * (int64_t)(blockIdx.x + i));
-            t[k] = part.top(c);                            // (rows that do not exist hold anything and go nowhere)
-            l[k] = part.sum(c);
+            const Part<NB, 16 * NT> part(a, i == 0 ? cut.slot : 2 * (int64_t)(blockIdx.x + i));
+            t[k] = *part.top(c);                           // (rows that do not exist hold anything and go nowhere)
+            l[k] = *part.sum(c);
             x[k] = *(const f32x4*)(part.row(c) + d);
             y[k] = *(const f32x4*)(part.row(c) + d + 4);
         }
@@ -1323,7 +1344,7 @@ Shape shape_of(const CacheView& c, bool bf16, int64_t tokens, int q_heads, int m
     const int64_t most = max_queries > 0 ? min((int64_t)max_queries, tokens) : tokens;
     s.nb = c.dim <= 64 ? 2 : c.dim <= 128 ? 4 : 8;
     const int64_t rows = most * group;
-    s.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+    s.nt = rows <= 16 ? 1 : rows <= 32 && s.nb < 8 ? 2 : 0;    // (32 rows of 256 elements do not fit the registers)
     const int r = s.nt ? 16 * s.nt : ROWS_TILE;
     s.tile_heads = min(group, r);
     s.head_tiles = (group + r - 1) / r;
@@ -1371,7 +1392,7 @@ template <int NB>
 void launch(const AttentionArgs& a, int nt, bool bf16, int shares, hipStream_t s) {
     if (nt == 0) launch<NB, 0>(a, bf16, shares, s);
     else if (nt == 1) launch<NB, 1>(a, bf16, shares, s);
-    else launch<NB, 2>(a, bf16, shares, s);
+    else if constexpr (NB < 8) launch<NB, 2>(a, bf16, shares, s);
 }
 
 mx_status check_pitches(int64_t ld, int64_t head_ld, int dim) {
