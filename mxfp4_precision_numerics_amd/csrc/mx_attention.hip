@@ -41,6 +41,7 @@ constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
 constexpr int UNIT = 64;              // keys that a wave takes at a time
 constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
 constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least
+constexpr int WHOLE_UNITS = 16;       // of a segment that is not cut
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -67,9 +68,10 @@ __device__ __forceinline__ void store_global(void* p, T v) {
 // All segments' units, in the order sequence, cache head (and part of its
 // group), tile, key, are one long line that the workgroups cut into equal
 // shares, whatever the lengths are: every workgroup finds its share from the
-// lengths themselves.  A segment that lies in one share is finished there; of
-// one that is cut every share leaves its part (sums, maxima) in the workspace,
-// two parts a workgroup at most, and a second launch joins them.
+// lengths themselves.  A segment that lies in one share, or is short, is
+// finished there; of one that is cut every share leaves its part (sums, maxima)
+// in the workspace, two parts a workgroup at most, and a second launch joins
+// them.
 // ---------------------------------------------------------------------------
 // A value that every lane has, for the scalar registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -123,6 +125,7 @@ __device__ __forceinline__ int64_t sum_floor(int64_t y, int q_log2) {      // ov
     return ((w * (w - 1) >> 1) << q_log2) + r * w;
 }
 __device__ __forceinline__ int64_t units_before(const AttentionArgs& a, const Seq& q, int x) {
+    if (x == 0) return 0;
     if (!a.causal) return (int64_t)x * end_unit(a, q, 0);
     const int64_t at = q.len - q.n, low = at - a.window + 1;
     int64_t units;
@@ -154,10 +157,12 @@ __device__ __forceinline__ int64_t units_of(const AttentionArgs& a, const Seq& q
     return units_before(a, q, tiles - 1) + end_unit(a, q, tiles - 1) - first_unit(a, q, tiles - 1);
 }
 
-// Where unit `at` of the line lies; the line's length.
+// The line's length, and where one unit of it lies: each thread has a stretch
+// of sequences.
 struct Line {
-    int64_t before[WAVES * 64 + 1];       // units before each thread's stretch of sequences
-    int64_t wave_units[WAVES];
+    int64_t wave_units[WAVES], total;
+    int64_t from;             // units before the stretch that holds it
+    int stretch;
 };
 
 struct Segment {
@@ -165,6 +170,10 @@ struct Segment {
     int s, head, tile;        // sequence, cache head * head_tiles + part of its group, tile
     int begin, end;           // its units (of keys)
     int64_t start;            // its first unit's place in the line
+
+    // Whether it is done by the share in which it starts: cutting a short one
+    // and joining it takes longer than its last steps.
+    __device__ __forceinline__ bool whole() const { return end - begin <= WHOLE_UNITS; }
 };
 
 // What a share leaves about the segment that it began and did not finish:
@@ -183,10 +192,12 @@ struct Cut {
 };
 static_assert(sizeof(Cut) % 16 == 0, "the parts follow the cuts, 16-byte aligned");
 
-__device__ __forceinline__ void measure_line(const AttentionArgs& a, Line& line) {
-    const int tid = threadIdx.x, per = (a.seqs + WAVES * 64 - 1) / (WAVES * 64);
+// Measures the line, and finds the stretch of unit share * (what a share has):
+// returns that unit's place, not less than the line's length if there is none.
+__device__ __forceinline__ int64_t measure_line(const AttentionArgs& a, Line& line, int64_t& per) {
+    const int tid = threadIdx.x, each = (a.seqs + WAVES * 64 - 1) / (WAVES * 64);
     int64_t mine = 0;
-    for (int s = tid * per; s < min((tid + 1) * per, a.seqs); ++s) mine += units_of(a, load_seq(a, s));
+    for (int s = tid * each; s < min((tid + 1) * each, a.seqs); ++s) mine += units_of(a, load_seq(a, s));
     mine *= a.line_heads;
     int64_t sum = mine;
 #pragma unroll
@@ -196,11 +207,23 @@ __device__ __forceinline__ void measure_line(const AttentionArgs& a, Line& line)
     }
     if ((tid & 63) == 63) line.wave_units[tid >> 6] = sum;
     __syncthreads();
-    int64_t base = 0;
-    for (int w = 0; w < tid >> 6; ++w) base += line.wave_units[w];
-    line.before[tid] = base + sum - mine;
-    if (tid == WAVES * 64 - 1) line.before[WAVES * 64] = base + sum;
+    int64_t base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const int64_t u = line.wave_units[w];
+        if (w < tid >> 6) base += u;
+        total += u;
+    }
+    total = uniform(total);
+    per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MIN_UNITS);
+    const int64_t at = blockIdx.x * per, from = base + sum - mine;
+    if (from <= at && at < from + mine) {
+        line.from = from;
+        line.stretch = tid;
+    }
+    if (tid == 0) line.total = total;
     __syncthreads();
+    return at;
 }
 
 __device__ __forceinline__ Seq load_uniform_seq(const AttentionArgs& a, int s) {
@@ -216,18 +239,12 @@ __device__ __forceinline__ void set_tile(const AttentionArgs& a, Segment& g) {
     g.end = end_unit(a, g.seq, g.tile);
 }
 
-// The segment that holds unit `at`, 0 <= at < the line's length.
+// The segment that holds unit `at`, which measure_line found.
 __device__ __forceinline__ Segment locate(const AttentionArgs& a, const Line& line, int64_t at) {
     Segment g;
-    int lo = 0, hi = WAVES * 64 - 1;                       // the last stretch that starts at or before it
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (uniform(line.before[mid]) <= at) lo = mid;
-        else hi = mid - 1;
-    }
-    const int per = (a.seqs + WAVES * 64 - 1) / (WAVES * 64);
-    int64_t from = uniform(line.before[lo]), units;
-    g.s = lo * per;
+    int lo, hi;
+    int64_t from = uniform(line.from), units;
+    g.s = uniform(line.stretch) * ((a.seqs + WAVES * 64 - 1) / (WAVES * 64));
     for (;; ++g.s) {
         g.seq = load_uniform_seq(a, g.s);
         units = units_of(a, g.seq);
@@ -518,55 +535,74 @@ __device__ __forceinline__ bool any_odd(uint2 w) {
 // Whether a row that sees the keys low .. last sees key from + i.
 __device__ __forceinline__ bool sees(int last, int low, int from, int i) { return i <= last - from && i >= low - from; }
 
-// A tile's queries into LDS, QT terms of bf16, transformed where the cache is;
-// 0 where there is none.  The whole workgroup calls.
+// A tile's queries on their way to LDS: eight elements of N rows a thread.
+// load() sends for them; store() puts them down as QT terms of bf16,
+// transformed where the cache is, 0 where there is no row.  The whole workgroup
+// calls.
 template <int NB, int ROWS, bool BF16, int QT>
-__device__ __forceinline__ void load_queries(const AttentionArgs& a, const Segment& seg, __bf16* to, int pitch) {
-    for (int i = threadIdx.x; i < ROWS * 4 * NB; i += WAVES * 64) {
-        const int c = i / (4 * NB), d = i % (4 * NB) * 8;
-        Row r;
-        const bool live = row_of(a, seg, c, r) && d < a.cache.dim;
-        const int64_t from = r.token * a.q_ld + r.head * a.q_head_ld + d;
-        float f[8] = {};
-        if (live) {
+struct Queries {
+    static constexpr int ITEMS = ROWS * 4 * NB, N = (ITEMS + WAVES * 64 - 1) / (WAVES * 64);
+    u32x4v w[N][BF16 ? 1 : 2];
+
+    __device__ __forceinline__ void load(const AttentionArgs& a, const Segment& seg) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = threadIdx.x + k * WAVES * 64, c = i / (4 * NB), d = i % (4 * NB) * 8;
+            Row r;
+            const bool live = row_of(a, seg, c, r) && d < a.cache.dim && i < ITEMS;
+            const int64_t from = r.token * a.q_ld + r.head * a.q_head_ld + d;
+#pragma unroll
+            for (int e = 0; e < (BF16 ? 1 : 2); ++e) {
+                w[k][e] = (u32x4v){0, 0, 0, 0};
+                if (live)
+                    w[k][e] = BF16 ? load_global<u32x4v>((const uint16_t*)a.q + from)
+                                   : load_global<u32x4v>((const float*)a.q + from + 4 * e);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const AttentionArgs& a, __bf16* to, int pitch) const {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = threadIdx.x + k * WAVES * 64, c = i / (4 * NB), d = i % (4 * NB) * 8;
+            if (i >= ITEMS) break;
+            float f[8];
             if constexpr (BF16) {
-                const u32x4v w = load_global<u32x4v>((const uint16_t*)a.q + from);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t u[4] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) { f[2 * e] = bf16lo(u[e]); f[2 * e + 1] = bf16hi(u[e]); }
             } else {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const u32x4v w = load_global<u32x4v>((const float*)a.q + from + 4 * e);
-                    f[4 * e] = __uint_as_float(w.x);
-                    f[4 * e + 1] = __uint_as_float(w.y);
-                    f[4 * e + 2] = __uint_as_float(w.z);
-                    f[4 * e + 3] = __uint_as_float(w.w);
+                    const u32x4v& x = w[k][BF16 ? 0 : e];
+                    f[4 * e] = __uint_as_float(x.x);
+                    f[4 * e + 1] = __uint_as_float(x.y);
+                    f[4 * e + 2] = __uint_as_float(x.z);
+                    f[4 * e + 3] = __uint_as_float(x.w);
                 }
             }
-        }
-        if (a.cache.rht) {
-            const uint32_t m = a.cache.mask >> (d & 31);
+            if (a.cache.rht) {
+                const uint32_t m = a.cache.mask >> (d & 31);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(__float_as_uint(f[e]) ^ (m >> e << 31));
-            rht32_quad(f, (d >> 3) & 3);
-        }
-        uint32_t u[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = pack(f[2 * e], f[2 * e + 1]);
-        *(uint4*)(to + c * pitch + d) = make_uint4(u[0], u[1], u[2], u[3]);
-        if constexpr (QT == 2) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // (an infinite element has no rest)
-                const float lo = bf16lo(u[e]), hi = bf16hi(u[e]);
-                w[e] = pack(__builtin_isinf(lo) ? 0.0f : f[2 * e] - lo, __builtin_isinf(hi) ? 0.0f : f[2 * e + 1] - hi);
+                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(__float_as_uint(f[e]) ^ (m >> e << 31));
+                rht32_quad(f, (d >> 3) & 3);
             }
-            *(uint4*)(to + (ROWS + c) * pitch + d) = make_uint4(w[0], w[1], w[2], w[3]);
+            uint32_t u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = pack(f[2 * e], f[2 * e + 1]);
+            *(uint4*)(to + c * pitch + d) = make_uint4(u[0], u[1], u[2], u[3]);
+            if constexpr (QT == 2) {
+                uint32_t v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // (an infinite element has no rest)
+                    const float lo = bf16lo(u[e]), hi = bf16hi(u[e]);
+                    v[e] = pack(__builtin_isinf(lo) ? 0.0f : f[2 * e] - lo, __builtin_isinf(hi) ? 0.0f : f[2 * e + 1] - hi);
+                }
+                *(uint4*)(to + (ROWS + c) * pitch + d) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
         }
     }
-}
+};
 
 template <int NB, int NT, bool EXACT, bool BF16, int QT, int PT>
 __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attention_kernel(AttentionArgs a) {
@@ -580,47 +616,23 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
     const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1;
     const float scale = a.scale;
 
-    measure_line(a, sh.line);
-    const int64_t total = uniform(sh.line.before[WAVES * 64]);
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MIN_UNITS);
-    const int64_t begin = blockIdx.x * per, stop = min(begin + per, total);
+    int64_t per;
+    const int64_t begin = measure_line(a, sh.line, per), total = uniform(sh.line.total), stop = min(begin + per, total);
     if (tid == 0) a.cuts[blockIdx.x].count = 0;
     if (begin >= total) return;
     Segment seg = locate(a, sh.line, begin);
+    int64_t at = begin;
+    if (seg.start < begin && seg.whole()) {                // the share before has all of it
+        at = seg.start + seg.end - seg.begin;
+        if (at >= stop) return;
+        next_segment(a, seg);
+    }
 
-    for (int64_t at = begin;;) {
+    for (;;) {
         const int head = seg.head / a.head_tiles;          // of the cache
         const int rows = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2)) * a.tile_heads;
-        __syncthreads();
-        load_queries<NB, 16 * NT, BF16, QT>(arguments(), seg, (__bf16*)sh.data, Sh::PITCH);
-        __syncthreads();
-
-        // the keys that each of the lane's rows sees, and those that all see
-        int last[NT], low[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            Row r;
-            const bool live = row_of(a, seg, 16 * n + col, r);
-            const int pos = seg.seq.len - seg.seq.n + r.query;
-            last[n] = !live ? -1 : a.causal ? pos : seg.seq.len - 1;
-            low[n] = a.window ? pos - a.window + 1 : 0;
-        }
-        const int pos0 = seg.seq.len - seg.seq.n + (seg.tile << a.tile_log2);
-        const int all_to = a.causal ? pos0 : seg.seq.len - 1;
-        const int all_from = a.window ? pos0 + rows / a.tile_heads - 1 - a.window + 1 : 0;
-
-        f32x4 acc[NT][M];
-        float top[NT], sum[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            top[n] = -__builtin_inff();
-            sum[n] = 0.0f;
-#pragma unroll
-            for (int m = 0; m < M; ++m) acc[n][m] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        }
-
         const int unit0 = seg.begin + (int)(at - seg.start);
-        const int unit1 = (int)min((int64_t)seg.end, seg.begin + (stop - seg.start));
+        const int unit1 = seg.whole() ? seg.end : (int)min((int64_t)seg.end, seg.begin + (stop - seg.start));
         // (a sequence without keys has no pages to look at)
         const int units = seg.seq.len == 0 ? 0 : unit1;
         const int32_t* table = a.table + seg.s * a.table_ld;
@@ -684,20 +696,53 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         };
 
         int unit = unit0 + wave, pages = 0, next_pages = 0;
+        // The first keys and the queries are on their way at the same time.  (The loads that the loop needs first come
+        // first, so that it waits for them alone.)
+        Queries<NB, 16 * NT, BF16, QT> queries;
         if (unit < units) {
-            // (all in the loop's own order, so that it waits for the oldest loads alone)
             pages = look_up(unit);
             next_pages = look_up(min(unit + WAVES, units - 1));
-            __builtin_amdgcn_sched_barrier(0);
+        }
+        queries.load(arguments(), seg);
+        __builtin_amdgcn_sched_barrier(0);
+        if (unit < units) {
             pages = checked(pages);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                load_k(unit, j, page_of(pages, 4 * j + (col >> 2)));
-                __builtin_amdgcn_sched_barrier(0);
-                load_v(unit, j, page_of(pages, 4 * j + g));
-                __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int j = 0; j < 2; ++j) load_k(unit, j, page_of(pages, 4 * j + (col >> 2)));
         }
+        __syncthreads();                                   // (the last segment's rows have been read from the same place)
+        queries.store(arguments(), (__bf16*)sh.data, Sh::PITCH);
+        __builtin_amdgcn_sched_barrier(0);
+        if (unit < units) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) load_v(unit, j, page_of(pages, 4 * j + g));
+        }
+        __syncthreads();
+
+        // the keys that each of the lane's rows sees, and those that all see
+        int last[NT], low[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            Row r;
+            const bool live = row_of(a, seg, 16 * n + col, r);
+            const int pos = seg.seq.len - seg.seq.n + r.query;
+            last[n] = !live ? -1 : a.causal ? pos : seg.seq.len - 1;
+            low[n] = a.window ? pos - a.window + 1 : 0;
+        }
+        const int pos0 = seg.seq.len - seg.seq.n + (seg.tile << a.tile_log2);
+        const int all_to = a.causal ? pos0 : seg.seq.len - 1;
+        const int all_from = a.window ? pos0 + rows / a.tile_heads - 1 - a.window + 1 : 0;
+
+        f32x4 acc[NT][M];
+        float top[NT], sum[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            top[n] = -__builtin_inff();
+            sum[n] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) acc[n][m] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        }
+
         for (; unit < units; unit += WAVES) {
             const int key0 = UNIT * unit, ahead = min(unit + WAVES, units - 1);
             const bool whole = key0 + UNIT - 1 <= all_to && key0 >= all_from && !__any(pages < 0);
@@ -901,7 +946,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
             }
         }
         const int64_t next = seg.start + (seg.end - seg.begin);
-        if (next > stop && seg.start >= begin && tid == 0) {
+        if (unit1 < seg.end && seg.start >= begin && tid == 0) {
             Cut cut;
             cut.seg = seg;
             cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
@@ -957,21 +1002,30 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
     const int row_bytes = EXACT ? 16 * NB : a.cache.dim >> 1;
     const float scale = a.scale;
 
-    measure_line(a, sh.line);
-    const int64_t total = uniform(sh.line.before[WAVES * 64]);
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MIN_UNITS);
-    const int64_t begin = blockIdx.x * per, stop = min(begin + per, total);
+    int64_t per;
+    const int64_t begin = measure_line(a, sh.line, per), total = uniform(sh.line.total), stop = min(begin + per, total);
     if (tid == 0) a.cuts[blockIdx.x].count = 0;
     if (begin >= total) return;
     Segment seg = locate(a, sh.line, begin);
+    int64_t at = begin;
+    if (seg.start < begin && seg.whole()) {                // the share before has all of it
+        at = seg.start + seg.end - seg.begin;
+        if (at >= stop) return;
+        next_segment(a, seg);
+    }
 
-    for (int64_t at = begin;;) {
+    for (;;) {
         const int head = seg.head / a.head_tiles;
         const int tokens = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2));
         const int rows = tokens * a.tile_heads;
-        __syncthreads();
-        load_queries<NB, ROWS_TILE, BF16, QT>(arguments(), seg, &sh.q[0][0][0], Sh::PITCH);
-        __syncthreads();
+        {
+            const AttentionArgs b = arguments();
+            Queries<NB, ROWS_TILE, BF16, QT> queries;
+            queries.load(b, seg);
+            __syncthreads();
+            queries.store(b, &sh.q[0][0][0], Sh::PITCH);
+            __syncthreads();
+        }
         bf16x8 qf[QT][NT][NB];
 #pragma unroll
         for (int y = 0; y < QT; ++y)
@@ -1011,7 +1065,7 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
         }
 
         const int unit0 = seg.begin + (int)(at - seg.start);
-        const int unit1 = (int)min((int64_t)seg.end, seg.begin + (stop - seg.start));
+        const int unit1 = seg.whole() ? seg.end : (int)min((int64_t)seg.end, seg.begin + (stop - seg.start));
         const int units = seg.seq.len == 0 ? unit0 : unit1;
         const int32_t* table = a.table + seg.s * a.table_ld;
         const int last_group = (seg.seq.len - 1) & ~7;
@@ -1240,7 +1294,7 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
             }
         }
         const int64_t next = seg.start + (seg.end - seg.begin);
-        if (next > stop && seg.start >= begin && tid == 0) {
+        if (unit1 < seg.end && seg.start >= begin && tid == 0) {
             Cut cut;
             cut.seg = seg;
             cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
@@ -1372,7 +1426,7 @@ void launch_rows(const AttentionArgs& a, bool bf16, dim3 grid, hipStream_t s) {
 }
 
 template <int NB, int NT>     // NT 0: attention_rows_kernel
-void launch(const AttentionArgs& a, bool bf16, int shares, hipStream_t s) {
+void launch(const AttentionArgs& a, bool bf16, int shares, bool joined, hipStream_t s) {
     constexpr int ROWS = NT ? 16 * NT : ROWS_TILE;
     const dim3 block(WAVES * 64), grid(shares), join(shares, ROWS / 2);
     const bool exact = a.cache.dim == 32 * NB;
@@ -1383,16 +1437,16 @@ void launch(const AttentionArgs& a, bool bf16, int shares, hipStream_t s) {
         if (exact) launch_main<NB, NT, true>(a, bf16, grid, s);
         else launch_main<NB, NT, false>(a, bf16, grid, s);
     }
-    if (shares == 1) return;
+    if (!joined) return;
     if (bf16) hipLaunchKernelGGL((attention_join_kernel<NB, ROWS / 16, true>), join, block, 0, s, a);
     else hipLaunchKernelGGL((attention_join_kernel<NB, ROWS / 16, false>), join, block, 0, s, a);
 }
 
 template <int NB>
-void launch(const AttentionArgs& a, int nt, bool bf16, int shares, hipStream_t s) {
-    if (nt == 0) launch<NB, 0>(a, bf16, shares, s);
-    else if (nt == 1) launch<NB, 1>(a, bf16, shares, s);
-    else if constexpr (NB < 8) launch<NB, 2>(a, bf16, shares, s);
+void launch(const AttentionArgs& a, int nt, bool bf16, int shares, bool joined, hipStream_t s) {
+    if (nt == 0) launch<NB, 0>(a, bf16, shares, joined, s);
+    else if (nt == 1) launch<NB, 1>(a, bf16, shares, joined, s);
+    else if constexpr (NB < 8) launch<NB, 2>(a, bf16, shares, joined, s);
 }
 
 mx_status check_pitches(int64_t ld, int64_t head_ld, int dim) {
@@ -1474,14 +1528,16 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.cuts = (Cut*)workspace;
     a.parts = (float*)(a.cuts + shape.shares);
     if (c.pages == 0) a.capacity = 0;
-    // no more workgroups than there can be work for
+    // no more workgroups than there can be work for, and no join where no segment can be long enough to be cut
     const int64_t tiles = (tokens / shape.tile_tokens + min(tokens, (int64_t)seqs)) * a.line_heads;
-    const int64_t units = tiles * max(ceil_div(a.capacity, UNIT), (int64_t)1);
-    const int shares = (int)min(shape.shares, ceil_div(units, MIN_UNITS));
+    int64_t longest = max(ceil_div(a.capacity, UNIT), (int64_t)1);
+    if (window) longest = min(longest, ((int64_t)window + shape.tile_tokens) / UNIT + 2);
+    const int shares = (int)min(shape.shares, ceil_div(tiles * longest, MIN_UNITS));
+    const bool join = shares > 1 && longest > WHOLE_UNITS;
     (void)hipGetLastError();
-    if (shape.nb == 2) launch<2>(a, shape.nt, bf16, shares, s);
-    else if (shape.nb == 4) launch<4>(a, shape.nt, bf16, shares, s);
-    else launch<8>(a, shape.nt, bf16, shares, s);
+    if (shape.nb == 2) launch<2>(a, shape.nt, bf16, shares, join, s);
+    else if (shape.nb == 4) launch<4>(a, shape.nt, bf16, shares, join, s);
+    else launch<8>(a, shape.nt, bf16, shares, join, s);
     return launch_status();
 }
 
