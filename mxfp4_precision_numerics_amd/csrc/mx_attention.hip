@@ -974,6 +974,10 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 // and drops what is below 2^-13 of it, so the scores would not be sums in fp32.)
 // ---------------------------------------------------------------------------
 constexpr int ROWS_TILE = 128, ROWS_WAVE = 32;
+// The exponentials' reference is kept until a row's largest score has outgrown it
+// by 2^GROWTH: any reference serves, as long as nothing overflows (568 us; 587
+// where the sums are scaled for each new maximum)
+constexpr float GROWTH = 8.0f;
 
 template <int NB, int QT>
 struct RowsShared {
@@ -1177,18 +1181,26 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
             __builtin_amdgcn_sched_barrier(0);
             if (key0 <= any_to && key0 + UNIT - 1 >= any_from) {
                 const bool whole = key0 + UNIT - 1 <= all_to && key0 >= all_from && !__any(pages < 0);
+                // (operands are read AHEAD steps before their products, for a read takes as long as several: two times 4096
+                // queries behind 4096 tokens, 32 heads of 128, take 650 us in place of 702)
+                constexpr int AHEAD = 2;
+                bf16x8 ring[AHEAD + 1];
                 f32x4 s[NT][4];
+                auto read_k = [&](int i) { ring[i % (AHEAD + 1)] = *(const bf16x8*)&sh.work.k[buf][(i * 64 + lane) * 16]; };
+                auto read_v = [&](int i) { ring[i % (AHEAD + 1)] = *(const bf16x8*)&sh.work.v[buf][(i * 64 + lane) * 16]; };
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
+                for (int i = 0; i < AHEAD; ++i) read_k(i);
 #pragma unroll
-                    for (int x = 0; x < NB; ++x) {
-                        const bf16x8 k = *(const bf16x8*)&sh.work.k[buf][((t * NB + x) * 64 + lane) * 16];
+                for (int i = 0; i < 4 * NB; ++i) {
+                    const int t = i / NB, x = i % NB;
+                    if (i + AHEAD < 4 * NB) read_k(i + AHEAD);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int y = 0; y < QT; ++y)
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int y = 0; y < QT; ++y)
-                                s[n][t] = mfma(k, qf[y][n][x], x == 0 && y == 0 ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : s[n][t]);
-                    }
+                            s[n][t] = mfma(ring[i % (AHEAD + 1)], qf[y][n][x],
+                                           x == 0 && y == 0 ? (f32x4){0.0f, 0.0f, 0.0f, 0.0f} : s[n][t]);
                 }
                 uint32_t p[NT][2][PT][4];
                 bool bad[2] = {false, false};
@@ -1211,14 +1223,14 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
 #pragma unroll
                     for (int i = 1; i < 16; ++i) m = fmaxf(m, x[i]);
                     m = fmaxf(across(m, MaxF()) * scale, top[n]);
-                    const float safe = m == -__builtin_inff() ? 0.0f : m;
-                    if (__any(m > top[n])) {
-                        const float f = __builtin_amdgcn_exp2f(top[n] - safe);
+                    if (__any(m > top[n] + GROWTH)) {
+                        const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[n] - m);
                         sum[n] *= f;
 #pragma unroll
                         for (int k = 0; k < M; ++k) acc[n][k] *= f;
+                        top[n] = m;
                     }
-                    top[n] = m;
+                    const float safe = top[n] == -__builtin_inff() ? 0.0f : top[n];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], scale, -safe));
@@ -1229,9 +1241,10 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
                         if constexpr (PT == 2) p[n][i >> 2][PT - 1][i & 3] = pack(e0 - bf16lo(w), e1 - bf16hi(w));
                     }
                 }
+                if (__builtin_amdgcn_readfirstlane(sh.work.odd[buf][0] | sh.work.odd[buf][1])) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (__builtin_amdgcn_readfirstlane(sh.work.odd[buf][j])) {
+                    for (int j = 0; j < 2; ++j) {
+                        if (!__builtin_amdgcn_readfirstlane(sh.work.odd[buf][j])) continue;
                         const uint4 mark = *(const uint4*)&sh.work.marks[buf][j][lane * 16];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -1249,15 +1262,22 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
                                 for (int k = 0; k < M; ++k) acc[n][k][i] = hit[i] == 0.0f ? acc[n][k][i] : __builtin_nanf("");
                         }
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) read_v(i);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
                     for (int k = 0; k < M; ++k) {
-                        const bf16x8 v = *(const bf16x8*)&sh.work.v[buf][((j * M + k) * 64 + lane) * 16];
+                        const int i = j * M + k;
+                        if (i + AHEAD < 2 * M) read_v(i + AHEAD);
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int y = 0; y < PT; ++y)
-                                acc[n][k] = mfma(v, operand(p[n][j][y][0], p[n][j][y][1], p[n][j][y][2], p[n][j][y][3]),
-                                                 acc[n][k]);
+                                acc[n][k] = mfma(ring[i % (AHEAD + 1)],
+                                                 operand(p[n][j][y][0], p[n][j][y][1], p[n][j][y][2], p[n][j][y][3]), acc[n][k]);
                     }
                 }
             }
@@ -1309,8 +1329,10 @@ __global__ __launch_bounds__(WAVES * 64, NB == 8 ? 1 : 2) void attention_rows_ke
 }
 
 // Joins the parts of the segments that were cut.  Workgroup x: the segment
-// that share x began and did not finish, if there is one; y: two of its rows.
-// Sets of threads (groups) share the parts, AHEAD of them under way at once.
+// that share x began and did not finish, if there is one.  A group of threads
+// joins two rows, up to AHEAD parts under way at once.  Where there are no more
+// parts than that every group takes rows of its own (512 segments of 128 rows in
+// two parts: 17 us less than shared), else workgroup y's groups share two rows.
 template <int NB, int NT, bool BF16>
 __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArgs a) {
     constexpr int PIECES = 4 * NB, ITEMS = 2 * PIECES, GROUPS = WAVES * 64 / ITEMS, AHEAD = 4;
@@ -1319,16 +1341,19 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
     if (cut.count == 0) return;
     const Segment& seg = cut.seg;
     const int rows = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2)) * a.tile_heads;
-    if (2 * (int)blockIdx.y >= rows) return;
+    const bool share = cut.count > AHEAD;
+    if (2 * (int)blockIdx.y * (share ? 1 : GROUPS) >= rows) return;
     const int item = threadIdx.x % ITEMS, group = threadIdx.x / ITEMS;
-    const int c = 2 * blockIdx.y + item / PIECES, d = item % PIECES * 8;
+    const int pair = share ? blockIdx.y : blockIdx.y * GROUPS + group;
+    const int c = 2 * min(pair, 8 * NT - 1) + item / PIECES, d = item % PIECES * 8;
+    const int first = share ? group : 0, step = share ? GROUPS : 1;
     float top = -__builtin_inff(), sum = 0.0f, v[8] = {};
-    for (int i0 = group; i0 < cut.count; i0 += AHEAD * GROUPS) {
+    for (int i0 = first; i0 < cut.count; i0 += AHEAD * step) {
         float t[AHEAD], l[AHEAD];
         f32x4 x[AHEAD], y[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const int i = min(i0 + k * GROUPS, cut.count - 1);
+            const int i = min(i0 + k * step, cut.count - 1);
             const Part<NB, 16 * NT> part(a, i == 0 ? cut.slot : 2 * (int64_t)(blockIdx.x + i));
             t[k] = *part.top(c);                           // (rows that do not exist hold anything and go nowhere)
             l[k] = *part.sum(c);
@@ -1338,7 +1363,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
         float m = top;
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            if (i0 + k * GROUPS >= cut.count) t[k] = -__builtin_inff();
+            if (i0 + k * step >= cut.count) t[k] = -__builtin_inff();
             m = fmaxf(m, t[k]);
         }
         const float safe = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(top - safe);
@@ -1347,7 +1372,7 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
         for (int k = 0; k < 8; ++k) v[k] *= f;
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            if (i0 + k * GROUPS >= cut.count) continue;
+            if (i0 + k * step >= cut.count) continue;
             const float e = __builtin_amdgcn_exp2f(t[k] - safe);
             sum += l[k] * e;
 #pragma unroll
@@ -1357,6 +1382,12 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
             }
         }
         top = m;
+    }
+    Row r;
+    const bool live = row_of(a, seg, c, r) && c < rows;
+    if (!share) {
+        finish<BF16>(a, r, live && pair < 8 * NT, d, v, top, sum);
+        return;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[group][item][k] = v[k];
@@ -1381,8 +1412,6 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += o[w][item][k] * e;
     }
-    Row r;
-    const bool live = row_of(a, seg, c, r) && c < rows;
     finish<BF16>(a, r, live, d, v, most, all);
 }
 
