@@ -42,6 +42,10 @@ constexpr int UNIT = 64;              // keys that a wave takes at a time
 constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
 constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least
 constexpr int WHOLE_UNITS = 16;       // of a segment that is not cut
+// The exponentials' reference is kept until a row's largest score has outgrown it
+// by 2^GROWTH: any reference serves, as long as nothing overflows (a prompt
+// of 2 x 4096 queries: 568 us; 587 where the sums are scaled for each new maximum)
+constexpr float GROWTH = 8.0f;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -794,14 +798,14 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 #pragma unroll
                     for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
                     m = fmaxf(across(m, MaxF()) * scale, top[n]);
-                    const float safe = m == -__builtin_inff() ? 0.0f : m;
-                    if (__any(m > top[n])) {
-                        const float f = __builtin_amdgcn_exp2f(top[n] - safe);
+                    if (__any(m > top[n] + GROWTH)) {
+                        const float f = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[n] - m);
                         sum[n] *= f;
 #pragma unroll
                         for (int k = 0; k < M; ++k) acc[n][k] *= f;
+                        top[n] = m;
                     }
-                    top[n] = m;
+                    const float safe = top[n] == -__builtin_inff() ? 0.0f : top[n];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, -safe));
@@ -974,10 +978,6 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 // and drops what is below 2^-13 of it, so the scores would not be sums in fp32.)
 // ---------------------------------------------------------------------------
 constexpr int ROWS_TILE = 128, ROWS_WAVE = 32;
-// The exponentials' reference is kept until a row's largest score has outgrown it
-// by 2^GROWTH: any reference serves, as long as nothing overflows (568 us; 587
-// where the sums are scaled for each new maximum)
-constexpr float GROWTH = 8.0f;
 
 template <int NB, int QT>
 struct RowsShared {
