@@ -96,7 +96,8 @@ __global__ __launch_bounds__(THREADS) void balance_kernel(BalanceArgs a) {
         float any = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) any = v[i] == -__builtin_inff() ? any : 1.0f;
-        used += live && lane == 0 && row_reduce<L>(any, MaxF()) > 0.0f;
+        const bool scored = row_reduce<L>(any, MaxF()) > 0.0f;     // (by all lanes of the row)
+        used += live && lane == 0 && scored;
         row_scores<L, N, false>(v, softmax, nullptr);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += live ? v[i] : 0.0f;
@@ -263,18 +264,17 @@ void launch(const BalanceBwdArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((balance_bwd_kernel<B, L, C>), dim3((uint32_t)ceil_div(a.tokens, 256 / L)), dim3(256), 0, s, a);
 }
 // The lanes that share a row and the chunks of four experts each holds.  With
-// many tokens half as many lanes take a row, as in the router.
+// many tokens half as many lanes take a row of the backward pass, as in the
+// router; the forward's workgroups walk over rows and keep a sum for every
+// element, for which fewer registers are faster than fewer lanes.
 constexpr int64_t MANY_TOKENS = 8192;
-template <bool B, class A>
-void dispatch(const A& a, bool many, hipStream_t s) {
+template <bool B, bool MANY, class A>
+void dispatch(const A& a, hipStream_t s) {
     const int e = a.experts;
     if (e <= 32) launch<B, 8, 1>(a, s);
-    else if (e <= 64 && many) launch<B, 8, 2>(a, s);
-    else if (e <= 128 && many) launch<B, 8, 4>(a, s);
-    else if (e <= 256 && many) launch<B, 8, 8>(a, s);
-    else if (e <= 64) launch<B, 16, 1>(a, s);
-    else if (e <= 128) launch<B, 16, 2>(a, s);
-    else if (e <= 256) launch<B, 16, 4>(a, s);
+    else if (e <= 64) launch<B, MANY ? 8 : 16, MANY ? 2 : 1>(a, s);
+    else if (e <= 128) launch<B, MANY ? 8 : 16, MANY ? 4 : 2>(a, s);
+    else if (e <= 256) launch<B, MANY ? 8 : 16, MANY ? 8 : 4>(a, s);
     else if (e <= 512) launch<B, 32, 4>(a, s);
     else launch<B, 64, 4>(a, s);
 }
@@ -314,8 +314,8 @@ mx_status mx_balance(const void* logits, mx_dtype lt, int64_t tokens, int32_t ex
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
     if (blocks > 0) {
-        if (lt == MX_BF16) dispatch<true>(a, false, s);
-        else dispatch<false>(a, false, s);
+        if (lt == MX_BF16) dispatch<true, false>(a, s);
+        else dispatch<false, false>(a, s);
     }
     int lanes_log2 = 0;
     while (1 << lanes_log2 < experts) ++lanes_log2;
@@ -344,9 +344,10 @@ mx_status mx_balance_bwd(const void* logits, mx_dtype lt, int64_t tokens, int32_
     a.vec_add = experts % 4 == 0 && a.add_ld % 4 == 0 && aligned_to(add, four);
     a.vec_out = experts % 4 == 0 && a.dld % 4 == 0 && aligned_to(dlogits, four);
     (void)hipGetLastError();
+    hipStream_t s = (hipStream_t)stream;
     const bool many = tokens >= MANY_TOKENS;
-    if (lt == MX_BF16) dispatch<true>(a, many, (hipStream_t)stream);
-    else dispatch<false>(a, many, (hipStream_t)stream);
+    if (lt == MX_BF16) many ? dispatch<true, true>(a, s) : dispatch<true, false>(a, s);
+    else many ? dispatch<false, true>(a, s) : dispatch<false, false>(a, s);
     return launch_status();
 }
 

@@ -203,3 +203,59 @@ def test_refusals():
                 lambda: mx.balance(l, ids, workspace=tt.empty(3, dtype=tt.uint8, device="cuda"))):
         with pytest.raises((ValueError, TypeError, mx.MXError)):
             bad()
+
+
+@pytest.mark.parametrize("experts", [5, 32, 60, 200, 500, 1024])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_rows_with_a_single_expert_left(kind, experts):
+    """Token t has a score for expert t alone: each has one, wherever it lies."""
+    tt = torch()
+    tokens = experts + 3
+    l = tt.full((tokens, experts), -float("inf"), dtype=tt.bfloat16 if kind == "bf16" else tt.float32, device="cuda")
+    at = tt.arange(experts, device="cuda")
+    l[at, at] = 0.5
+    ids = tt.full((tokens, 1), -1, dtype=tt.int32, device="cuda")
+    ids[:experts, 0] = at.int()
+    loss, counts, slope = mx.balance(l, ids)
+    want = ref.balance(l.double().cpu().numpy(), ids.cpu().numpy(), 0)
+    assert (counts == 1).all()
+    assert np.abs(slope.cpu().numpy() - want[2]).max() <= 2.0 ** -23 * want[2].max()
+    assert abs(float(loss) - want[0]) <= (tokens + experts + 8) * 2.0 ** -24 * want[0]
+    assert (mx.balance_bwd(l, slope) == 0).all()           # the only score of a row is 1 whatever its logit
+
+
+@pytest.mark.parametrize("experts", [60, 128, 250])
+def test_many_tokens(experts):
+    """As many tokens as the backward pass takes with fewer lanes a row, and one fewer."""
+    tt = torch()
+    for tokens in (8191, 8192):
+        l64, l = logits_of(tokens, experts, "f32", 21, padding=5)
+        ids = ids_of(tokens, experts, 2, 22)
+        loss, counts, slope = mx.balance(l, dev(ids), score=mx.SIGMOID)
+        want = ref.balance(l64, ids, 1)
+        assert np.array_equal(counts.cpu().numpy(), want[1])
+        assert abs(float(loss) - want[0]) <= (tokens + experts + 8) * 2.0 ** -24 * want[0]
+        got = mx.balance_bwd(l, slope, score=mx.SIGMOID).double().cpu().numpy()
+        g = ref.balance_bwd(l64, want[2], 1)
+        s = np.where(np.isneginf(l64), 0.0, 1.0 / (1.0 + np.exp(-l64)))
+        s = s / np.maximum(s.sum(1, keepdims=True), 1e-300)
+        tol = s * (want[2] + (s * want[2]).sum(1, keepdims=True)) * (2 * experts + 16) * 2.0 ** -24
+        assert (np.abs(got - g) <= tol + 2.0 ** -24 * np.abs(g) + 1e-37).all()
+
+
+def test_two_streams_at_once():
+    tt = torch()
+    calls = []
+    for seed in (31, 32):
+        _, l = logits_of(4000, 100, "bf16", seed)
+        calls.append((l, dev(ids_of(4000, 100, 4, seed)), tt.cuda.Stream()))
+    want = [mx.balance(l, ids) for l, ids, _ in calls]
+    tt.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for l, ids, stream in calls:
+            with tt.cuda.stream(stream):
+                got.append(mx.balance(l, ids))
+    tt.cuda.synchronize()
+    for i, have in enumerate(got):
+        assert all(tt.equal(a, b) for a, b in zip(have, want[i % 2]))
