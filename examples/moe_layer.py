@@ -3,10 +3,11 @@ kernels: routing, dispatch plan, MXFP4 quantizers and grouped GEMMs, the
 weighted combine, all their gradients, and clipping by the global norm.
 
     python examples/moe_layer.py [--tokens N] [--d-model D] [--d-ff F] [--experts E] [--top-k K] [--steps S]
+                                 [--balance C]
 
 The layer learns to reproduce a fixed random mixture of experts of the same
-shape from synthetic tokens; the loss of every step is printed.  Sizes are
-multiples of 32.  The activation between the two expert linears (SiLU-gated)
+shape from synthetic tokens; the loss of every step is printed.  With --balance
+C times the router's balance loss is added to it.  Sizes are multiples of 32.  The activation between the two expert linears (SiLU-gated)
 and the router's small products are plain torch.
 """
 import argparse
@@ -22,13 +23,13 @@ from mxfp4_precision_numerics_amd import mx  # noqa: E402
 class MoELayer:
     """y = x + sum over a token's experts of weight * down(gated(up(x)))."""
 
-    def __init__(self, d_model, d_ff, experts, top_k, seed):
+    def __init__(self, d_model, d_ff, experts, top_k, seed, balance=0.0):
         gen = torch.Generator("cuda").manual_seed(seed)
 
         def normal(*shape):
             return torch.randn(shape, device="cuda", generator=gen) * shape[-2] ** -0.5
 
-        self.top_k, self.experts = top_k, experts
+        self.top_k, self.experts, self.balance = top_k, experts, balance
         self.router = normal(d_model, experts)
         self.up = normal(experts, d_model, 2 * d_ff)       # gate and up projections side by side
         self.down = normal(experts, d_ff, d_model)
@@ -43,6 +44,8 @@ class MoELayer:
         if padding:
             logits[-padding:] = -float("inf")
         ids, weights = mx.route(logits, self.top_k)
+        if self.balance:                                   # its loss, the experts' assignments, what backward needs
+            self.balanced = mx.balance(logits, ids)
         offsets, row_index, slot = mx.route_plan(ids, self.experts)
         rows, d = row_index.numel(), x.shape[1]
         up, down = mx.quantize_2d(self.up), mx.quantize_2d(self.down)
@@ -78,6 +81,8 @@ class MoELayer:
 
         dy, dweights = mx.combine_bwd(dout, y, slot, weights, used_rows=offsets[-1:])
         dlogits = mx.route_bwd(logits, ids, dweights)
+        if self.balance:
+            mx.balance_bwd(logits, self.balanced[2], scale=self.balance, add=dlogits, dlogits=dlogits)
         ddown = weight_gradient(mx.quantize_1d(a, stream_id=0, **col), mx.quantize_1d(dy, stream_id=1, **col),
                                 a.shape[1], d)
         da = mx.grouped_gemm(*mx.quantize_1d(dy, stream_id=2, **row), down[0], down[1], offsets, rows, a.shape[1], d,
@@ -97,11 +102,11 @@ class MoELayer:
 
 
 def train(tokens=512, d_model=256, d_ff=128, experts=8, top_k=2, steps=60, rate=2.0, max_norm=1.0, seed=0,
-          report=None):
-    """Losses of the steps."""
+          report=None, balance=0.0):
+    """Losses of the steps, without the balance loss."""
     gen = torch.Generator("cuda").manual_seed(seed)
     teacher = MoELayer(d_model, d_ff, experts, top_k, seed + 1)
-    layer = MoELayer(d_model, d_ff, experts, top_k, seed + 2)
+    layer = MoELayer(d_model, d_ff, experts, top_k, seed + 2, balance)
     padding = tokens // 16
     x = torch.randn((tokens, d_model), device="cuda", generator=gen).to(torch.bfloat16)
     target = teacher.forward(x, padding).float()
@@ -115,7 +120,10 @@ def train(tokens=512, d_model=256, d_ff=128, experts=8, top_k=2, steps=60, rate=
         for p, g in zip(layer.parameters(), grads):
             p -= rate * g
         if report:
-            report("step %3d  loss %9.4f  gradient norm %8.4f" % (step, losses[-1], float(norm)))
+            line = "step %3d  loss %9.4f  gradient norm %8.4f" % (step, losses[-1], float(norm))
+            if balance:
+                line += "  balance %6.4f  fullest expert %d" % (float(layer.balanced[0]), int(layer.balanced[1].max()))
+            report(line)
     return losses
 
 
@@ -123,5 +131,7 @@ if __name__ == "__main__":
     parser = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("tokens", 512), ("d-model", 256), ("d-ff", 128), ("experts", 8), ("top-k", 2), ("steps", 60)):
         parser.add_argument("--" + name, type=int, default=value)
+    parser.add_argument("--balance", type=float, default=0.0)
     args = parser.parse_args()
-    train(args.tokens, args.d_model, args.d_ff, args.experts, args.top_k, args.steps, report=print)
+    train(args.tokens, args.d_model, args.d_ff, args.experts, args.top_k, args.steps, report=print,
+          balance=args.balance)
