@@ -31,7 +31,7 @@ struct AttentionArgs {
     void* out;
     int64_t out_ld, out_head_ld;
     float* lse;
-    int group, tile_tokens, tile_log2, tile_heads, head_tiles, line_heads;
+    int near, min_units, group, tile_tokens, tile_log2, tile_heads, head_tiles, line_heads;
     uint32_t code_page, scale_page;   // bytes of a page's codes, scales
     float* parts;
     Cut* cuts;                    // one a share
@@ -40,7 +40,7 @@ struct AttentionArgs {
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
 constexpr int UNIT = 64;              // keys that a wave takes at a time
 constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
-constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least
+constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least, where segments are cut
 constexpr int WHOLE_UNITS = 16;       // of a segment that is not cut
 // The exponentials' reference is kept until a row's largest score has outgrown it
 // by 2^GROWTH: any reference serves, as long as nothing overflows (a prompt
@@ -196,6 +196,14 @@ struct Cut {
 };
 static_assert(sizeof(Cut) % 16 == 0, "the parts follow the cuts, 16-byte aligned");
 
+// The workgroup's share.  Workgroups go round the 8 XCDs in turn.  Few rows over
+// long caches: neighbouring shares, which hold parts of one sequence, are put on
+// one XCD (5 rows of 32 sequences of 8192 tokens, 8 heads of 128: 65 us in place
+// of 81); else they are spread (prompts of 2048 tokens: 114 in place of 122).
+__device__ __forceinline__ int share_id(const AttentionArgs& a) {
+    return a.near ? (int)((blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3)) : (int)blockIdx.x;
+}
+
 // Measures the line, and finds the stretch of unit share * (what a share has):
 // returns that unit's place, not less than the line's length if there is none.
 __device__ __forceinline__ int64_t measure_line(const AttentionArgs& a, Line& line, int64_t& per) {
@@ -219,8 +227,8 @@ __device__ __forceinline__ int64_t measure_line(const AttentionArgs& a, Line& li
         total += u;
     }
     total = uniform(total);
-    per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MIN_UNITS);
-    const int64_t at = blockIdx.x * per, from = base + sum - mine;
+    per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.min_units);
+    const int64_t at = share_id(a) * per, from = base + sum - mine;
     if (from <= at && at < from + mine) {
         line.from = from;
         line.stretch = tid;
@@ -622,7 +630,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 
     int64_t per;
     const int64_t begin = measure_line(a, sh.line, per), total = uniform(sh.line.total), stop = min(begin + per, total);
-    if (tid == 0) a.cuts[blockIdx.x].count = 0;
+    if (tid == 0) a.cuts[share_id(a)].count = 0;
     if (begin >= total) return;
     Segment seg = locate(a, sh.line, begin);
     int64_t at = begin;
@@ -895,7 +903,7 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         __syncthreads();                                   // (also: nobody reads the queries any more)
         const AttentionArgs b = arguments();
         const bool complete = at == seg.start && unit1 == seg.end;
-        const Part<NB, 16 * NT> part(b, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
+        const Part<NB, 16 * NT> part(b, 2 * (int64_t)share_id(b) + (at == begin ? 0 : 1));
         constexpr int SIDES = 32 * NB / Sh::SIDE;
         float* o = (float*)sh.data;
 #pragma unroll
@@ -953,10 +961,10 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         if (unit1 < seg.end && seg.start >= begin && tid == 0) {
             Cut cut;
             cut.seg = seg;
-            cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
-            cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
+            cut.slot = 2 * (int64_t)share_id(b) + (at == begin ? 0 : 1);
+            cut.count = (int)((next - 1) / per) - share_id(b) + 1;
             cut.pad = 0;
-            cut.write(b.cuts + blockIdx.x);
+            cut.write(b.cuts + share_id(b));
         }
         at = next;
         if (at >= stop) return;
@@ -1010,7 +1018,7 @@ __global__ __launch_bounds__(rows_waves(NB) * 64, NB == 8 ? 1 : 2) void attentio
 
     int64_t per;
     const int64_t begin = measure_line(a, sh.line, per), total = uniform(sh.line.total), stop = min(begin + per, total);
-    if (tid == 0) a.cuts[blockIdx.x].count = 0;
+    if (tid == 0) a.cuts[share_id(a)].count = 0;
     if (begin >= total) return;
     Segment seg = locate(a, sh.line, begin);
     int64_t at = begin;
@@ -1288,7 +1296,7 @@ __global__ __launch_bounds__(rows_waves(NB) * 64, NB == 8 ? 1 : 2) void attentio
 
         const AttentionArgs b = arguments();
         const bool complete = at == seg.start && unit1 == seg.end;
-        const Part<NB, ROWS_TILE> part(b, 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1));
+        const Part<NB, ROWS_TILE> part(b, 2 * (int64_t)share_id(b) + (at == begin ? 0 : 1));
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int c = wave * ROWS_WAVE + 16 * n + col;
@@ -1317,10 +1325,10 @@ __global__ __launch_bounds__(rows_waves(NB) * 64, NB == 8 ? 1 : 2) void attentio
         if (unit1 < seg.end && seg.start >= begin && tid == 0) {
             Cut cut;
             cut.seg = seg;
-            cut.slot = 2 * (int64_t)blockIdx.x + (at == begin ? 0 : 1);
-            cut.count = (int)((next - 1) / per) - (int)blockIdx.x + 1;
+            cut.slot = 2 * (int64_t)share_id(b) + (at == begin ? 0 : 1);
+            cut.count = (int)((next - 1) / per) - share_id(b) + 1;
             cut.pad = 0;
-            cut.write(b.cuts + blockIdx.x);
+            cut.write(b.cuts + share_id(b));
         }
         at = next;
         if (at >= stop) return;
@@ -1415,19 +1423,34 @@ __global__ __launch_bounds__(WAVES * 64) void attention_join_kernel(AttentionArg
     finish<BF16>(a, r, live, d, v, most, all);
 }
 
+// Which kernel, by the rows of a sequence and a head.  Tiles of 16 or 32 rows read
+// the cache once each and split the keys over a workgroup's waves; a tile of 128
+// reads it once, and every wave passes over all keys.  32 sequences of 8192
+// tokens, 8 heads of 128: 36 rows take 108 us in tiles of 32, 171 in one of 128;
+// 96 rows 164 and 182; 128 rows 218 and 196.  Heads of 256, tiles of 16: 20 rows
+// 140 and 275, 36 rows 306 and 278.
+// Few tiles of 128 do not fill the chip, unless their caches are long: 2 heads of
+// 800 rows over 1000 tokens take 20 us in tiles of 32, 40 in tiles of 128; 8 heads
+// of 1024 rows over 256 tokens 33 and 30.
+constexpr int64_t FEW_TILES = 64, FEW_UNITS = 8192;
+
 // What the host chooses from the sizes it knows.
 struct Shape {
     int nb, nt, tile_tokens, tile_heads, head_tiles;     // nt 0: attention_rows_kernel
     int64_t shares, part_floats;
 };
 
-Shape shape_of(const CacheView& c, bool bf16, int64_t tokens, int q_heads, int max_queries) {
+// capacity: of a sequence, -1 if it is not known: then the shape that needs the larger workspace.
+Shape shape_of(const CacheView& c, int64_t tokens, int q_heads, int max_queries, int64_t capacity) {
     Shape s;
     const int group = q_heads / c.heads;
     const int64_t most = max_queries > 0 ? min((int64_t)max_queries, tokens) : tokens;
     s.nb = c.dim <= 64 ? 2 : c.dim <= 128 ? 4 : 8;
     const int64_t rows = most * group;
-    s.nt = rows <= 16 ? 1 : rows <= 32 && s.nb < 8 ? 2 : 0;    // (32 rows of 256 elements do not fit the registers)
+    const int64_t tiles = tokens * q_heads / ROWS_TILE;
+    const bool few = capacity >= 0 && tiles < FEW_TILES && tiles * (capacity / UNIT) < FEW_UNITS;
+    if (s.nb < 8) s.nt = rows <= 16 ? 1 : rows <= 96 || few ? 2 : 0;
+    else s.nt = rows <= 32 || few ? 1 : 0;                 // (32 rows of 256 elements do not fit the registers)
     const int r = s.nt ? 16 * s.nt : ROWS_TILE;
     s.tile_heads = min(group, r);
     s.head_tiles = (group + r - 1) / r;
@@ -1491,7 +1514,7 @@ int64_t mx_cache_attention_workspace(const mx_cache* cache, mx_dtype qt, int64_t
     CacheView c;
     if (view_cache(cache, c) != MX_OK || q_heads < 1 || q_heads % c.heads || max_queries < 0) return 0;
     if (tokens < 1 || tokens > INT32_MAX / q_heads || (qt != MX_F32 && qt != MX_BF16)) return 0;
-    const Shape s = shape_of(c, qt == MX_BF16, tokens, q_heads, max_queries);
+    const Shape s = shape_of(c, tokens, q_heads, max_queries, -1);
     return s.shares * (2 * s.part_floats * (int64_t)sizeof(float) + (int64_t)sizeof(Cut));
 }
 
@@ -1545,7 +1568,8 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.lse = lse;
     hipStream_t s = (hipStream_t)stream;
     const bool bf16 = qt == MX_BF16;
-    const Shape shape = shape_of(c, bf16, tokens, q_heads, max_queries);
+    if (c.pages == 0) a.capacity = 0;
+    const Shape shape = shape_of(c, tokens, q_heads, max_queries, a.capacity);
     a.group = q_heads / c.heads;
     a.tile_tokens = shape.tile_tokens;
     a.tile_log2 = __builtin_ctz(shape.tile_tokens);
@@ -1556,13 +1580,16 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.scale_page = (uint32_t)(c.heads * cache->page_size * (c.dim / 32));
     a.cuts = (Cut*)workspace;
     a.parts = (float*)(a.cuts + shape.shares);
-    if (c.pages == 0) a.capacity = 0;
     // no more workgroups than there can be work for, and no join where no segment can be long enough to be cut
     const int64_t tiles = (tokens / shape.tile_tokens + min(tokens, (int64_t)seqs)) * a.line_heads;
     int64_t longest = max(ceil_div(a.capacity, UNIT), (int64_t)1);
     if (window) longest = min(longest, ((int64_t)window + shape.tile_tokens) / UNIT + 2);
-    const int shares = (int)min(shape.shares, ceil_div(tiles * longest, MIN_UNITS));
-    const bool join = shares > 1 && longest > WHOLE_UNITS;
+    const bool join = longest > WHOLE_UNITS;
+    // (short segments go to workgroups of their own as long as there are any: 32 heads of a prompt of 128 tokens take
+    // 13 us, 30 with four units a share)
+    a.min_units = (int)min(max(longest / 4, (int64_t)1), (int64_t)MIN_UNITS);
+    a.near = join && shape.nt;
+    const int shares = (int)min(shape.shares, ceil_div(ceil_div(tiles * longest, a.min_units), 8) * 8);
     (void)hipGetLastError();
     if (shape.nb == 2) launch<2>(a, shape.nt, bf16, shares, join, s);
     else if (shape.nb == 4) launch<4>(a, shape.nt, bf16, shares, join, s);
