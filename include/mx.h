@@ -639,9 +639,9 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
  * the logarithm of the denominator (-inf where that is 0).
  * out: q's type, out_ld and out_head_ld like q's; it overlaps no input.
  * Scores, the softmax's statistics and sums are fp32.  bf16 queries enter the
- * products as they are; fp32 ones, and transformed ones, as a sum of two bf16
- * (2^-17 relative); exp(..) enters the product with v as bf16, for fp32 outputs
- * as a sum of two.  Every sum has a fixed order, given the lengths.
+ * products as they are; transformed, as a sum of two bf16 (2^-17 relative); fp32
+ * ones as a sum of three.  exp(..) enters the product with v as bf16, for fp32
+ * outputs as a sum of three.  Every sum has a fixed order, given the lengths.
  * max_queries: the most rows that a sequence has, if the caller knows it (it
  * only selects the kernel); 0: unknown.
  * workspace: mx_cache_attention_workspace(...) bytes, 16-byte aligned, its

@@ -572,6 +572,7 @@ struct Queries {
             }
         }
     }
+    template <int ONLY = -1>                               // that term alone
     __device__ __forceinline__ void store(const AttentionArgs& a, __bf16* to, int pitch) const {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -598,19 +599,19 @@ struct Queries {
                 for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(__float_as_uint(f[e]) ^ (m >> e << 31));
                 rht32_quad(f, (d >> 3) & 3);
             }
-            uint32_t u[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = pack(f[2 * e], f[2 * e + 1]);
-            *(uint4*)(to + c * pitch + d) = make_uint4(u[0], u[1], u[2], u[3]);
-            if constexpr (QT == 2) {
-                uint32_t v[4];
+            for (int y = 0; y < QT; ++y) {
+                uint32_t u[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // (an infinite element has no rest)
+                for (int e = 0; e < 4; ++e) u[e] = pack(f[2 * e], f[2 * e + 1]);
+                if (ONLY < 0 || ONLY == y)
+                    *(uint4*)(to + ((ONLY < 0 ? y * ROWS : 0) + c) * pitch + d) = make_uint4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {              // what is left (of an infinite element, nothing)
                     const float lo = bf16lo(u[e]), hi = bf16hi(u[e]);
-                    v[e] = pack(__builtin_isinf(lo) ? 0.0f : f[2 * e] - lo, __builtin_isinf(hi) ? 0.0f : f[2 * e + 1] - hi);
+                    f[2 * e] = __builtin_isinf(lo) ? 0.0f : f[2 * e] - lo;
+                    f[2 * e + 1] = __builtin_isinf(hi) ? 0.0f : f[2 * e + 1] - hi;
                 }
-                *(uint4*)(to + (ROWS + c) * pitch + d) = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
     }
@@ -821,9 +822,13 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        p[n][0][i] = pack(x[2 * i], x[2 * i + 1]);
-                        if constexpr (PT == 2)
-                            p[n][PT - 1][i] = pack(x[2 * i] - bf16lo(p[n][0][i]), x[2 * i + 1] - bf16hi(p[n][0][i]));
+                        float e0 = x[2 * i], e1 = x[2 * i + 1];
+#pragma unroll
+                        for (int y = 0; y < PT; ++y) {
+                            const uint32_t w = p[n][y][i] = pack(e0, e1);
+                            e0 -= bf16lo(w);
+                            e1 -= bf16hi(w);
+                        }
                     }
                 }
 
@@ -986,7 +991,10 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 // and drops what is below 2^-13 of it, so the scores would not be sums in fp32.)
 // ---------------------------------------------------------------------------
 constexpr int ROWS_TILE = 128;
-constexpr int rows_waves(int nb) { return nb == 8 ? 8 : 4; }
+constexpr int rows_waves(int nb, int qt) { return nb == 8 || (nb == 4 && qt == 3) ? 8 : 4; }
+
+template <int I>
+struct Int { static constexpr int value = I; };
 
 template <int NB, int QT>
 struct RowsShared {
@@ -994,7 +1002,7 @@ struct RowsShared {
     static constexpr int PITCH = 32 * NB + 8;                  // of q, in bf16
     static constexpr int K_BYTES = 4 * NB * 1024, V_BYTES = 2 * M * 1024;
     union {
-        alignas(16) __bf16 q[QT][ROWS_TILE][PITCH];
+        alignas(16) __bf16 q[ROWS_TILE][PITCH];            // one term at a time
         struct {
             alignas(16) unsigned char k[2][K_BYTES], v[2][V_BYTES];
             alignas(16) unsigned char marks[2][2][1024];
@@ -1005,9 +1013,9 @@ struct RowsShared {
 };
 
 template <int NB, bool EXACT, bool BF16, int QT, int PT>
-__global__ __launch_bounds__(rows_waves(NB) * 64, NB == 8 ? 1 : 2) void attention_rows_kernel(AttentionArgs a) {
+__global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 1 : 2) void attention_rows_kernel(AttentionArgs a) {
     using Sh = RowsShared<NB, QT>;
-    constexpr int PARTS = rows_waves(NB) / 4, ROWS_WAVE = ROWS_TILE / rows_waves(NB), M = Sh::M, NT = ROWS_WAVE / 16;
+    constexpr int PARTS = rows_waves(NB, QT) / 4, ROWS_WAVE = ROWS_TILE / rows_waves(NB, QT), M = Sh::M, NT = ROWS_WAVE / 16;
     constexpr int KX = NB / PARTS, KV = NB / (2 * PARTS);          // what a lane loads of a key: dwords of K, bytes of V
     __shared__ Sh sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1032,22 +1040,26 @@ __global__ __launch_bounds__(rows_waves(NB) * 64, NB == 8 ? 1 : 2) void attentio
         const int head = seg.head / a.head_tiles;
         const int tokens = min(a.tile_tokens, seg.seq.n - (seg.tile << a.tile_log2));
         const int rows = tokens * a.tile_heads;
+        bf16x8 qf[QT][NT][NB];
         {
             const AttentionArgs b = arguments();
-            Queries<NB, ROWS_TILE, BF16, QT, rows_waves(NB) * 64> queries;
+            Queries<NB, ROWS_TILE, BF16, QT, rows_waves(NB, QT) * 64> queries;
             queries.load(b, seg);
-            __syncthreads();
-            queries.store(b, &sh.q[0][0][0], Sh::PITCH);
-            __syncthreads();
+            auto term = [&](auto y) {
+                constexpr int Y = decltype(y)::value;
+                __syncthreads();
+                queries.template store<Y>(b, &sh.q[0][0], Sh::PITCH);
+                __syncthreads();
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < NB; ++x)
+                        qf[Y][n][x] = *(const bf16x8*)&sh.q[wave * ROWS_WAVE + 16 * n + col][8 * NB * g + 8 * x];
+            };
+            term(Int<0>());
+            if constexpr (QT > 1) term(Int<1>());
+            if constexpr (QT > 2) term(Int<2>());
         }
-        bf16x8 qf[QT][NT][NB];
-#pragma unroll
-        for (int y = 0; y < QT; ++y)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int x = 0; x < NB; ++x)
-                    qf[y][n][x] = *(const bf16x8*)&sh.q[y][wave * ROWS_WAVE + 16 * n + col][8 * NB * g + 8 * x];
 
         // the keys that each of the lane's rows sees; those that all of the wave's see, and that any does
         int last[NT], low[NT];
@@ -1100,13 +1112,13 @@ __global__ __launch_bounds__(rows_waves(NB) * 64, NB == 8 ? 1 : 2) void attentio
             const int page_k = max(page_of(pages, 4 * j_in + (col >> 2)), 0);
             const uint8_t* codes = in_page(my.k, page_k, a.code_page) + (ok + 4 * t_in) * row_bytes;
             const uint8_t* scales = in_page(my.ks, page_k, a.scale_page) + ok + 4 * t_in + (col & 3);
-            if constexpr (NB == 2) {
-                const uint2 w = *(const uint2*)codes;
+            if constexpr (KX == 2) {
+                const uint2 w = *(const uint2*)(codes + 8 * k_part);
                 kc[0] = w.x;
                 kc[1] = w.y;
                 kb = *scales;
             } else {
-                const int more = my.half(k_part);
+                const int more = NB == 8 ? my.half(k_part) : 0;
                 const uint4 w = *(const uint4*)(codes + 16 * more);
                 kc[0] = w.x;
                 kc[1] = w.y;
@@ -1241,12 +1253,15 @@ __global__ __launch_bounds__(rows_waves(NB) * 64, NB == 8 ? 1 : 2) void attentio
                     const float safe = top[n] == -__builtin_inff() ? 0.0f : top[n];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], scale, -safe));
-                        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i + 1], scale, -safe));
+                        float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i], scale, -safe));
+                        float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * i + 1], scale, -safe));
                         sum[n] += e0 + e1;
-                        const uint32_t w = pack(e0, e1);
-                        p[n][i >> 2][0][i & 3] = w;
-                        if constexpr (PT == 2) p[n][i >> 2][PT - 1][i & 3] = pack(e0 - bf16lo(w), e1 - bf16hi(w));
+#pragma unroll
+                        for (int y = 0; y < PT; ++y) {
+                            const uint32_t w = p[n][i >> 2][y][i & 3] = pack(e0, e1);
+                            e0 -= bf16lo(w);
+                            e1 -= bf16hi(w);
+                        }
                     }
                 }
                 if (__builtin_amdgcn_readfirstlane(sh.work.odd[buf][0] | sh.work.odd[buf][1])) {
@@ -1464,15 +1479,15 @@ Shape shape_of(const CacheView& c, int64_t tokens, int q_heads, int max_queries,
 template <int NB, int NT, bool EXACT>
 void launch_main(const AttentionArgs& a, bool bf16, dim3 grid, hipStream_t s) {
     const dim3 block(WAVES * 64);
-    if (!bf16) hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, false, 2, 2>), grid, block, 0, s, a);
+    if (!bf16) hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, false, 3, 3>), grid, block, 0, s, a);
     else if (a.cache.rht) hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, true, 2, 1>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((attention_kernel<NB, NT, EXACT, true, 1, 1>), grid, block, 0, s, a);
 }
 
 template <int NB, bool EXACT>
 void launch_rows(const AttentionArgs& a, bool bf16, dim3 grid, hipStream_t s) {
-    const dim3 block(rows_waves(NB) * 64);
-    if (!bf16) hipLaunchKernelGGL((attention_rows_kernel<NB, EXACT, false, 2, 2>), grid, block, 0, s, a);
+    const dim3 block(rows_waves(NB, 1) * 64);
+    if (!bf16) hipLaunchKernelGGL((attention_rows_kernel<NB, EXACT, false, 3, 3>), grid, dim3(rows_waves(NB, 3) * 64), 0, s, a);
     else if (a.cache.rht) hipLaunchKernelGGL((attention_rows_kernel<NB, EXACT, true, 2, 1>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((attention_rows_kernel<NB, EXACT, true, 1, 1>), grid, block, 0, s, a);
 }
