@@ -496,7 +496,14 @@ __device__ __forceinline__ float scale_of(uint32_t word, int byte) {       // by
 // Keys of a wave's 64: 32 j + 8 g + 4 t + i is row 4 g + i of score product
 // (j, t).  Lane l: column l & 15, group g = l >> 4.
 // NB: blocks of 32 that a row is padded to (2, 4, 8); NT: products of 16 rows.
-// QT: terms of q; PT: terms of p.
+// QT: terms of q, PT: terms of p, in bf16: one each for bf16 rows (p's half step
+// of 2^-9 is that of the output), two of q where it was transformed (then it is
+// no bf16 any more), three for fp32 rows (with two, an output's error is 3.3e-6 of
+// its norm, with three 3e-7).
+// Bound by HBM: 64 requests of up to 16384 tokens, 8 heads of 128, 131 us (4.5
+// TB/s); one of 262144 tokens 53 us (5.5).  Keys and values go from memory to
+// registers to the products, no byte through LDS, and a step's loads are sent
+// for during the step before.
 // ---------------------------------------------------------------------------
 template <int NB, int NT, int QT>
 struct Shared {
@@ -980,11 +987,15 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 // ---------------------------------------------------------------------------
 // Many rows of a sequence: prompts, drafts of many heads.
 //
-// A tile has 128 rows; a wave takes 32 of them and every key.  The workgroup
-// brings in 64 keys at a time, each wave a quarter: it widens K and V to bf16
-// operands, once for all waves, and puts them into LDS lane by lane as the
-// products read them (no bank conflicts).  Two buffers; the next unit's is
-// filled while this one's is read.  Products as in attention_kernel.
+// A tile has 128 rows; a wave takes 32 of them (16 where more do not fit the
+// registers) and every key.  The workgroup brings in 64 keys at a time, each wave
+// its part: it widens K and V to bf16 operands, once for all waves, and puts them
+// into LDS lane by lane as the products read them (no bank conflicts).  Two
+// buffers; the next unit's is filled while this one's is read.  Products as in
+// attention_kernel.  Bound by the vector instructions (exponentials, sums,
+// widening) beside the products: 2 x 4096 queries behind 4096 tokens, 32 heads of
+// 128, 530 us and 20 for the join, 780 TFLOP/s; 2 x 2048 behind 2048, 32 heads of
+// 256, 543 us, 760 TFLOP/s (1125 us with 32 rows a wave, whose registers spill).
 //
 // (K's codes could enter a block-scaled product as they are, with q as a sum of
 // e4m3 terms.  Within 16 elements that product aligns its terms to the largest
@@ -1471,7 +1482,7 @@ Shape shape_of(const CacheView& c, int64_t tokens, int q_heads, int max_queries,
     s.head_tiles = (group + r - 1) / r;
     s.tile_tokens = 1;
     while (2 * s.tile_tokens * s.tile_heads <= r) s.tile_tokens *= 2;
-    s.shares = s.nt == 1 && s.nb < 8 ? 768 : 512;
+    s.shares = s.nt == 1 && s.nb < 8 ? 768 : 512;          // the workgroups that the chip holds at once: 3 or 2 a CU
     s.part_floats = (int64_t)r * (32 * s.nb + 2);
     return s;
 }
