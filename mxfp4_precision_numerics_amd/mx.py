@@ -79,22 +79,22 @@ def lib():
         L.mx_grad_workspace.restype = i64
         L.mx_grad_norm.argtypes = [P, P, P, i32, P, P, P]
         L.mx_grad_clip.argtypes = [P, P, P, i32, P, f32, P, P, P]
-        L.mx_balance_workspace.argtypes = [i64, i32]
-        L.mx_balance_workspace.restype = i64
-        L.mx_balance.argtypes = [P, c_int, i64, i32, i64, c_int, P, i32, P, P, P, P, P]
-        L.mx_balance_bwd.argtypes = [P, c_int, i64, i32, i64, c_int, P, P, f32, P, i64, P, i64, P]
-        L.mx_cache_write.argtypes = [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]
-        L.mx_cache_read.argtypes = [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]
-        L.mx_cache_attention_workspace.argtypes = [P, c_int, i64, i32, i32]
-        L.mx_cache_attention_workspace.restype = i64
-        L.mx_cache_attention.argtypes = [P, P, c_int, i64, i32, i64, i64, P, i32, i32, P, i64, i32, P, f32, c_int,
-                                         i32, P, P, i64, i64, P, P, P]
         for name in ("mx_rht", "mx_quantize_1d", "mx_quantize_2d", "mx_quantize_2d_deosc", "mx_dequantize",
                      "mx_quantize_1d_ex", "mx_dequantize_1d_ex", "mx_quantize_1d_dual",
                      "mx_grouped_gemm", "mx_grouped_gemm_q", "mx_route", "mx_route_bwd", "mx_route_plan",
-                     "mx_combine", "mx_combine_bwd", "mx_grad_norm", "mx_grad_clip", "mx_balance", "mx_balance_bwd",
-                     "mx_cache_write", "mx_cache_read", "mx_cache_attention"):
+                     "mx_combine", "mx_combine_bwd", "mx_grad_norm", "mx_grad_clip"):
             getattr(L, name).restype = c_int
+        for name, restype, argtypes in (
+                ("mx_balance_workspace", i64, [i64, i32]),
+                ("mx_balance", c_int, [P, c_int, i64, i32, i64, c_int, P, i32, P, P, P, P, P]),
+                ("mx_balance_bwd", c_int, [P, c_int, i64, i32, i64, c_int, P, P, f32, P, i64, P, i64, P]),
+                ("mx_cache_write", c_int, [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]),
+                ("mx_cache_read", c_int, [P, P, i64, i64, P, i64, i64, c_int, i64, P, P]),
+                ("mx_cache_attention_workspace", i64, [P, c_int, i64, i32, i32]),
+                ("mx_cache_attention", c_int, [P, P, c_int, i64, i32, i64, i64, P, i32, i32, P, i64, i32, P, f32, c_int,
+                                               i32, P, P, i64, i64, P, P, P])):
+            if hasattr(L, name):      # (not in a library built of the other sources alone)
+                getattr(L, name).restype, getattr(L, name).argtypes = restype, argtypes
         _lib = L
     return _lib
 
