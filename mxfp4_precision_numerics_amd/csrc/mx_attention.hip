@@ -7,6 +7,7 @@
 #include "mx_cache.h"
 #include "mx_device.h"
 #include "mx_host.h"
+#include "mx_line.h"
 
 namespace {
 
@@ -38,7 +39,6 @@ struct AttentionArgs {
 };
 
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
-constexpr int UNIT = 64;              // keys that a wave takes at a time
 constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
 constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least, where segments are cut
 constexpr int WHOLE_UNITS = 16;       // of a segment that is not cut
@@ -84,11 +84,6 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
 }
 
-struct Seq {
-    int64_t row0;             // its first query row
-    int n, len;               // queries, keys
-};
-
 __device__ __forceinline__ Seq load_seq(const AttentionArgs& a, int s) {
     Seq q;
     int64_t b = s, e = s + 1;
@@ -100,65 +95,6 @@ __device__ __forceinline__ Seq load_seq(const AttentionArgs& a, int s) {
     q.n = (int)(e - b);
     q.len = (int)min(max((int64_t)load_global<int32_t>(a.lengths + s), (int64_t)0), a.capacity);
     return q;
-}
-
-// Of a sequence's tile i: the first unit that its rows see, and the one after
-// the last (a tile whose rows see nothing still has one).
-__device__ __forceinline__ int first_unit(const AttentionArgs& a, const Seq& q, int i) {
-    return a.window ? max(q.len - q.n + i * a.tile_tokens - a.window + 1, 0) / UNIT : 0;
-}
-__device__ __forceinline__ int end_unit(const AttentionArgs& a, const Seq& q, int i) {
-    const int hi = a.causal ? q.len - q.n + min((i + 1) * a.tile_tokens, q.n) : q.len;
-    return max((hi + UNIT - 1) / UNIT, 1);
-}
-__device__ __forceinline__ int tiles_of(const AttentionArgs& a, const Seq& q) {
-    return (q.n + a.tile_tokens - 1) >> a.tile_log2;
-}
-
-// Units of a sequence's first x tiles, all of them full ones: sums over the
-// tiles of their ends less their begins.  With t tokens a tile, t <= 64 and Q =
-// 64 / t, tile i ends at ceil((b + i + 1) / Q) and begins at floor((c + i) / Q)
-// for b and c made of the sequence's lengths; with t = 64 C at A + (i + 1) C and
-// B + i C.  Ends are 1 at least, begins 0.
-__device__ __forceinline__ int64_t sum_ceil(int64_t y, int q_log2) {       // over j = 1 .. y
-    const int64_t w = y >> q_log2, r = y - (w << q_log2);
-    return ((w * (w + 1) >> 1) << q_log2) + r * (w + 1);
-}
-__device__ __forceinline__ int64_t sum_floor(int64_t y, int q_log2) {      // over j = 0 .. y - 1
-    const int64_t w = y >> q_log2, r = y - (w << q_log2);
-    return ((w * (w - 1) >> 1) << q_log2) + r * w;
-}
-__device__ __forceinline__ int64_t units_before(const AttentionArgs& a, const Seq& q, int x) {
-    if (x == 0) return 0;
-    if (!a.causal) return (int64_t)x * end_unit(a, q, 0);
-    const int64_t at = q.len - q.n, low = at - a.window + 1;
-    int64_t units;
-    if (a.tile_log2 <= 6) {
-        const int q_log2 = 6 - a.tile_log2;
-        const int64_t b = (at + a.tile_tokens - 1) >> a.tile_log2;
-        units = min((int64_t)x, max(-b, (int64_t)0));                      // tiles before the first key: one each
-        units += sum_ceil(max(b + x, (int64_t)0), q_log2) - sum_ceil(max(b, (int64_t)0), q_log2);
-        if (a.window) {
-            const int64_t c = low >> a.tile_log2;
-            units -= sum_floor(max(c + x, (int64_t)0), q_log2) - sum_floor(max(c, (int64_t)0), q_log2);
-        }
-    } else {
-        const int c_log2 = a.tile_log2 - 6;
-        const int64_t n = x, end0 = (at + UNIT - 1) >> 6;
-        const int64_t ones = min(n, max((1 - end0) >> c_log2, (int64_t)0));
-        units = ones + (n - ones) * end0 + (((n * (n + 1) - ones * (ones + 1)) >> 1) << c_log2);
-        if (a.window) {
-            const int64_t begin0 = low >> 6;
-            const int64_t none = min(n, max((-begin0 + (1 << c_log2) - 1) >> c_log2, (int64_t)0));
-            units -= (n - none) * begin0 + (((n * (n - 1) - none * (none - 1)) >> 1) << c_log2);
-        }
-    }
-    return units;
-}
-__device__ __forceinline__ int64_t units_of(const AttentionArgs& a, const Seq& q) {
-    const int tiles = tiles_of(a, q);
-    if (tiles == 0) return 0;
-    return units_before(a, q, tiles - 1) + end_unit(a, q, tiles - 1) - first_unit(a, q, tiles - 1);
 }
 
 // The line's length, and where one unit of it lies: each thread has a stretch
@@ -319,7 +255,7 @@ __device__ __forceinline__ bool row_of(const AttentionArgs& a, const Segment& g,
     r.query = (g.tile << a.tile_log2) + t;
     r.token = g.seq.row0 + r.query;
     r.head = part * a.group + h;
-    return t < a.tile_tokens && h < a.group && r.query < g.seq.n;
+    return t < a.tile_tokens && h < a.group && t < g.seq.n - (g.tile << a.tile_log2);
 }
 
 // ---------------------------------------------------------------------------
@@ -745,13 +681,13 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
         for (int n = 0; n < NT; ++n) {
             Row r;
             const bool live = row_of(a, seg, 16 * n + col, r);
-            const int pos = seg.seq.len - seg.seq.n + r.query;
+            const int pos = position(seg.seq, r.query);
             last[n] = !live ? -1 : a.causal ? pos : seg.seq.len - 1;
-            low[n] = a.window ? pos - a.window + 1 : 0;
+            low[n] = first_key(a, pos);
         }
-        const int pos0 = seg.seq.len - seg.seq.n + (seg.tile << a.tile_log2);
-        const int all_to = a.causal ? pos0 : seg.seq.len - 1;
-        const int all_from = a.window ? pos0 + rows / a.tile_heads - 1 - a.window + 1 : 0;
+        const int query0 = seg.tile << a.tile_log2;
+        const int all_to = a.causal ? position(seg.seq, query0) : seg.seq.len - 1;
+        const int all_from = first_key(a, position(seg.seq, query0 + rows / a.tile_heads - 1));
 
         f32x4 acc[NT][M];
         float top[NT], sum[NT];
@@ -1078,18 +1014,19 @@ __global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 
         for (int n = 0; n < NT; ++n) {
             Row r;
             const bool live = row_of(a, seg, wave * ROWS_WAVE + 16 * n + col, r);
-            const int pos = seg.seq.len - seg.seq.n + r.query;
+            const int pos = position(seg.seq, r.query);
             last[n] = !live ? -1 : a.causal ? pos : seg.seq.len - 1;
-            low[n] = a.window ? pos - a.window + 1 : 0;
+            low[n] = first_key(a, pos);
         }
-        const int pos0 = seg.seq.len - seg.seq.n + (seg.tile << a.tile_log2);
+        const int query0 = seg.tile << a.tile_log2;
         const int first_token = wave * ROWS_WAVE / a.tile_heads;
         const int last_token = min((wave * ROWS_WAVE + ROWS_WAVE - 1) / a.tile_heads, tokens - 1);
         const bool idle = first_token >= tokens;
-        const int all_to = a.causal ? pos0 + first_token : seg.seq.len - 1;
-        const int any_to = idle ? -1 : a.causal ? pos0 + last_token : seg.seq.len - 1;
-        const int all_from = a.window ? pos0 + last_token - a.window + 1 : 0;
-        const int any_from = a.window ? pos0 + first_token - a.window + 1 : 0;
+        const int pos_first = position(seg.seq, query0 + min(first_token, tokens - 1));
+        const int pos_last = position(seg.seq, query0 + last_token);
+        const int all_to = a.causal ? pos_first : seg.seq.len - 1;
+        const int any_to = idle ? -1 : a.causal ? pos_last : seg.seq.len - 1;
+        const int all_from = first_key(a, pos_last), any_from = first_key(a, pos_first);
 
         f32x4 acc[NT][M];
         float top[NT], sum[NT];
@@ -1582,11 +1519,12 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.seqs = seqs;
     a.table = page_table;
     a.table_ld = table_ld ? table_ld : table_pages;
-    a.capacity = (int64_t)table_pages * cache->page_size;
+    a.capacity = c.pages ? (int64_t)table_pages * cache->page_size : 0;
     a.lengths = lengths;
     a.scale = scale * LOG2E;
     a.causal = causal != 0;
-    a.window = window;
+    // (a window of all that a sequence can hold hides nothing, and costs no masks)
+    a.window = window < a.capacity ? window : 0;
     a.sinks = sinks;
     a.out = out;
     a.out_ld = out_ld ? out_ld : row;
@@ -1594,7 +1532,6 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.lse = lse;
     hipStream_t s = (hipStream_t)stream;
     const bool bf16 = qt == MX_BF16;
-    if (c.pages == 0) a.capacity = 0;
     const Shape shape = shape_of(c, tokens, q_heads, max_queries, a.capacity);
     a.group = q_heads / c.heads;
     a.tile_tokens = shape.tile_tokens;
@@ -1609,7 +1546,7 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     // no more workgroups than there can be work for, and no join where no segment can be long enough to be cut
     const int64_t tiles = (tokens / shape.tile_tokens + min(tokens, (int64_t)seqs)) * a.line_heads;
     int64_t longest = max(ceil_div(a.capacity, UNIT), (int64_t)1);
-    if (window) longest = min(longest, ((int64_t)window + shape.tile_tokens) / UNIT + 2);
+    if (a.window) longest = min(longest, ((int64_t)a.window + shape.tile_tokens) / UNIT + 2);
     const bool join = longest > WHOLE_UNITS;
     // (short segments go to workgroups of their own as long as there are any: 32 heads of a prompt of 128 tokens take
     // 13 us, 30 with four units a share)

@@ -1,0 +1,89 @@
+"""The attention's line of units (csrc/mx_line.h) on the host, where it is the
+same arithmetic: the keys that a tile sees and the units before it, against
+sums in 64 bits over the tiles, up to the largest lengths, windows and numbers
+of queries, with the undefined-behaviour sanitizer on."""
+import os
+import subprocess
+import tempfile
+
+import pytest
+
+from mxfp4_precision_numerics_amd import build
+
+PROGRAM = r'''
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include "mx_line.h"
+
+using namespace mx;
+
+struct Args { int causal, window, tile_tokens, tile_log2; };
+
+static void same(long long have, long long want, const char* what, const Args& a, const Seq& q, long long i) {
+    if (have == want) return;
+    printf("%s of tile %lld: %lld, not %lld (causal %d window %d tile %d queries %d keys %d)\n", what, i, have, want,
+           a.causal, a.window, a.tile_tokens, q.n, q.len);
+    exit(1);
+}
+
+static void check(const Args& a, const Seq& q) {
+    const int64_t n = q.n, len = q.len, t = a.tile_tokens, tiles = (n + t - 1) / t;
+    same(tiles_of(a, q), tiles, "tiles", a, q, 0);
+    int64_t sum = 0;
+    const int64_t step = tiles > 5000 ? tiles / 97 : 1;
+    for (int64_t i = 0; i < tiles; i += (i < 50 || i >= tiles - 50 || step == 1) ? 1 : std::min(step, tiles - 50 - i)) {
+        const int64_t pos = len - n + i * t, hi = a.causal ? len - n + std::min((i + 1) * t, n) : len;
+        const int64_t end = std::max<int64_t>((std::max<int64_t>(hi, 0) + 63) / 64, 1);
+        const int64_t begin = a.window ? std::max<int64_t>(pos - a.window + 1, 0) / 64 : 0;
+        same(first_unit(a, q, (int)i), begin, "first unit", a, q, i);
+        same(end_unit(a, q, (int)i), end, "end", a, q, i);
+        if (begin >= end) same(begin, end, "length", a, q, i);
+        for (int64_t row : {i * t, std::min((i + 1) * t, n) - 1}) {
+            same(position(q, (int)row), std::max<int64_t>(len - n + row, -1), "position", a, q, i);
+            const int p = position(q, (int)row);
+            same(first_key(a, p), a.window ? std::max<int64_t>((int64_t)p - a.window + 1, 0) : 0, "first key", a, q, i);
+        }
+        if (step == 1) {
+            same(units_before(a, q, (int)i), sum, "units before", a, q, i);
+            sum += end - begin;
+        } else if (i + 1 < tiles) {
+            same(units_before(a, q, (int)i + 1) - units_before(a, q, (int)i), end - begin, "units", a, q, i);
+        }
+    }
+    if (step == 1) same(units_of(a, q), sum, "units", a, q, tiles);
+}
+
+int main() {
+    std::mt19937 rng(1);
+    auto below = [&](int n) { return (int)(rng() % (unsigned)n); };
+    const int most = 2147483647;
+    for (int causal = 0; causal < 2; ++causal) {
+        for (int log2 = 0; log2 < 8; ++log2) {
+            for (int i = 0; i < 3000; ++i) {
+                const int windows[] = {0, 1 + below(500), 1 + below(70), most, most - below(100), 1 << 30};
+                check(Args{causal, causal ? windows[below(6)] : 0, 1 << log2, log2}, Seq{0, below(300), below(400)});
+            }
+            for (int len : {0, 1, 20, 63, 64, 65, 1 << 20, 1 << 30, most - 64, most - 15, most})
+                for (int n : {0, 1, 2, 3, 40, 1000, 1 << 20, 1 << 30, most - 64, most})
+                    for (int window : {0, 1, 64, 100000, 1 << 30, most - 64, most - 1, most})
+                        if (causal || !window) check(Args{causal, window, 1 << log2, log2}, Seq{0, n, len});
+        }
+    }
+    printf("line ok\n");
+}
+'''
+
+
+@pytest.mark.skipif(not os.path.exists(build.HIPCC), reason="no hipcc")
+def test_tiles_and_units_against_sums_in_64_bits():
+    with tempfile.TemporaryDirectory() as d:
+        src, exe = os.path.join(d, "line.cpp"), os.path.join(d, "line")
+        with open(src, "w") as f:
+            f.write(PROGRAM)
+        r = subprocess.run([build.HIPCC, "-x", "hip", "--offload-host-only", "-O1", "-std=c++17", "-I", build.CSRC,
+                            "-Xarch_host", "-fsanitize=undefined", "-Xarch_host", "-fno-sanitize-recover=all",
+                            src, "-o", exe], capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-3000:]
+        r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and "line ok" in r.stdout, (r.stdout + r.stderr)[-3000:]
