@@ -631,10 +631,15 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
  * causal != 0: the queries are the sequence's last tokens: the i-th of n sees
  * the keys j <= lengths[s] - n + i, with window > 0 only the last `window` of
  * these.  causal == 0: every key (window must be 0).
- * A row that sees no key, or whose denominator is 0, gets out = 0.  Neither a key that a row does not see
- * nor what lies in the cache behind a sequence's length reaches it, whatever
- * its bytes; a non-finite key or value that it sees makes it NaN as the formula
- * says (a value: in its block).
+ * A row that sees no key, or whose denominator is 0, gets out = 0.  Neither a
+ * key that a row does not see nor what lies in the cache behind a sequence's
+ * length reaches it, whatever its bytes.  A key that is not finite makes the rows
+ * that see it NaN, as the formula says, a value elements of its block: NaN, or
+ * the formula's infinity.  (Not finite: all of a block with the scale byte 0xFF;
+ * of blocks with 253 and 254, which mx_cache_write does not leave, the elements
+ * past fp32's range.)
+ * A row's sum of p v is kept relative to its largest score, or to one up to 2^8
+ * smaller: values as near as that to the largest fp32 may overflow in it.
  * sinks (DEVICE fp32[q_heads]) or NULL.  lse [tokens][q_heads] fp32 or NULL:
  * the logarithm of the denominator (-inf where that is 0).
  * out: q's type, out_ld and out_head_ld like q's; it overlaps no input.

@@ -3,6 +3,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/mx.h"
 #include "mx_cache.h"
 #include "mx_device.h"
@@ -481,10 +483,43 @@ __device__ __forceinline__ const uint8_t* in_page(const uint8_t* p, int page, ui
     return p + (uint64_t)(uint32_t)page * bytes;
 }
 
-// Whether one of eight scale bytes is 0xFF.
+// Values that are not finite as bf16 (or fp32): all of a block with the scale
+// byte 0xFF, and with the bytes 253 and 254 (2^126 and 2^127) the codes from 4 and
+// from 2 on.  A row's product must not meet those of keys that it does not see,
+// for 0 times them is NaN.
+// Whether one of eight scale bytes is 253 or more.
 __device__ __forceinline__ bool any_odd(uint2 w) {
-    const uint32_t x = ((w.x & 0x7F7F7F7Fu) + 0x01010101u) & w.x, y = ((w.y & 0x7F7F7F7Fu) + 0x01010101u) & w.y;
+    const uint32_t x = ((w.x & 0x7F7F7F7Fu) + 0x03030303u) & w.x, y = ((w.y & 0x7F7F7F7Fu) + 0x03030303u) & w.y;
     return ((x | y) & 0x80808080u) != 0;
+}
+// Of eight keys' scales those become 0 whose codes (the lane's, WORDS each) are
+// not all finite; a bit each says which.
+template <int WORDS>
+__device__ __forceinline__ uint32_t take_out(uint2& scales, const uint32_t (&codes)[8][WORDS]) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t& w = i < 4 ? scales.x : scales.y;
+        const uint32_t byte = (w >> (8 * (i & 3))) & 0xFFu;
+        uint32_t two = 0, four = 0;                        // magnitudes of 2 or more, of 4 or more
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) {
+            two |= codes[i][k] & 0x44444444u;
+            four |= codes[i][k] & (codes[i][k] << 1) & 0x44444444u;
+        }
+        if (byte == 0xFFu || (byte == 0xFEu && two) || (byte == 0xFDu && four)) {
+            w &= ~(0xFFu << (8 * (i & 3)));
+            out |= 1u << i;
+        }
+    }
+    return out;
+}
+// Eight bits as an operand: 1 where a bit is set.
+__device__ __forceinline__ bf16x8 ones(uint32_t b) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ((b >> (2 * i)) & 1u) * 0x3F80u | ((b >> (2 * i + 1)) & 1u) * 0x3F800000u;
+    return operand(w[0], w[1], w[2], w[3]);
 }
 
 // Whether a row that sees the keys low .. last sees key from + i.
@@ -782,26 +817,16 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
                     // A value that is not finite reaches the rows that see it, and no others: its scale becomes 0
                     // here, and a product of the marks "not finite" and "seen" says where there was one.
                     if (__any(any_odd(scales))) {
-                        uint32_t mark[4] = {0, 0, 0, 0};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            uint32_t& w = i < 4 ? scales.x : scales.y;
-                            const uint32_t byte = 0xFFu << (8 * (i & 3));
-                            if ((w & byte) == byte) {
-                                w &= ~byte;
-                                mark[i >> 1] |= 0x3F80u << (16 * (i & 1));
-                            }
-                        }
+                        const bf16x8 mark = ones(take_out(scales, vc[j]));
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            uint32_t seen[4] = {0, 0, 0, 0};
+                            uint32_t seen = 0;
                             int from = key0 + 32 * j + 8 * g;
                             asm volatile("" : "+v"(from));     // (the comparisons made above are not kept for this)
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                if (sees(last[n], low[n], from, i) && !bad) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
-                            const f32x4 hit = mfma(operand(mark[0], mark[1], mark[2], mark[3]),
-                                                   operand(seen[0], seen[1], seen[2], seen[3]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+                                if (sees(last[n], low[n], from, i) && !bad) seen |= 1u << i;
+                            const f32x4 hit = mfma(mark, ones(seen), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 if (hit[i] == 0.0f) continue;
@@ -945,15 +970,17 @@ struct Int { static constexpr int value = I; };
 
 template <int NB, int QT>
 struct RowsShared {
-    static constexpr int M = 2 * NB;
+    static constexpr int M = 2 * NB, V_PARTS = rows_waves(NB, QT) / 2;
+    typedef std::conditional_t<V_PARTS == 2, int, int64_t> Odd;    // of a buffer, a byte each
     static constexpr int PITCH = 32 * NB + 8;                  // of q, in bf16
     static constexpr int K_BYTES = 4 * NB * 1024, V_BYTES = 2 * M * 1024;
     union {
         alignas(16) __bf16 q[ROWS_TILE][PITCH];            // one term at a time
         struct {
             alignas(16) unsigned char k[2][K_BYTES], v[2][V_BYTES];
-            alignas(16) unsigned char marks[2][2][1024];
-            int odd[2][2];
+            // values that are not finite: of each wave that brought some in, a lane's keys as bits; whether there are any
+            unsigned char marks[2][2][V_PARTS][64];
+            alignas(8) unsigned char odd[2][2][V_PARTS];
         } work;
     };
     Line line;
@@ -1051,7 +1078,7 @@ __global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 
         // half of them (k_part), and of V 32 keys, a half or a quarter of each lane's elements
         const int k_in = wave / PARTS, k_part = wave % PARTS, j_in = k_in >> 1, t_in = k_in & 1;
         const int v_part = wave % (2 * PARTS);
-        uint32_t kc[KX], vc[8];
+        uint32_t kc[KX], vc[8][1];
         int kb;
         uint2 vs;
         const Lane<NB, EXACT> my(a, head, col, g);
@@ -1079,9 +1106,9 @@ __global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 
             const uint8_t* from = in_page(my.v, page_v, a.code_page) + ov * row_bytes + v_part * KV;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if constexpr (KV == 1) vc[i] = from[i * row_bytes];
-                else if constexpr (KV == 2) vc[i] = *(const uint16_t*)(from + i * row_bytes);
-                else vc[i] = *(const uint32_t*)(from + i * row_bytes);
+                if constexpr (KV == 1) vc[i][0] = from[i * row_bytes];
+                else if constexpr (KV == 2) vc[i][0] = *(const uint16_t*)(from + i * row_bytes);
+                else vc[i][0] = *(const uint32_t*)(from + i * row_bytes);
             }
             vs = *(const uint2*)(in_page(my.vs, page_v, a.scale_page) + ov);
         };
@@ -1092,22 +1119,13 @@ __global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 
                 widen8(kc[x], scale_operand((uint32_t)kb), u);
                 *(uint4*)&sh.work.k[buf][((k_in * NB + k_part * KX + x) * 64 + lane) * 16] = make_uint4(u[0], u[1], u[2], u[3]);
             }
-            // a value that is not finite: its scale becomes 0, and a mark says where it was
+            // values that are not finite: their scale becomes 0, and a mark says where they were
             const bool any = __any(any_odd(vs));
             if (any) {
-                uint32_t mark[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t& w = i < 4 ? vs.x : vs.y;
-                    const uint32_t byte = 0xFFu << (8 * (i & 3));
-                    if ((w & byte) == byte) {
-                        w &= ~byte;
-                        mark[i >> 1] |= 0x3F80u << (16 * (i & 1));
-                    }
-                }
-                if (v_part == 0) *(uint4*)&sh.work.marks[buf][j_in][lane * 16] = make_uint4(mark[0], mark[1], mark[2], mark[3]);
+                const uint32_t out = take_out(vs, vc);
+                sh.work.marks[buf][j_in][v_part][lane] = (unsigned char)out;
             }
-            if (v_part == 0 && lane == 0) sh.work.odd[buf][j_in] = any;
+            if (lane == 0) sh.work.odd[buf][j_in][v_part] = any;
             float sc[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) sc[i] = scale_of(i < 4 ? vs.x : vs.y, i & 3);
@@ -1115,7 +1133,7 @@ __global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 
             for (int b = 0; b < KV; ++b) {
                 uint32_t u[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = widen2(vc[i], sc[i], b);
+                for (int i = 0; i < 8; ++i) u[i] = widen2(vc[i][0], sc[i], b);
 #pragma unroll
                 for (int second = 0; second < 2; ++second) {
                     const uint32_t sel = second ? 0x07060302u : 0x05040100u;
@@ -1212,25 +1230,30 @@ __global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 
                         }
                     }
                 }
-                if (__builtin_amdgcn_readfirstlane(sh.work.odd[buf][0] | sh.work.odd[buf][1])) {
+                typedef typename Sh::Odd Odd;
+                const Odd odd = uniform(*(const Odd*)&sh.work.odd[buf][0][0]);
+                if (odd) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        if (!__builtin_amdgcn_readfirstlane(sh.work.odd[buf][j])) continue;
-                        const uint4 mark = *(const uint4*)&sh.work.marks[buf][j][lane * 16];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            uint32_t seen[4] = {0, 0, 0, 0};
-                            int from = key0 + 32 * j + 8 * g;
-                            asm volatile("" : "+v"(from));     // (the comparisons made above are not kept for this)
+                        for (int part = 0; part < Sh::V_PARTS; ++part) {
+                            if (!((odd >> (8 * (j * Sh::V_PARTS + part))) & 1)) continue;
+                            const bf16x8 mark = ones(sh.work.marks[buf][j][part][lane]);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (sees(last[n], low[n], from, i) && !bad[j]) seen[i >> 1] |= 0x3F80u << (16 * (i & 1));
-                            const f32x4 hit = mfma(operand(mark.x, mark.y, mark.z, mark.w),
-                                                   operand(seen[0], seen[1], seen[2], seen[3]), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+                            for (int n = 0; n < NT; ++n) {
+                                uint32_t seen = 0;
+                                int from = key0 + 32 * j + 8 * g;
+                                asm volatile("" : "+v"(from)); // (the comparisons made above are not kept for this)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                                for (int i = 0; i < 8; ++i)
+                                    if (sees(last[n], low[n], from, i) && !bad[j]) seen |= 1u << i;
+                                const f32x4 hit = mfma(mark, ones(seen), (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
-                                for (int k = 0; k < M; ++k) acc[n][k][i] = hit[i] == 0.0f ? acc[n][k][i] : __builtin_nanf("");
+                                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                    for (int k = 2 * KV * part; k < 2 * KV * (part + 1); ++k)
+                                        acc[n][k][i] = hit[i] == 0.0f ? acc[n][k][i] : __builtin_nanf("");
+                            }
                         }
                     }
                 }

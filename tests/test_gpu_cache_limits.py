@@ -1,10 +1,11 @@
 """GPU: the attention over the MXFP4 cache at the ends of what its arguments
-may be: windows up to 2^31 - 1.  Compared, and with the tolerances, as in
-test_gpu_cache.py."""
+may be: windows up to 2^31 - 1, every scale byte in what a row does not see.
+Compared, and with the tolerances, as in test_gpu_cache.py."""
 import numpy as np
 import pytest
 
 from gpu_util import torch
+from oracle import cache as ref
 from test_gpu_cache import Setup
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +33,77 @@ def test_sequences_without_keys_beside_others(window):
     got = s.call(window=window)
     s.check(got, s.want(window=min(window, 10 ** 6)))
     assert (got[0][:41] == 0).all() and bool(tt.isneginf(got[1][:41]).all())
+
+
+def same(a, b):
+    return all(np.array_equal(x.float().cpu().numpy(), y.float().cpu().numpy(), equal_nan=True) for x, y in zip(a, b))
+
+
+def fill(s, slots, byte, codes):
+    for c, sc in ((0, 1), (2, 3)):
+        s.cache_host[c][slots // s.page, :, slots % s.page] = codes
+        s.cache_host[sc][slots // s.page, :, :, slots % s.page] = byte
+
+
+# scale bytes from which on some codes, or all, pass the range of fp32; codes of 6, 4, -2 and 2, 0.5
+BYTES = [(253, 0x77), (253, 0x66), (254, 0x77), (254, 0xC4), (254, 0x11), (255, 0x77), (255, 0x00)]
+
+
+@pytest.mark.parametrize("byte, codes", BYTES)
+@pytest.mark.parametrize("queries", [None, [3, 70, 2], [1, 5, 4]])
+@pytest.mark.parametrize("dim, kind, rht", [(64, "bf16", False), (96, "f32", True), (128, "bf16", True), (160, "bf16", False),
+                                            (256, "f32", False)])
+def test_bytes_that_no_row_sees(dim, kind, rht, queries, byte, codes):
+    """Behind a sequence's length, before a window, and in the page that stands
+    in for one that does not exist."""
+    s = Setup([70, 200, 5], 2, 2, dim, 16, kind, rht, queries=queries, seed=303)
+    missing = np.argwhere(s.table == 0)
+    for at in [tuple(m) for m in missing] or [(1, 4)]:
+        s.table[at] = -1
+    known = None if queries is None else max(queries)
+    want, far = s.call(max_queries=known), s.call(max_queries=known, window=20)
+    s.check(want, s.want())
+    s.check(far, s.want(window=20))
+    pages = len(s.cache_host[0])
+    kept, kept_far = set(), set()
+    for row, n, count in zip(s.table, s.lengths, s.queries):
+        slots = ref.token_slots(row, int(n), 16, pages).tolist()
+        kept |= set(slots)
+        kept_far |= set(slots[max(0, int(n) - count - 19):])
+    clean = [a.copy() for a in s.cache_host]
+    fill(s, np.setdiff1d(np.arange(pages * 16), list(kept)), byte, codes)
+    assert same(s.call(max_queries=known), want)
+    s.cache_host = clean
+    fill(s, np.setdiff1d(np.arange(pages * 16), list(kept_far)), byte, codes)
+    assert same(s.call(max_queries=known, window=20), far)
+
+
+@pytest.mark.parametrize("byte, codes", BYTES)
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("dim, kind, group", [(64, "bf16", 2), (128, "bf16", 2), (128, "f32", 1), (256, "bf16", 2), (32, "bf16", 4)])
+@pytest.mark.parametrize("known", [True, False])
+def test_values_that_some_rows_see(known, dim, kind, group, window, byte, codes):
+    """A block of a value: rows that do not see it, and the other blocks of those
+    that do, keep their bits."""
+    s = Setup([100], 2, group, dim, 16, kind, queries=[8 if known else 90], seed=304)
+    n = s.queries[0]
+    key = 96 if known else 41
+    args = dict(window=window, scale=1e-3, max_queries=n if known else None)     # (every p about the same)
+    slot = int(ref.token_slots(s.table[0], key + 1, 16, len(s.cache_host[0]))[-1])
+    block = dim // 32 - 1
+    s.cache_host[3][slot // 16, 1, block, slot % 16] = 0
+    want = s.call(**args)
+    s.cache_host[2][slot // 16, 1, slot % 16, 16 * block:16 * block + 16] = codes
+    s.cache_host[3][slot // 16, 1, block, slot % 16] = byte
+    got = s.call(**args)
+    pos = np.arange(n) + 100 - n
+    seen = (pos >= key) & ((pos < key + window) | (window == 0))
+    assert seen.any() and not seen.all()
+    touched = np.zeros(got[0].shape, dtype=bool)
+    touched[seen, group:, 32 * block:] = True
+    have, kept = got[0].float().cpu().numpy(), want[0].float().cpu().numpy()
+    assert np.array_equal(have[~touched], kept[~touched]) and same(got[1:], want[1:])
+    if byte < 255 and codes == 0x11:
+        s.check(got, s.want(window=window, scale=1e-3))    # finite: 2^125 and 2^126
+    else:
+        assert not np.isfinite(have[touched]).any()
