@@ -640,8 +640,9 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
  * past fp32's range.)
  * A row's sum of p v is kept relative to its largest score, or to one up to 2^8
  * smaller: values as near as that to the largest fp32 may overflow in it.
- * sinks (DEVICE fp32[q_heads]) or NULL.  lse [tokens][q_heads] fp32 or NULL:
- * the logarithm of the denominator (-inf where that is 0).
+ * sinks (DEVICE fp32[q_heads], any values: -inf adds nothing, +inf makes the
+ * head's rows 0) or NULL.  lse [tokens][q_heads] fp32 or NULL: the logarithm of
+ * the denominator (-inf where that is 0).
  * out: q's type, out_ld and out_head_ld like q's; it overlaps no input.
  * Scores, the softmax's statistics and sums are fp32.  bf16 queries enter the
  * products as they are; transformed, as a sum of two bf16 (2^-17 relative); fp32

@@ -40,7 +40,7 @@ struct AttentionArgs {
     Cut* cuts;                    // one a share
 };
 
-constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
+constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f, MAX_FLOAT = 3.40282347e38f;
 constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
 constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least, where segments are cut
 constexpr int WHOLE_UNITS = 16;       // of a segment that is not cut
@@ -260,6 +260,30 @@ __device__ __forceinline__ bool row_of(const AttentionArgs& a, const Segment& g,
     return t < a.tile_tokens && h < a.group && t < g.seq.n - (g.tile << a.tile_log2);
 }
 
+// A row's maximum, sum and the factor of its sums with its head's sink logit.
+// Times log2 e a sink near the largest fp32, or infinite, is held at that: less a
+// finite maximum it is no NaN, and every other p is 0 next to it.
+struct Sink {
+    float top, sum, factor;
+
+    __device__ __forceinline__ Sink(const AttentionArgs& a, const Row& r, bool live, float t, float s)
+        : top(t), sum(s), factor(1.0f) {
+        if (!a.sinks) return;
+        const float x = live ? load_global<float>(a.sinks + r.head) : 0.0f;
+        float sink = x * LOG2E;
+        if (__builtin_isinf(sink) && x != -__builtin_inff()) sink = __builtin_copysignf(MAX_FLOAT, x);
+        top = fmaxf(t, sink);
+        const float safe = top == -__builtin_inff() ? 0.0f : top;
+        factor = __builtin_amdgcn_exp2f(t - safe);
+        sum = s * factor + __builtin_amdgcn_exp2f(sink - safe);
+    }
+    __device__ __forceinline__ void store_lse(const AttentionArgs& a, const Row& r) const {
+        float l = sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2;
+        if (a.sinks && fabsf(top) == MAX_FLOAT) l = load_global<float>(a.sinks + r.head);      // (held, and alone)
+        store_global(a.lse + r.token * a.q_heads + r.head, l);
+    }
+};
+
 // ---------------------------------------------------------------------------
 // Eight elements of a row from the tile's sums: the sink, the division, the
 // transform back, the rounding.  top, sum: the row's maximum (times log2 e) and
@@ -269,17 +293,14 @@ __device__ __forceinline__ bool row_of(const AttentionArgs& a, const Segment& g,
 template <bool BF16>
 __device__ __forceinline__ void finish(const AttentionArgs& a, const Row& r, bool live, int d, float* o, float top,
                                        float sum) {
+    const Sink all(a, r, live, top, sum);
     if (a.sinks) {
-        const float sink = live ? load_global<float>(a.sinks + r.head) * LOG2E : 0.0f, m = fmaxf(top, sink);
-        const float safe = m == -__builtin_inff() ? 0.0f : m, f = __builtin_amdgcn_exp2f(top - safe);
-        sum = sum * f + __builtin_amdgcn_exp2f(sink - safe);
-        top = m;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= f;
+        for (int i = 0; i < 8; ++i) o[i] *= all.factor;
     }
-    const float inv = 1.0f / sum;
+    const float inv = 1.0f / all.sum;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = sum == 0.0f ? 0.0f : o[i] * inv;
+    for (int i = 0; i < 8; ++i) o[i] = all.sum == 0.0f ? 0.0f : o[i] * inv;
     if (a.cache.rht) {
         rht32_quad(o, (d >> 3) & 3);
         const uint32_t m = a.cache.mask >> (d & 31);
@@ -300,8 +321,7 @@ __device__ __forceinline__ void finish(const AttentionArgs& a, const Row& r, boo
                          (u32x4v){__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
                                   __float_as_uint(o[4 * i + 3])});
     }
-    if (a.lse && d == 0)
-        store_global(a.lse + r.token * a.q_heads + r.head, sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2);
+    if (a.lse && d == 0) all.store_lse(a, r);
 }
 
 // A part in the workspace: sums [rows][32 NB], maxima [rows], sums of p [rows].
@@ -338,17 +358,10 @@ template <int NB, bool BF16>
 __device__ __forceinline__ void finish_row(const AttentionArgs& a, const Row& r, bool live, int d, float* o, float top,
                                            float sum) {
     constexpr int N = 8 * NB;
-    float f = 1.0f;
-    if (a.sinks) {
-        const float sink = live ? load_global<float>(a.sinks + r.head) * LOG2E : 0.0f, m = fmaxf(top, sink);
-        const float safe = m == -__builtin_inff() ? 0.0f : m;
-        f = __builtin_amdgcn_exp2f(top - safe);
-        sum = sum * f + __builtin_amdgcn_exp2f(sink - safe);
-        top = m;
-    }
-    const float inv = f / sum;
+    const Sink all(a, r, live, top, sum);
+    const float inv = all.factor / all.sum;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = sum == 0.0f ? 0.0f : o[i] * inv;
+    for (int i = 0; i < N; ++i) o[i] = all.sum == 0.0f ? 0.0f : o[i] * inv;
     if (a.cache.rht) {
         constexpr int IN = N < 32 ? N : 32;
 #pragma unroll
@@ -383,8 +396,7 @@ __device__ __forceinline__ void finish_row(const AttentionArgs& a, const Row& r,
                                       __float_as_uint(o[i + k + 3])});
         }
     }
-    if (a.lse && d == 0)
-        store_global(a.lse + r.token * a.q_heads + r.head, sum == 0.0f ? -__builtin_inff() : (top + log2f(sum)) * LN2);
+    if (a.lse && d == 0) all.store_lse(a, r);
 }
 
 // The other value of a row of 16 lanes' neighbour (16 lanes on, then 32): of

@@ -1,10 +1,11 @@
 """GPU: the attention over the MXFP4 cache at the ends of what its arguments
-may be: windows up to 2^31 - 1, every scale byte in what a row does not see.
+may be: windows up to 2^31 - 1, every scale byte in what a row does not see,
+sinks up to infinity.
 Compared, and with the tolerances, as in test_gpu_cache.py."""
 import numpy as np
 import pytest
 
-from gpu_util import torch
+from gpu_util import dev, torch
 from oracle import cache as ref
 from test_gpu_cache import Setup
 
@@ -107,3 +108,23 @@ def test_values_that_some_rows_see(known, dim, kind, group, window, byte, codes)
         s.check(got, s.want(window=window, scale=1e-3))    # finite: 2^125 and 2^126
     else:
         assert not np.isfinite(have[touched]).any()
+
+
+@pytest.mark.parametrize("lengths, queries", [([0, 65, 300], None), ([0, 65, 300], [2, 3, 70]), ([2500, 0], [3, 1]),
+                                              ([2500, 0], [60, 2])])
+@pytest.mark.parametrize("kind, rht", [("bf16", True), ("f32", False)])
+def test_large_sinks(lengths, queries, kind, rht):
+    """Times log2 e the second and third pass fp32's range."""
+    s = Setup(lengths, 2, 4, 64, 16, kind, rht, queries=queries, seed=305)
+    sinks = np.array([np.inf, 3e38, np.finfo(np.float32).min, 2e38, -2e38, -np.inf, 1.0, np.nan], dtype=np.float32)
+    out, lse = s.call(sinks=dev(sinks))
+    assert (out[:, 0] == 0).all() and (lse[:, 0] == np.inf).all()
+    assert (out[:, 1] == 0).all() and (lse[:, 1] == float(sinks[1])).all()
+    assert bool(out[:, 7].isnan().all()) and bool(lse[:, 7].isnan().all())
+    finite = sinks.copy()
+    finite[0] = finite[7] = 1.0                            # (checked above)
+    want = s.want(sinks=finite)
+    for w in want:
+        w[:, [0, 7]] = 0.0
+    out[:, [0, 7]], lse[:, [0, 7]] = 0.0, 0.0
+    s.check((out, lse), want)
