@@ -1442,7 +1442,7 @@ struct Shape {
 Shape shape_of(const CacheView& c, int64_t tokens, int q_heads, int max_queries, int64_t capacity) {
     Shape s;
     const int group = q_heads / c.heads;
-    const int64_t most = max_queries > 0 ? min((int64_t)max_queries, tokens) : tokens;
+    const int64_t most = max_queries > 0 ? lesser(max_queries, tokens) : tokens;
     s.nb = c.dim <= 64 ? 2 : c.dim <= 128 ? 4 : 8;
     const int64_t rows = most * group;
     const int64_t tiles = tokens * q_heads / ROWS_TILE;
@@ -1579,15 +1579,15 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     a.cuts = (Cut*)workspace;
     a.parts = (float*)(a.cuts + shape.shares);
     // no more workgroups than there can be work for, and no join where no segment can be long enough to be cut
-    const int64_t tiles = (tokens / shape.tile_tokens + min(tokens, (int64_t)seqs)) * a.line_heads;
-    int64_t longest = max(ceil_div(a.capacity, UNIT), (int64_t)1);
-    if (a.window) longest = min(longest, ((int64_t)a.window + shape.tile_tokens) / UNIT + 2);
+    const int64_t tiles = (tokens / shape.tile_tokens + lesser(tokens, seqs)) * a.line_heads;
+    int64_t longest = greater(ceil_div(a.capacity, UNIT), 1);
+    if (a.window) longest = lesser(longest, ((int64_t)a.window + shape.tile_tokens) / UNIT + 2);
     const bool join = longest > WHOLE_UNITS;
     // (short segments go to workgroups of their own as long as there are any: 32 heads of a prompt of 128 tokens take
     // 13 us, 30 with four units a share)
-    a.min_units = (int)min(max(longest / 4, (int64_t)1), (int64_t)MIN_UNITS);
+    a.min_units = (int)lesser(greater(longest / 4, 1), MIN_UNITS);
     a.near = join && shape.nt;
-    const int shares = (int)min(shape.shares, ceil_div(ceil_div(tiles * longest, a.min_units), 8) * 8);
+    const int shares = shares_of(shape.shares, tiles, longest, a.min_units);
     (void)hipGetLastError();
     if (shape.nb == 2) launch<2>(a, shape.nt, bf16, shares, join, s);
     else if (shape.nb == 4) launch<4>(a, shape.nt, bf16, shares, join, s);

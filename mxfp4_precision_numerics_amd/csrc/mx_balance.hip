@@ -291,7 +291,7 @@ mx_status check_balance(mx_dtype lt, int64_t tokens, int32_t experts, int64_t ld
     return ld && ld < experts ? MX_ERR_SHAPE : MX_OK;
 }
 
-int blocks_of(int64_t tokens) { return (int)min(ceil_div(tokens, 64), (int64_t)MAX_BLOCKS); }
+int blocks_of(int64_t tokens) { return (int)lesser(ceil_div(tokens, 64), MAX_BLOCKS); }
 
 }  // namespace
 

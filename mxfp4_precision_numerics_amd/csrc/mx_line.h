@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mx_host.h"
+
 namespace mx {
 
 constexpr int UNIT = 64;              // keys that a wave takes at a time
@@ -41,10 +43,6 @@ template <class A>
 __host__ __device__ __forceinline__ int tiles_of(const A& a, const Seq& q) {
     return (int)(((uint32_t)q.n + a.tile_tokens - 1) >> a.tile_log2);
 }
-
-// (The runtime's host min and max are of 32 bits, whatever they are given.)
-__host__ __device__ __forceinline__ int64_t lesser(int64_t a, int64_t b) { return b < a ? b : a; }
-__host__ __device__ __forceinline__ int64_t greater(int64_t a, int64_t b) { return a < b ? b : a; }
 
 // Units of a sequence's first x tiles, all of them full ones: sums over the
 // tiles of their ends less their begins.  With t tokens a tile, t <= 64 and Q =
@@ -92,6 +90,13 @@ __host__ __device__ __forceinline__ int64_t units_of(const A& a, const Seq& q) {
     const int tiles = tiles_of(a, q);
     if (tiles == 0) return 0;
     return units_before(a, q, tiles - 1) + end_unit(a, q, tiles - 1) - first_unit(a, q, tiles - 1);
+}
+
+// Workgroups of a launch, a multiple of 8 (one of the XCDs each): no more than
+// there can be work for, at least min_units of `tiles` times up to `longest`
+// units each.
+inline int shares_of(int64_t most, int64_t tiles, int64_t longest, int min_units) {
+    return (int)lesser(most, ceil_div(ceil_div(tiles * longest, min_units), 8) * 8);
 }
 
 }  // namespace mx

@@ -1,7 +1,8 @@
 """The attention's line of units (csrc/mx_line.h) on the host, where it is the
 same arithmetic: the keys that a tile sees and the units before it, against
 sums in 64 bits over the tiles, up to the largest lengths, windows and numbers
-of queries, with the undefined-behaviour sanitizer on."""
+of queries, and the workgroups of a launch, with the undefined-behaviour
+sanitizer on."""
 import os
 import subprocess
 import tempfile
@@ -75,15 +76,55 @@ int main() {
 '''
 
 
-@pytest.mark.skipif(not os.path.exists(build.HIPCC), reason="no hipcc")
-def test_tiles_and_units_against_sums_in_64_bits():
+LAUNCHES = r'''
+#include <cstdio>
+#include "mx_line.h"
+
+int main() {
+    for (long long tiles : {1ll, 7ll, 300ll, 1ll << 20, 1ll << 23, 2147483647ll})
+        for (long long longest : {1ll, 5ll, 1000ll, 1ll << 20, 1ll << 25})
+            for (int min_units = 1; min_units <= 4; ++min_units) {
+                const __int128 groups = ((__int128)tiles * longest + min_units - 1) / min_units;
+                const __int128 want = groups > 512 ? 512 : (groups + 7) / 8 * 8;
+                const int have = mx::shares_of(512, tiles, longest, min_units);
+                if (have == (int)want) continue;
+                printf("%d workgroups, not %d, for %lld tiles of %lld units\n", have, (int)want, tiles, longest);
+                return 1;
+            }
+    printf("launches ok\n");
+}
+'''
+
+
+def run(program):
     with tempfile.TemporaryDirectory() as d:
         src, exe = os.path.join(d, "line.cpp"), os.path.join(d, "line")
         with open(src, "w") as f:
-            f.write(PROGRAM)
+            f.write(program)
         r = subprocess.run([build.HIPCC, "-x", "hip", "--offload-host-only", "-O1", "-std=c++17", "-I", build.CSRC,
                             "-Xarch_host", "-fsanitize=undefined", "-Xarch_host", "-fno-sanitize-recover=all",
                             src, "-o", exe], capture_output=True, text=True)
         assert r.returncode == 0, r.stderr[-3000:]
         r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
-        assert r.returncode == 0 and "line ok" in r.stdout, (r.stdout + r.stderr)[-3000:]
+        assert r.returncode == 0, (r.stdout + r.stderr)[-3000:]
+        return r.stdout
+
+
+pytestmark = pytest.mark.skipif(not os.path.exists(build.HIPCC), reason="no hipcc")
+
+
+def test_tiles_and_units_against_sums_in_64_bits():
+    assert "line ok" in run(PROGRAM)
+
+
+def test_workgroups_of_a_launch():
+    assert "launches ok" in run(LAUNCHES)
+
+
+@pytest.mark.parametrize("source", ["mx_attention.hip", "mx_cache.hip", "mx_balance.hip"])
+def test_host_code_cuts_no_sizes(source):
+    """No 64-bit size becomes one of 32 bits without a cast (the runtime's host
+    min and max take ints)."""
+    r = subprocess.run([build.HIPCC, "--offload-host-only", "-O0", "-std=c++17", "-fPIC", "-c", "-Werror=shorten-64-to-32",
+                        os.path.join(build.CSRC, source), "-o", os.devnull], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
