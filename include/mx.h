@@ -653,7 +653,7 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
  * workspace: mx_cache_attention_workspace(...) bytes, 16-byte aligned, its
  * contents irrelevant before and after; calls that may run at the same time
  * need one each.
- * scale > 0 and finite; tokens * q_heads < 2^31; seqs < 2^24; seqs > 0 where
+ * 0 < scale <= 2^127; tokens * q_heads < 2^31; seqs < 2^24; seqs > 0 where
  * tokens > 0.
  * Errors: MX_ERR_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
  * MX_ERR_LAUNCH.  tokens == 0 launches nothing. */

@@ -41,6 +41,7 @@ struct AttentionArgs {
 };
 
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f, MAX_FLOAT = 3.40282347e38f;
+constexpr float MAX_SCALE = 0x1p127f;  // times log2 e still finite
 constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
 constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least, where segments are cut
 constexpr int WHOLE_UNITS = 16;       // of a segment that is not cut
@@ -1531,7 +1532,7 @@ mx_status mx_cache_attention(const mx_cache* cache, const void* q, mx_dtype qt, 
     if (table_pages < 0 || table_ld < 0 || (table_ld && table_ld < table_pages) ||
         table_pages > INT32_MAX / cache->page_size)
         return MX_ERR_SHAPE;
-    if (max_queries < 0 || window < 0 || (window && !causal) || !(scale > 0.0f) || !(scale - scale == 0.0f))
+    if (max_queries < 0 || window < 0 || (window && !causal) || !(scale > 0.0f) || !(scale <= MAX_SCALE))
         return MX_ERR_SHAPE;
     if (check_pitches(q_ld, q_head_ld, c.dim) != MX_OK || check_pitches(out_ld, out_head_ld, c.dim) != MX_OK)
         return MX_ERR_SHAPE;
