@@ -873,7 +873,13 @@ class KVCache:
     """A paged key/value cache in MXFP4 over four uint8 device tensors (see
     mx_cache): codes [pages, heads, page_size, head_dim // 2] and scales
     [pages, heads, head_dim // 32, page_size], of keys and of values.  With
-    use_rht what it holds is transformed (sign_mask)."""
+    use_rht what it holds is transformed (sign_mask).
+
+    It describes these tensors' storage as it is now: its fields cannot be
+    set, and calls refuse it once a tensor's storage has been replaced."""
+
+    _FIELDS = frozenset(("k_codes", "k_scales", "v_codes", "v_scales", "pages", "heads", "page_size", "head_dim",
+                         "use_rht", "sign_mask", "device_index"))
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, use_rht: bool = False, sign_mask: int = 0):
         torch = _torch()
@@ -884,15 +890,28 @@ class KVCache:
             _shaped(t, (pages, heads, page_size, half), torch.uint8, name)
         for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
             _shaped(t, (pages, heads, half // 16, page_size), torch.uint8, name)
-        self.device_index = k_codes.get_device()
-        if any(t.get_device() != self.device_index for t in (k_scales, v_codes, v_scales)):
+        device = k_codes.get_device()
+        if any(t.get_device() != device for t in (k_scales, v_codes, v_scales)):
             raise ValueError("the cache's tensors are on different devices")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, 2 * half
-        self.use_rht, self.sign_mask = bool(use_rht), int(sign_mask)
-        self._struct = _CacheStruct(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, heads,
-                                    page_size, 2 * half, self.use_rht, self.sign_mask)
-        self._at = ctypes.addressof(self._struct)
+        tensors = (k_codes, k_scales, v_codes, v_scales)
+        at = tuple(t.data_ptr() for t in tensors)
+        struct = _CacheStruct(*[p or None for p in at], pages, heads, page_size, 2 * half, bool(use_rht), int(sign_mask))
+        vars(self).update(k_codes=k_codes, k_scales=k_scales, v_codes=v_codes, v_scales=v_scales, device_index=device,
+                          pages=pages, heads=heads, page_size=page_size, head_dim=2 * half, use_rht=bool(use_rht),
+                          sign_mask=int(sign_mask), _tensors=tensors, _struct=struct, _addresses=at)
+
+    def __setattr__(self, name, value):
+        if name in self._FIELDS:
+            raise AttributeError("a KVCache's %s cannot be set; make another KVCache" % name)
+        super().__setattr__(name, value)
+
+    @property
+    def _at(self):
+        """The address of the mx_cache, for a call."""
+        a, b, c, d = self._tensors
+        if (a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr()) != self._addresses:
+            raise ValueError("the storage of the cache's tensors has been replaced; make another KVCache")
+        return ctypes.addressof(self._struct)
 
 
 def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, use_rht: bool = False, sign_mask: int = 0,
@@ -1006,12 +1025,13 @@ def cache_attention(cache, q, page_table, lengths, scale=None, q_offsets=None, m
         _same(lse, (tokens, q_heads), torch.float32, "lse")
     elif need_lse:
         lse = _new(q.device, torch.float32, tokens, q_heads)
-    need = lib().mx_cache_attention_workspace(cache._at, _dtype_code(q), tokens, q_heads, max_queries)
+    at = cache._at
+    need = lib().mx_cache_attention_workspace(at, _dtype_code(q), tokens, q_heads, max_queries)
     workspace = _workspace(workspace, need, q.device)
     _here(cache.device_index, q=q, page_table=page_table, lengths=lengths, q_offsets=q_offsets, sinks=sinks, out=out,
           lse=lse, workspace=workspace)
     _check("mx_cache_attention", lib().mx_cache_attention(
-        cache._at, _ptr(q), _dtype_code(q), tokens, q_heads, q_ld, q_head, _ptr(q_offsets), max_queries, seqs,
+        at, _ptr(q), _dtype_code(q), tokens, q_heads, q_ld, q_head, _ptr(q_offsets), max_queries, seqs,
         _ptr(page_table), table_ld, table_pages, _ptr(lengths), dim ** -0.5 if scale is None else float(scale),
         int(bool(causal)), window, _ptr(sinks), _ptr(out), out_ld, out_head, _ptr(lse), _ptr(workspace), _stream()))
     return out, lse

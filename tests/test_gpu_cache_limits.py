@@ -166,3 +166,35 @@ def test_as_many_tokens_as_there_can_be(rows, window):
     # the rows before the last see the page without its last tokens, once: less than 130 of 2^30 tokens
     assert (np.abs(out.double().cpu().numpy() - want[0]) <= tol + 130 * 2.0 ** -30 * np.abs(want[0]).max()).all()
     assert (np.abs(lse.double().cpu().numpy() - want[1] - np.log(whole)) <= 2.0 ** -6).all()
+
+
+@pytest.mark.parametrize("name, value", [("use_rht", True), ("sign_mask", 5), ("k_codes", None), ("v_scales", None), ("pages", 1),
+                                         ("head_dim", 32)])
+def test_fields_of_a_cache_cannot_be_set(name, value):
+    cache = mx.kv_cache(4, 2, 16, 64)
+    before = getattr(cache, name)
+    with pytest.raises(AttributeError):
+        setattr(cache, name, value)
+    assert getattr(cache, name) is before
+
+
+@pytest.mark.parametrize("which", ["k_codes", "k_scales", "v_codes", "v_scales"])
+@pytest.mark.parametrize("how", ["data", "set_", "resize_", "storage"])
+def test_a_cache_whose_storage_was_replaced_is_refused(which, how):
+    """By each call, which would use the freed address."""
+    tt = torch()
+    cache = mx.kv_cache(4, 2, 16, 64)
+    x, ints = tt.ones((3, 2, 64), device="cuda"), tt.zeros(3, dtype=tt.int32, device="cuda")
+    t = getattr(cache, which)
+    if how == "data":
+        t.data = t.clone()
+    elif how == "set_":
+        t.set_(tt.zeros_like(t))
+    elif how == "resize_":
+        t.resize_((64,) + tuple(t.shape[1:]))
+    else:
+        t.untyped_storage().resize_(0)
+    for call in (lambda: mx.cache_write(cache, x, x, ints), lambda: mx.cache_read(cache, ints),
+                 lambda: mx.cache_attention(cache, x, tt.zeros((3, 1), dtype=tt.int32, device="cuda"), ints + 1)):
+        with pytest.raises(ValueError, match="storage"):
+            call()
