@@ -1014,6 +1014,9 @@ def cache_attention(cache, q, page_table, lengths, scale=None, q_offsets=None, m
         _same(q_offsets, (seqs + 1,), torch.int32, "q_offsets")
     if max_queries is None:
         max_queries = 1 if q_offsets is None else 0
+    for name, value in (("window", window), ("max_queries", max_queries)):
+        if not 0 <= value < 2 ** 31:
+            raise ValueError("%s must be from 0 to 2^31 - 1" % name)
     if sinks is not None:
         _same(sinks, (q_heads,), torch.float32, "sinks")
     out_ld = out_head = 0

@@ -198,3 +198,12 @@ def test_a_cache_whose_storage_was_replaced_is_refused(which, how):
                  lambda: mx.cache_attention(cache, x, tt.zeros((3, 1), dtype=tt.int32, device="cuda"), ints + 1)):
         with pytest.raises(ValueError, match="storage"):
             call()
+
+
+@pytest.mark.parametrize("name, value", [("window", 2 ** 32 + 5), ("window", 2 ** 31), ("window", -2 ** 32), ("max_queries", 2 ** 32 + 1),
+                                         ("max_queries", -2 ** 32)])
+def test_numbers_past_32_bits_are_refused(name, value):
+    """The first was a window of 5, the second was refused with another reason."""
+    s = Setup([70], 1, 2, 32, 16, seed=308)
+    with pytest.raises((ValueError, mx.MXError), match=name):
+        s.call(**{name: value})
