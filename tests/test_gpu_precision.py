@@ -38,9 +38,9 @@ def bounds(reach, lse):
     return 16 * reach + 42, 8 * reach + 22 + 4 * (np.abs(lse) + reach)
 
 
-def units(dim, length, seed):
+def units(dim, length, seed, width=0):
     """A cache whose pages hold the unit vectors, and a table that has them
-    somewhere within `length` tokens."""
+    somewhere within `length` tokens (and is for `width`)."""
     tt, rng = torch(), np.random.default_rng(seed)
     pages = dim // 16
     cache = mx.kv_cache(pages, 1, 16, dim)
@@ -51,7 +51,7 @@ def units(dim, length, seed):
         t.copy_(tt.from_numpy(codes))
     for t in (cache.k_scales, cache.v_scales):
         t.fill_(127)
-    table = np.full((1, length // 16), -1, dtype=np.int32)
+    table = np.full((1, max(length, width) // 16), -1, dtype=np.int32)
     table[0, np.sort(rng.choice(length // 16, size=pages, replace=False))] = rng.permutation(pages)
     return cache, dev(table)
 
@@ -60,10 +60,12 @@ def units(dim, length, seed):
 @pytest.mark.parametrize("length", [256, 4096])
 @pytest.mark.parametrize("rows", [1, 20, 300])
 @pytest.mark.parametrize("dim", [32, 64, 96, 128, 256])
-def test_three_terms(dim, rows, length, reach):
-    """Few rows and many, in one share and joined from several."""
+@pytest.mark.parametrize("width", [0, 2 ** 23])
+def test_three_terms(width, dim, rows, length, reach):
+    """Few rows and many, in one share and joined from several; a table for many
+    tokens chooses the kernel for many rows where there are 300."""
     tt = torch()
-    cache, table = units(dim, length, dim + length)
+    cache, table = units(dim, length, dim + length, width)
     heads = 1 if rows > 1 else 16
     q = np.random.default_rng(rows).uniform(-reach, reach, size=(rows, heads, dim)).astype(np.float32)
     out, lse = mx.cache_attention(cache, dev(q), table, tt.tensor([length], dtype=tt.int32, device="cuda"), scale=1.0,
