@@ -27,13 +27,13 @@ struct CacheArgs {
     const int32_t* slots;
     int64_t tokens;
     int lanes;                // of a row: dim / 8
-    int per;                  // tokens of a workgroup's pass: 256 / lanes
+    int per;                  // tokens of a workgroup: 256 / lanes
 };
 
-// What a thread of a pass handles: eight elements of one token's row of one
-// head; four lanes hold a block of 32, the lanes after them the token's next
-// blocks, then the head's next token, so that a wave writes consecutive tokens
-// of a page: whole lines of codes, neighbouring scale bytes.
+// What a thread handles: eight elements of one token's row of one head; four
+// lanes hold a block of 32, the lanes after them the token's next blocks, then
+// the head's next token, so that a wave writes consecutive tokens of a page:
+// whole lines of codes, neighbouring scale bytes.
 struct Piece {
     int64_t token, slot;      // slot -1: outside the cache, or no such token
     int at;                   // first element
@@ -96,90 +96,74 @@ __device__ __forceinline__ void flip_signs(float* f, uint32_t mask, int q) {
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(__float_as_uint(f[i]) ^ (m >> i << 31));
 }
 
-// PASSES passes of a workgroup, keys and values: all of their loads are under
-// way before the first is used.  The quantizer's rule on 32 elements, four lanes a
-// block.  16384 tokens of 8 heads of 128, bf16, transformed: 22.7 us, 3.7 TB/s of
-// HBM traffic (read 66 MB, written 17); its grid comes and goes in a few microseconds
-// of that.
-template <bool BF16, int PASSES>
+// The quantizer's rule on 32 elements, four lanes a block; the loads of keys and
+// values are under way together.  16384 tokens of 8 heads of 128, bf16,
+// transformed: 19.0 us, 4.5 TB/s of HBM traffic (read 66 MB, written 18); its grid
+// comes and goes in a few microseconds of that.  (Two tokens a thread, with twice
+// the loads under way: 25.4 us in place of 24.5 over eight such batches in turn,
+// 4096 tokens 9.3 in place of 8.1.)
+template <bool BF16>
 __global__ __launch_bounds__(256) void cache_write_kernel(CacheArgs a) {
     const int head = blockIdx.y, q = threadIdx.x & 3;
-    float f[PASSES][2][8];
-    int64_t slot[PASSES];
+    const Piece p(a, (int64_t)blockIdx.x * a.per);
+    if (p.slot < 0) return;                                // (the four lanes of a block together)
+    float f[2][8];
 #pragma unroll
-    for (int u = 0; u < PASSES; ++u) {
-        const Piece p(a, ((int64_t)blockIdx.x * PASSES + u) * a.per);
-        slot[u] = p.slot;
-        if (p.slot < 0) continue;                          // (the four lanes of a block together)
+    for (int which = 0; which < 2; ++which) load8<BF16>(a.rows.p[which], p.row(a, which, head), f[which]);
+    const int64_t codes_at = a.cache.codes_at(p.page(a), head, p.offset(a)) + (p.at >> 1);
+    const int64_t scale_at =
+        a.cache.scales_at(p.page(a), head, p.offset(a)) + ((int64_t)(p.at >> 5) << a.cache.page_log2);
 #pragma unroll
-        for (int which = 0; which < 2; ++which) load8<BF16>(a.rows.p[which], p.row(a, which, head), f[u][which]);
-    }
-#pragma unroll
-    for (int u = 0; u < PASSES; ++u) {
-        if (slot[u] < 0) continue;
-        const int at = ((int)threadIdx.x - (int)threadIdx.x / a.lanes * a.lanes) * 8;
-        const int64_t page = slot[u] >> a.cache.page_log2;
-        const int offset = (int)slot[u] & ((1 << a.cache.page_log2) - 1);
-        const int64_t codes_at = a.cache.codes_at(page, head, offset) + (at >> 1);
-        const int64_t scale_at = a.cache.scales_at(page, head, offset) + ((int64_t)(at >> 5) << a.cache.page_log2);
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            float* v = f[u][which];
-            if (a.cache.rht) {
-                flip_signs(v, a.cache.mask, q);
-                rht32_quad(v, q);
-            }
-            uint32_t most = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-            const uint32_t byte = scale_byte_from_amax_bits(quad_max_u(most));
-            uint32_t codes = cvt8_rne(v, scale_operand(byte));
-            if (byte == 0xFFu) codes = 0;                  // non-finite block: codes are 0
-            *(uint32_t*)(a.cache.codes[which] + codes_at) = codes;
-            if (q == 0) a.cache.scales[which][scale_at] = (uint8_t)byte;
+    for (int which = 0; which < 2; ++which) {
+        float* v = f[which];
+        if (a.cache.rht) {
+            flip_signs(v, a.cache.mask, q);
+            rht32_quad(v, q);
         }
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        const uint32_t byte = scale_byte_from_amax_bits(quad_max_u(most));
+        uint32_t codes = cvt8_rne(v, scale_operand(byte));
+        if (byte == 0xFFu) codes = 0;                      // non-finite block: codes are 0
+        *(uint32_t*)(a.cache.codes[which] + codes_at) = codes;
+        if (q == 0) a.cache.scales[which][scale_at] = (uint8_t)byte;
     }
 }
 
-// The same way back (the same tokens: 21.9 us, 3.9 TB/s).
-template <bool BF16, int PASSES>
+// The same way back (the same tokens: 22.9 us, 3.8 TB/s).
+template <bool BF16>
 __global__ __launch_bounds__(256) void cache_read_kernel(CacheArgs a) {
     const int head = blockIdx.y, q = threadIdx.x & 3;
-    uint32_t codes[PASSES][2], byte[PASSES][2];
-#pragma unroll
-    for (int u = 0; u < PASSES; ++u) {
-        const Piece p(a, ((int64_t)blockIdx.x * PASSES + u) * a.per);
-        if (p.slot < 0) continue;
+    const Piece p(a, (int64_t)blockIdx.x * a.per);
+    if (!p.live) return;
+    uint32_t codes[2] = {0, 0}, byte[2] = {0, 0};
+    if (p.slot >= 0) {
         const int64_t codes_at = a.cache.codes_at(p.page(a), head, p.offset(a)) + (p.at >> 1);
         const int64_t scale_at =
             a.cache.scales_at(p.page(a), head, p.offset(a)) + ((int64_t)(p.at >> 5) << a.cache.page_log2);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            codes[u][which] = *(const uint32_t*)(a.cache.codes[which] + codes_at);
-            byte[u][which] = a.cache.scales[which][scale_at];
+            codes[which] = *(const uint32_t*)(a.cache.codes[which] + codes_at);
+            byte[which] = a.cache.scales[which][scale_at];
         }
     }
 #pragma unroll
-    for (int u = 0; u < PASSES; ++u) {
-        const Piece p(a, ((int64_t)blockIdx.x * PASSES + u) * a.per);
-        if (!p.live) continue;
+    for (int which = 0; which < 2; ++which) {
+        if (!a.rows.p[which]) continue;
+        float f[8] = {};
+        if (p.slot >= 0) {
+            decode8(codes[which], scale_operand(byte[which]), f);
+            if (byte[which] == 0xFFu) {
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            if (!a.rows.p[which]) continue;
-            float f[8] = {};
-            if (p.slot >= 0) {
-                decode8(codes[u][which], scale_operand(byte[u][which]), f);
-                if (byte[u][which] == 0xFFu) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(0x7FC00000u);
-                }
-                if (a.cache.rht) {
-                    rht32_quad(f, q);
-                    flip_signs(f, a.cache.mask, q);
-                }
+                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(0x7FC00000u);
             }
-            store8<BF16>(a.rows.p[which], p.row(a, which, head), f);
+            if (a.cache.rht) {
+                rht32_quad(f, q);
+                flip_signs(f, a.cache.mask, q);
+            }
         }
+        store8<BF16>(a.rows.p[which], p.row(a, which, head), f);
     }
 }
 
@@ -198,11 +182,6 @@ CacheArgs cache_args(const CacheView& c, void* k, int64_t k_ld, int64_t k_head_l
                      slots, tokens, c.dim / 8, 256 / (c.dim / 8)};
 }
 
-// Passes of a workgroup: two where that leaves the GPU full.
-// One pass where that is few workgroups, for a short call has too few of them for the chip;
-// two where there are many, each of which then has twice the loads under way.
-int passes(const CacheArgs& a) { return ceil_div(a.tokens, a.per) * a.cache.heads > 4096 ? 2 : 1; }
-
 }  // namespace
 
 extern "C" {
@@ -220,17 +199,11 @@ mx_status mx_cache_write(const mx_cache* cache, const void* k, int64_t k_ld, int
     if (!aligned_to(k, type_bytes(t)) || !aligned_to(v, type_bytes(t)) || !aligned_to(slots, 4)) return MX_ERR_ALIGN;
     const CacheArgs a = cache_args(c, const_cast<void*>(k), k_ld, k_head_ld, const_cast<void*>(v), v_ld, v_head_ld,
                                    tokens, slots);
-    const int n = passes(a);
-    const dim3 grid((uint32_t)ceil_div(tokens, (int64_t)n * a.per), c.heads);
+    const dim3 grid((uint32_t)ceil_div(tokens, a.per), c.heads);
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (t == MX_BF16) {
-        if (n == 2) hipLaunchKernelGGL((cache_write_kernel<true, 2>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((cache_write_kernel<true, 1>), grid, dim3(256), 0, s, a);
-    } else {
-        if (n == 2) hipLaunchKernelGGL((cache_write_kernel<false, 2>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((cache_write_kernel<false, 1>), grid, dim3(256), 0, s, a);
-    }
+    if (t == MX_BF16) hipLaunchKernelGGL(cache_write_kernel<true>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(cache_write_kernel<false>, grid, dim3(256), 0, s, a);
     return launch_status();
 }
 
@@ -245,17 +218,11 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
     if (!slots) return MX_ERR_NULL;
     if (!aligned_to(k, type_bytes(t)) || !aligned_to(v, type_bytes(t)) || !aligned_to(slots, 4)) return MX_ERR_ALIGN;
     const CacheArgs a = cache_args(c, k, k_ld, k_head_ld, v, v_ld, v_head_ld, tokens, slots);
-    const int n = passes(a);
-    const dim3 grid((uint32_t)ceil_div(tokens, (int64_t)n * a.per), c.heads);
+    const dim3 grid((uint32_t)ceil_div(tokens, a.per), c.heads);
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    if (t == MX_BF16) {
-        if (n == 2) hipLaunchKernelGGL((cache_read_kernel<true, 2>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((cache_read_kernel<true, 1>), grid, dim3(256), 0, s, a);
-    } else {
-        if (n == 2) hipLaunchKernelGGL((cache_read_kernel<false, 2>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((cache_read_kernel<false, 1>), grid, dim3(256), 0, s, a);
-    }
+    if (t == MX_BF16) hipLaunchKernelGGL(cache_read_kernel<true>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(cache_read_kernel<false>, grid, dim3(256), 0, s, a);
     return launch_status();
 }
 

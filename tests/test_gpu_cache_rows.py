@@ -13,7 +13,7 @@ from test_gpu_cache_limits import BYTES, fill, same
 
 pytestmark = pytest.mark.gpu
 
-HEADS = [(32, "bf16", False), (64, "bf16", True), (64, "f32", False), (96, "bf16", False), (96, "f32", True), (128, "bf16", False),
+HEADS = [(32, "bf16", False), (32, "bf16", True), (32, "f32", True), (96, "bf16", True), (64, "bf16", True), (64, "f32", False), (96, "bf16", False), (96, "f32", True), (128, "bf16", False),
          (128, "bf16", True), (128, "f32", False), (160, "bf16", True), (192, "f32", True), (224, "bf16", False),
          (256, "bf16", False), (256, "bf16", True), (256, "f32", False)]
 IDS = ["%d-%s-%s" % h for h in HEADS]
