@@ -7,8 +7,9 @@ weighted combine, all their gradients, and clipping by the global norm.
 
 The layer learns to reproduce a fixed random mixture of experts of the same
 shape from synthetic tokens; the loss of every step is printed.  With --balance
-C times the router's balance loss is added to it.  Sizes are multiples of 32.  The activation between the two expert linears (SiLU-gated)
-and the router's small products are plain torch.
+C times the router's balance loss is added to it.  Sizes are multiples of 32.
+The activation between the two expert linears (SiLU-gated) and the router's
+small products are plain torch.
 """
 import argparse
 import os

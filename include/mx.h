@@ -647,9 +647,11 @@ mx_status mx_cache_read(const mx_cache* cache, void* k, int64_t k_ld, int64_t k_
  * Scores, the softmax's statistics and sums are fp32.  bf16 queries enter the
  * products as they are; transformed, as a sum of two bf16 (2^-17 relative); fp32
  * ones as a sum of three.  exp(..) enters the product with v as bf16, for fp32
- * outputs as a sum of three.  Every sum has a fixed order, given the lengths.
+ * outputs as a sum of three: a caller who wants more than bf16 rows keep passes
+ * fp32 ones.  Every sum has a fixed order, given the lengths.
  * max_queries: the most rows that a sequence has, if the caller knows it (it
- * only selects the kernel); 0: unknown.
+ * only selects the kernel); 0: unknown, the kernel is that for one sequence with
+ * all rows (64 requests of up to 16384 tokens, 5 rows each: 329 us, 189 with 5).
  * workspace: mx_cache_attention_workspace(...) bytes, 16-byte aligned, its
  * contents irrelevant before and after; calls that may run at the same time
  * need one each.

@@ -46,8 +46,9 @@ constexpr int WAVES = 4;              // of a workgroup, sharing a tile's keys
 constexpr int MIN_UNITS = WAVES;      // of a workgroup's share, at least, where segments are cut
 constexpr int WHOLE_UNITS = 16;       // of a segment that is not cut
 // The exponentials' reference is kept until a row's largest score has outgrown it
-// by 2^GROWTH: any reference serves, as long as nothing overflows (a prompt
-// of 2 x 4096 queries: 568 us; 587 where the sums are scaled for each new maximum)
+// by 2^GROWTH: any reference serves, as long as nothing overflows (two prompts, 4096
+// queries behind 4096 tokens and 517 behind 1685, 32 heads of 128: 568 us; 587 where
+// the sums are scaled for each new maximum)
 constexpr float GROWTH = 8.0f;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -447,12 +448,15 @@ __device__ __forceinline__ float scale_of(uint32_t word, int byte) {       // by
 // Keys of a wave's 64: 32 j + 8 g + 4 t + i is row 4 g + i of score product
 // (j, t).  Lane l: column l & 15, group g = l >> 4.
 // NB: blocks of 32 that a row is padded to (2, 4, 8); NT: products of 16 rows.
-// QT: terms of q, PT: terms of p, in bf16: one each for bf16 rows (p's half step
-// of 2^-9 is that of the output), two of q where it was transformed (then it is
-// no bf16 any more), three for fp32 rows (with two, an output's error is 3.3e-6 of
-// its norm, with three 3e-7).
-// Bound by HBM: 64 requests of up to 16384 tokens, 8 heads of 128, 131 us (4.5
-// TB/s); one of 262144 tokens 53 us (5.5).  Keys and values go from memory to
+// QT: terms of q, PT: terms of p, in bf16: one each for bf16 rows, two of q where
+// it was transformed (then it is no bf16 any more), three for fp32 rows (with two,
+// an output's error is 3.3e-6 of its norm, with three 3e-7).  p's half step of 2^-8
+// is that of a bf16 output, whose error against 64 bits it makes 2.1e-3 to 2.3e-3
+// of the norm, 1.7e-3 of it the output's own rounding.  Two terms of p leave that
+// alone, for 3 to 5% of the time with one query a request, 17% with five, 24% of a
+// prompt's; who wants them has them, and more, with fp32 queries.
+// Bound by HBM: 64 requests of up to 16384 tokens, 8 heads of 128, 139 us (4.5
+// TB/s); one of 262144 tokens 53 us (5.6).  Keys and values go from memory to
 // registers to the products, no byte through LDS, and a step's loads are sent
 // for during the step before.
 // ---------------------------------------------------------------------------
@@ -967,9 +971,10 @@ __global__ __launch_bounds__(WAVES * 64, NT == 1 && NB < 8 ? 3 : 2) void attenti
 // into LDS lane by lane as the products read them (no bank conflicts).  Two
 // buffers; the next unit's is filled while this one's is read.  Products as in
 // attention_kernel.  Bound by the vector instructions (exponentials, sums,
-// widening) beside the products: 2 x 4096 queries behind 4096 tokens, 32 heads of
-// 128, 530 us and 20 for the join, 780 TFLOP/s; 2 x 2048 behind 2048, 32 heads of
-// 256, 543 us, 760 TFLOP/s (1125 us with 32 rows a wave, whose registers spill).
+// widening) beside the products: two prompts, 4096 queries behind 4096 tokens and
+// 517 behind 1685, 32 heads of 128, 533 us and 21 for the join, 774 TFLOP/s; two of
+// 4096 behind 4096, 976 us, 845 TFLOP/s; two of 2048 behind 2048, 32 heads of 256,
+// 543 us, 760 TFLOP/s (1125 us with 32 rows a wave, whose registers spill).
 //
 // (K's codes could enter a block-scaled product as they are, with q as a sum of
 // e4m3 terms.  Within 16 elements that product aligns its terms to the largest
@@ -1180,8 +1185,8 @@ __global__ __launch_bounds__(rows_waves(NB, QT) * 64, rows_waves(NB, QT) == 8 ? 
             __builtin_amdgcn_sched_barrier(0);
             if (key0 <= any_to && key0 + UNIT - 1 >= any_from) {
                 const bool whole = key0 + UNIT - 1 <= all_to && key0 >= all_from && !__any(pages < 0);
-                // (operands are read AHEAD steps before their products, for a read takes as long as several: two times 4096
-                // queries behind 4096 tokens, 32 heads of 128, take 650 us in place of 702)
+                // (operands are read AHEAD steps before their products, for a read takes as long as several: the two
+                // prompts above took 650 us in place of 702)
                 constexpr int AHEAD = 2;
                 bf16x8 ring[AHEAD + 1];
                 f32x4 s[NT][4];

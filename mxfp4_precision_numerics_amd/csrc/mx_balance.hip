@@ -70,7 +70,8 @@ __device__ __forceinline__ void row_scores(float* v, bool softmax, float* rest) 
 // L lanes share a row, as in the router.  Sums per expert stay in the registers of
 // the lanes that hold the expert, so a token costs no atomics; few, large
 // workgroups leave few rows to be added up.  65536 x 256 in fp32: 19.6 us (3.6
-// TB/s; bound by the exponentials), 16384 x 32 in bf16 4.9 us.
+// TB/s); the vector instructions, 27 an element, two of them exponential and
+// reciprocal, take three quarters of the issue slots.  16384 x 32 in bf16 4.7 us.
 template <bool BF16, int L, int C>
 __global__ __launch_bounds__(THREADS) void balance_kernel(BalanceArgs a) {
     constexpr int N = 4 * C, ROWS = THREADS / L, E = 4 * L * C;
@@ -211,7 +212,7 @@ typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 // dl = factor * s (slope - <slope, s>), for sigmoid scores times 1 - sigmoid(l), and
-// `add` more.  One pass; 65536 x 256 in fp32 with `add` 32.6 us, 6.2 TB/s: HBM.
+// `add` more.  One pass; 65536 x 256 in fp32 with `add` 31.1 us, 6.5 TB/s: HBM.
 template <bool BF16, int L, int C>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
     constexpr int N = 4 * C, ROWS = 256 / L;

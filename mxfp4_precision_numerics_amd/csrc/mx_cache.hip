@@ -99,9 +99,9 @@ __device__ __forceinline__ void flip_signs(float* f, uint32_t mask, int q) {
 // The quantizer's rule on 32 elements, four lanes a block; the loads of keys and
 // values are under way together.  16384 tokens of 8 heads of 128, bf16,
 // transformed: 19.0 us, 4.5 TB/s of HBM traffic (read 66 MB, written 18); its grid
-// comes and goes in a few microseconds of that.  (Two tokens a thread, with twice
-// the loads under way: 25.4 us in place of 24.5 over eight such batches in turn,
-// 4096 tokens 9.3 in place of 8.1.)
+// comes and goes in a few microseconds of that.  (Eight such batches in turn: 22.2 us each,
+// 25 with two tokens a thread, whose loads are under way together; 4096 tokens 7.8
+// and 9.2.)
 template <bool BF16>
 __global__ __launch_bounds__(256) void cache_write_kernel(CacheArgs a) {
     const int head = blockIdx.y, q = threadIdx.x & 3;

@@ -1000,7 +1000,9 @@ def cache_attention(cache, q, page_table, lengths, scale=None, q_offsets=None, m
     included.  q_offsets int32 [seqs + 1]: the rows of each sequence; None: one
     each.  scale: 1 / sqrt(head_dim) by default.  causal, window, sinks (fp32
     [q_heads]) as in mx_cache_attention.  max_queries: the most rows of a
-    sequence, if known.  workspace: uint8, at least
+    sequence, which a batch of short ones should pass (without it the kernel
+    is chosen as if one sequence had all rows).  fp32 queries are computed and
+    returned to fp32 precision.  workspace: uint8, at least
     mx_cache_attention_workspace bytes, or None to allocate it."""
     torch = _torch()
     q_ld, q_head = _heads(q, "q")
