@@ -10,6 +10,7 @@
 #include "mx_device.h"
 #include "mx_host.h"
 #include "mx_line.h"
+#include "mx_rows.h"
 
 namespace {
 
@@ -411,8 +412,6 @@ __device__ __forceinline__ float across(float v, Op op) {
     r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return op(__uint_as_float(r.x), __uint_as_float(r.y));
 }
-struct MaxF { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
-struct AddF { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
 
 // Eight codes and their scale as bf16, exactly (E2M1 times a power of two).
 __device__ __forceinline__ void widen8(uint32_t w, float scale, uint32_t* u) {

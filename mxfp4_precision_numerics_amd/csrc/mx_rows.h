@@ -1,5 +1,5 @@
-// mx_rows.h -- rows of router logits shared by a few lanes: loads, reductions,
-// softmax statistics (gfx950).
+// mx_rows.h -- rows of router logits shared by a few lanes: loads, reductions
+// (their operations are the attention's too), softmax statistics (gfx950).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <math.h>
