@@ -578,7 +578,8 @@ mx_status mx_grad_clip(const void* const* grads, const mx_dtype* types, const in
  *   use_rht: what is held is the RHT (sign_mask) of the keys and values, which
  *     spreads large channels over their block before they are rounded.  The
  *     transform is orthogonal: queries transformed alike give the same scores,
- *     and an output is transformed back once.
+ *     and an output is transformed back once.  Its sums are fp32, there and
+ *     back: a block whose magnitudes add up past fp32's range is not finite.
  * head_dim: a multiple of 32 up to 256; page_size: a power of two from 16 to
  * 4096; heads <= 1024; pages * page_size < 2^31.  All four buffers 16-byte
  * aligned.  The struct is host memory and read during the call only. */
